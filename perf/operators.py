@@ -1,0 +1,483 @@
+"""Cases that measure the sequence mixers beside the SDM core: the short causal
+convolution, the selective state space scan and sliding-window attention with
+sinks, each for prompts, single tokens and training.
+
+With `own` false every operator is computed in its plain form (elementary
+torch operations in float32, rounded once at the end); with `own` true through
+the package's entry points.  Sizes follow the repository's 1.4B-style layer
+(8 sequences of 4096 tokens, width 2048; its dense counterpart has heads of
+d_qk = 64 and d_v = 128; its local layers a window of 128 and two query heads
+for each key head), beside generic ones.
+"""
+import math
+
+import torch
+
+own = False
+
+DTYPES = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+def listed():
+    return [
+        # -- short convolution over x, B and C of a layer of width 2048 (2048 + 2 * 64 channels)
+        # one decode token for each of 32 sequences: latency
+        dict(name="conv step bf16", op="conv", mode="step", dtype="bf16", B=32, T=1, C=2176, K=4, ragged=False),
+        # a batch of prompts
+        dict(name="conv prompt bf16", op="conv", mode="fwd", dtype="bf16", B=8, T=4096, C=2176, K=4, ragged=False),
+        # training on a padded float32 batch of odd sizes
+        dict(name="conv backward f32 odd", op="conv", mode="bwd", dtype="f32", B=5, T=1021, C=1090, K=3, ragged=True),
+        # -- selective scan
+        # one decode token for each of 32 sequences
+        dict(name="scan step bf16", op="scan", mode="step", dtype="bf16", B=32, T=1, H=16, P=128, N=64, G=1, ragged=False),
+        # a batch of prompts at the 1.4B-style width
+        dict(name="scan prompt bf16", op="scan", mode="fwd", dtype="bf16", B=8, T=4096, H=16, P=128, N=64, G=1, ragged=False),
+        # one long document: few chains, a long time axis
+        dict(name="scan long bf16", op="scan", mode="fwd", dtype="bf16", B=1, T=65536, H=16, P=64, N=128, G=1, ragged=False),
+        # a small padded float32 batch of odd sizes, two groups
+        dict(name="scan f32 odd", op="scan", mode="fwd", dtype="f32", B=5, T=777, H=6, P=50, N=20, G=2, ragged=True),
+        # a training step's backward at the 1.4B-style width
+        dict(name="scan backward bf16", op="scan", mode="bwd", dtype="bf16", B=8, T=4096, H=16, P=128, N=64, G=1, ragged=False),
+        # -- sliding-window attention with sinks
+        # one decode token for each of 32 sequences from the rolling cache
+        dict(name="window step bf16", op="window", mode="step", dtype="bf16", B=32, T=1, Hq=16, Hk=8, D=128, W=128, S=4, ragged=False),
+        # a batch of prompts
+        dict(name="window prompt bf16", op="window", mode="fwd", dtype="bf16", B=8, T=4096, Hq=16, Hk=8, D=128, W=128, S=4, ragged=False),
+        # a padded float32 batch of odd sizes with a wider window
+        dict(name="window f32 odd", op="window", mode="fwd", dtype="f32", B=3, T=1333, Hq=6, Hk=2, D=72, W=301, S=5, ragged=True),
+        # a training step's backward
+        dict(name="window backward bf16", op="window", mode="bwd", dtype="bf16", B=8, T=4096, Hq=16, Hk=8, D=128, W=128, S=4, ragged=False),
+    ]
+
+
+def _log(rng, lo, hi):
+    return min(hi, max(lo, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))))
+
+
+def draw(rng):
+    op = rng.choice(["conv", "scan", "window"])
+    mode = rng.choice(["fwd", "bwd", "step"])
+    c = dict(op=op, mode=mode, dtype=rng.choice(["bf16", "bf16", "f32"]), B=_log(rng, 1, 32),
+             T=1 if mode == "step" else _log(rng, 1, 16384), ragged=rng.random() < 0.3)
+    if op == "conv":
+        c.update(C=_log(rng, 16, 4352), K=rng.choice([2, 3, 4, 4, 5]))
+        most, each = 8 * 4096 * 2176, c["C"]
+    elif op == "scan":
+        G = rng.choice([1, 1, 2, 4])
+        c.update(H=G * rng.randint(1, 32 // G), P=rng.choice([32, 64, 128, _log(rng, 8, 128)]),
+                 N=rng.choice([16, 64, 128, _log(rng, 8, 128)]), G=G)
+        most, each = 8 * 4096 * 16 * 128, c["H"] * max(c["P"], c["N"])
+    else:
+        Hk, r = rng.randint(1, 16), rng.choice([1, 2, 2, 4, 8])
+        c.update(Hq=Hk * r, Hk=Hk, D=rng.choice([64, 128, 128, _log(rng, 16, 256)]), W=_log(rng, 1, 4096),
+                 S=rng.choice([0, 1, 4, rng.randint(0, 64)]))
+        most, each = 8 * 4096 * 16 * 132 * 128, c["Hq"] * (min(c["W"], c["T"] if mode != "step" else c["W"]) + c["S"]) * c["D"]
+    most //= 2 if c["dtype"] == "f32" else 1
+    if c["B"] * c["T"] * each > most:  # within the largest listed case's work
+        c["B"] = max(1, most // (c["T"] * each))
+        c["T"] = max(1, min(c["T"], most // (c["B"] * each)))
+    return c
+
+
+# ---------------------------------------------------------------- inputs
+
+def prepare(case, seed):
+    c, dt = case, DTYPES[case["dtype"]]
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+
+    def normal(*shape, scale=1.0, shift=0.0, dtype=dt):
+        return (torch.randn(shape, generator=g, device="cuda") * scale + shift).to(dtype)
+
+    f32 = torch.float32
+    B, T = c["B"], c["T"]
+    s = dict(case=c, lengths=None)
+    if c["ragged"]:  # a padded batch: one full row, the others anywhere from empty to full
+        n = torch.randint(0, T + 1, (B,), generator=g, device="cuda", dtype=torch.int32)
+        n[0] = T
+        s["lengths"] = n
+    if c["op"] == "conv":
+        C, K = c["C"], c["K"]
+        s.update(x=normal(B, T, C), weight=normal(C, K, scale=K ** -0.5, dtype=f32), bias=normal(C, scale=0.1, dtype=f32))
+        if c["mode"] == "step":
+            s["state"] = normal(B, K - 1, C)
+        if c["mode"] == "bwd":
+            s["dy"] = normal(B, T, C)
+    elif c["op"] == "scan":
+        H, P, N, G = c["H"], c["P"], c["N"], c["G"]
+        # x, B and C are slices of the convolution's output, as in a layer
+        xbc = normal(B, T, H * P + 2 * G * N)
+        s.update(x=xbc[..., :H * P].unflatten(-1, (H, P)), Bm=xbc[..., H * P:H * P + G * N].unflatten(-1, (G, N)),
+                 Cm=xbc[..., H * P + G * N:].unflatten(-1, (G, N)), dt=normal(B, T, H),
+                 A=-(1.0 + 15.0 * torch.rand(H, generator=g, device="cuda")), D=normal(H, dtype=f32),
+                 dt_bias=normal(H, scale=0.1, shift=-4.0, dtype=f32))
+        if c["mode"] == "step":
+            s["state"] = normal(B, H, P, N, scale=0.1, dtype=f32)
+        if c["mode"] == "bwd":
+            s["dy"] = normal(B, T, H, P)
+    else:
+        Hq, Hk, D = c["Hq"], c["Hk"], c["D"]
+        # q, k and v are slices of one projection's output, as in a layer
+        qkv = normal(B, T, (Hq + 2 * Hk) * D).unflatten(-1, (Hq + 2 * Hk, D))
+        s.update(q=qkv[:, :, :Hq], k=qkv[:, :, Hq:Hq + Hk], v=qkv[:, :, Hq + Hk:])
+        if c["mode"] == "step":
+            R = c["S"] + c["W"]
+            s.update(ck=normal(B, R, Hk, D), cv=normal(B, R, Hk, D))
+            # streams of every age, from their first token to far past the window
+            s["pos"] = torch.randint(0, 4 * R + 1, (B,), generator=g, device="cuda", dtype=torch.int64)
+        if c["mode"] == "bwd":
+            o, lse = _window(s["q"], s["k"], s["v"], s["lengths"], c["W"], c["S"])
+            s.update(o=o.to(dt), lse=lse, do=normal(B, T, Hq, D))
+    return s
+
+
+def run(state):
+    return (_run_own if own else _run_plain)(state)
+
+
+# ---------------------------------------------------------------- the package's calls
+
+def _run_own(s):
+    import sparse_memory_linear_select_amd as sdm
+
+    c, n = s["case"], s["lengths"]
+    step = c["mode"] == "step"
+    if c["op"] == "conv":
+        conv = sdm.CausalConv(s["weight"], s["bias"], silu=True)
+        if c["mode"] == "bwd":
+            g = conv.backward(s["x"], s["dy"], lengths=n)
+            return dict(dx=g["dx"], dweight=g["dweight"], dbias=g["dbias"])
+        y, state = conv.forward(s["x"], state=s.get("state"), cont=step, lengths=n)
+        return dict(y=y, state=state)
+    if c["op"] == "scan":
+        scan = sdm.SelectiveScan(s["A"], D=s["D"], dt_bias=s["dt_bias"], softplus=True)
+        if c["mode"] == "bwd":
+            g = scan.backward(s["x"], s["dt"], s["Bm"], s["Cm"], s["dy"], lengths=n)
+            return {k: g[k] for k in ("dx", "ddt", "dB", "dC", "dA", "dD", "ddt_bias")}
+        y, state = scan.forward(s["x"], s["dt"], s["Bm"], s["Cm"], state=s.get("state"), cont=step, lengths=n)
+        return dict(y=y, state=state)
+    att = sdm.WindowAttention(c["Hq"], c["Hk"], c["D"], window=c["W"], sinks=c["S"])
+    if c["mode"] == "bwd":
+        g = att.backward(s["q"], s["k"], s["v"], s["o"], s["lse"], s["do"], lengths=n)
+        return {k: g[k] for k in ("dq", "dk", "dv")}
+    if step:
+        o, lse = att.forward(s["q"], s["k"], s["v"], cache=(s["ck"], s["cv"]), pos=s["pos"], cont=True, lengths=n)
+        return dict(o=o, lse=lse, ck=s["ck"], cv=s["cv"])
+    o, lse = att.forward(s["q"], s["k"], s["v"], lengths=n)
+    return dict(o=o, lse=lse)
+
+
+# ---------------------------------------------------------------- the plain forms
+
+def _valid(lengths, B, T, device):
+    """[B, T]: which rows hold tokens."""
+    if lengths is None:
+        return torch.ones(B, T, dtype=torch.bool, device=device)
+    return torch.arange(T, device=device)[None] < lengths[:, None]
+
+
+def _conv(x, weight, bias, state, lengths):
+    B, T, C = x.shape
+    K = weight.shape[1]
+    xe = torch.cat([x.new_zeros(B, K - 1, C) if state is None else state, x], 1)
+    z = (xe.unfold(1, K, 1) * weight).sum(-1) + bias
+    y = torch.where(_valid(lengths, B, T, x.device)[..., None], z * torch.sigmoid(z), 0)
+    n = torch.full((B,), T, device=x.device) if lengths is None else lengths
+    rows = n.long()[:, None] + torch.arange(K - 1, device=x.device)
+    return y, xe.gather(1, rows[..., None].expand(-1, -1, C))
+
+
+def _scan(x, dt, Bm, Cm, A, D, dt_bias, state, lengths):
+    """In chunks of about sqrt(T) tokens: products within a chunk, and of the
+    chunks' states with the decays between chunks."""
+    B, T, H, P = x.shape
+    G, N = Bm.shape[2:]
+    Q = 1 << max(4, math.ceil(math.log2(max(T, 2)) / 2))
+    nc = -(-T // Q)
+    z = dt + dt_bias
+    delta = torch.clamp(z, min=0) + torch.log1p(torch.exp(-z.abs()))
+    delta = torch.where(_valid(lengths, B, T, x.device)[..., None], delta, 0)
+
+    def chunks(t, heads):  # [B, T, heads, n] -> [B, H, chunk, Q, n]
+        t = torch.nn.functional.pad(t, (0, 0, 0, 0, 0, nc * Q - T))
+        t = t.reshape(B, nc, Q, heads, t.shape[-1]).permute(0, 3, 1, 2, 4)
+        return t.repeat_interleave(H // heads, 1)
+
+    d = chunks(delta[..., None], H)[..., 0]                       # [B, H, nc, Q]
+    cum = torch.cumsum(d.double() * A.double()[:, None, None], -1)
+    xc, bc, cc = chunks(x, H), chunks(Bm, G), chunks(Cm, G)
+    low = torch.ones(Q, Q, dtype=torch.bool, device=x.device).tril()
+    gap = torch.where(low, cum[..., :, None] - cum[..., None, :], -math.inf)
+    inside = torch.matmul(cc, bc.transpose(-1, -2)) * torch.exp(gap.float()) * d[..., None, :]
+    y = torch.matmul(inside, xc)
+    left = torch.exp((cum[..., -1:] - cum).float()) * d
+    own_part = torch.matmul((xc * left[..., None]).transpose(-1, -2), bc)  # [B, H, nc, P, N]
+    first = x.new_zeros(B, H, 1, P, N) if state is None else state[:, :, None]
+    parts = torch.cat([first, own_part], 2)                       # entry c + 1: what chunk c adds
+    total = torch.nn.functional.pad(torch.cumsum(cum[..., -1], -1), (1, 0))    # [B, H, nc + 1]
+    low = torch.ones(nc + 1, nc + 1, dtype=torch.bool, device=x.device).tril()
+    gap = torch.where(low, total[..., :, None] - total[..., None, :], -math.inf)
+    starts = torch.matmul(torch.exp(gap.float()), parts.flatten(-2)).unflatten(-1, (P, N))
+    y = y + torch.matmul(cc, starts[:, :, :nc].transpose(-1, -2)) * torch.exp(cum.float())[..., None]
+    y = y + D[:, None, None, None] * xc
+    y = y.permute(0, 2, 3, 1, 4).reshape(B, nc * Q, H, P)[:, :T]
+    y = torch.where(_valid(lengths, B, T, x.device)[..., None, None], y, 0)
+    return y, starts[:, :, nc]
+
+
+def _attend(q, keys, vals, seen):
+    """q [..., n, D], keys and vals [..., m, D], seen [..., n, m] -> o, lse in float32."""
+    score = torch.matmul(q, keys.transpose(-1, -2)) * q.shape[-1] ** -0.5
+    score = torch.where(seen, score, -math.inf)
+    top = score.amax(-1, keepdim=True)
+    top = torch.where(top > -math.inf, top, 0)
+    p = torch.exp(score - top)
+    den = p.sum(-1, keepdim=True)
+    o = torch.matmul(p, vals) / torch.where(den > 0, den, 1)
+    return o, (torch.log(den) + top)[..., 0]
+
+
+def _window(q, k, v, lengths, W, S):
+    """Blocks of queries against the keys that their windows span, and the sinks.
+    A row behind its sequence's length gives zeros, and zero for its lse."""
+    B, T, Hq, D = q.shape
+    Hk = k.shape[2]
+    Q = min(T, max(16, W))
+    nb = -(-T // Q)
+    dev = q.device
+    qb = torch.nn.functional.pad(q.float(), (0, 0, 0, 0, 0, nb * Q - T)).reshape(B, nb, Q, Hk, Hq // Hk, D)
+    qb = qb.permute(0, 1, 3, 4, 2, 5)                              # [B, nb, Hk, r, Q, D]
+    i = torch.arange(nb * Q, device=dev).reshape(nb, Q)
+    j = i[:, :1] - (W - 1) + torch.arange(Q + W - 1, device=dev)   # [nb, Q + W - 1]
+    sink = torch.arange(min(S, T), device=dev).expand(nb, -1)
+    near = (j[:, None] >= 0) & (j[:, None] <= i[..., None]) & (j[:, None] > i[..., None] - W)
+    far = sink[:, None] <= i[..., None] - W
+    seen = torch.cat([far, near], -1)                              # [nb, Q, m]
+    j = torch.cat([sink, j.clamp(0, T - 1)], -1)
+    ok = _valid(lengths, B, T, dev)
+    okq = torch.nn.functional.pad(ok, (0, nb * Q - T)).reshape(B, nb, 1, 1, Q, 1)
+    kb = k.float()[:, j].permute(0, 1, 3, 2, 4)[:, :, :, None]      # [B, nb, Hk, 1, m, D]
+    vb = v.float()[:, j].permute(0, 1, 3, 2, 4)[:, :, :, None]
+    o, lse = _attend(qb, kb, vb, seen[None, :, None, None] & okq)
+    o = o.permute(0, 1, 4, 2, 3, 5).reshape(B, nb * Q, Hq, D)[:, :T]
+    lse = lse.permute(0, 1, 4, 2, 3).reshape(B, nb * Q, Hq)[:, :T]
+    return o, torch.where(ok[..., None], lse, 0)
+
+
+def _window_step(q, k, v, ck, cv, pos, lengths, S, W):
+    """One token for each sequence: its row into the rolling cache, then attention over the cache."""
+    B, R, Hk, D = ck.shape
+    on = _valid(lengths, B, 1, q.device)[:, 0]
+    slot = torch.where(pos < S, pos, S + (pos - S) % W)
+    at = torch.arange(B, device=q.device), slot
+    ck[at] = torch.where(on[:, None, None], k[:, 0], ck[at])
+    cv[at] = torch.where(on[:, None, None], v[:, 0], cv[at])
+    # the cache fills from its first row on: a row is in use once as many tokens have come
+    used = (torch.arange(R, device=q.device) <= pos[:, None]) & on[:, None]
+    qh = q[:, 0].float().reshape(B, Hk, -1, D)
+    o, lse = _attend(qh, ck.float().transpose(1, 2), cv.float().transpose(1, 2), used[:, None, None])
+    lse = torch.where(on[:, None], lse.reshape(B, -1), 0)
+    return o.reshape(B, 1, -1, D), lse[:, None]
+
+
+def _run_plain(s):
+    c, n = s["case"], s["lengths"]
+    dt = DTYPES[c["dtype"]]
+    bwd = c["mode"] == "bwd"
+
+    def leaf(name):
+        return s[name].float().detach().requires_grad_(bwd)
+
+    if c["op"] == "conv":
+        x, w, b = leaf("x"), leaf("weight"), leaf("bias")
+        old = s["state"].float() if "state" in s else None
+        with torch.set_grad_enabled(bwd):
+            y, state = _conv(x, w, b, old, n)
+        if bwd:
+            dx, dw, db = torch.autograd.grad(y, (x, w, b), s["dy"].float())
+            return dict(dx=dx.to(dt), dweight=dw, dbias=db)
+        if old is not None:
+            s["state"].copy_(state)
+        return dict(y=y.to(dt), state=state.to(dt))
+    if c["op"] == "scan":
+        names = ("x", "dt", "Bm", "Cm", "A", "D", "dt_bias")
+        args = [leaf(k) for k in names]
+        with torch.set_grad_enabled(bwd):
+            y, state = _scan(*args, s.get("state"), n)
+        if bwd:
+            g = torch.autograd.grad(y, args, s["dy"].float())
+            return dict(dx=g[0].to(dt), ddt=g[1].to(dt), dB=g[2].to(dt), dC=g[3].to(dt), dA=g[4], dD=g[5], ddt_bias=g[6])
+        if "state" in s:
+            s["state"].copy_(state)
+        return dict(y=y.to(dt), state=state)
+    if bwd:
+        q, k, v = leaf("q"), leaf("k"), leaf("v")
+        with torch.enable_grad():
+            o, _ = _window(q, k, v, n, c["W"], c["S"])
+        dq, dk, dv = torch.autograd.grad(o, (q, k, v), s["do"].float())
+        return dict(dq=dq.to(dt), dk=dk.to(dt), dv=dv.to(dt))
+    if c["mode"] == "step":
+        o, lse = _window_step(s["q"], s["k"], s["v"], s["ck"], s["cv"], s["pos"], n, c["S"], c["W"])
+        return dict(o=o.to(dt), lse=lse, ck=s["ck"], cv=s["cv"])
+    o, lse = _window(s["q"], s["k"], s["v"], n, c["W"], c["S"])
+    return dict(o=o.to(dt), lse=lse)
+
+
+# ---------------------------------------------------------------- what a pass cannot do without
+
+def work(case):
+    c = case
+    e = 4 if c["dtype"] == "f32" else 2
+    B, T, mode = c["B"], c["T"], c["mode"]
+    bwd = mode == "bwd"
+    step = mode == "step"
+    if c["op"] == "conv":
+        C, K = c["C"], c["K"]
+        el = B * T * C
+        state = B * (K - 1) * C * e * (0 if bwd else 2 if step else 1)
+        return dict(bytes=el * e * (3 if bwd else 2) + state + C * (K + 1) * 4 * (2 if bwd else 1), flops=el * (6 * K if bwd else 2 * K))
+    if c["op"] == "scan":
+        H, P, N, G = c["H"], c["P"], c["N"], c["G"]
+        once = B * T * (2 * H * P + H + 2 * G * N) * e
+        state = B * H * P * N * 4 * (0 if bwd else 2 if step else 1)
+        grads = B * T * (H * P + H + 2 * G * N) * e if bwd else 0
+        return dict(bytes=once + state + grads, flops=B * T * H * P * N * (14 if bwd else 5))
+    Hq, Hk, D, W, S = c["Hq"], c["Hk"], c["D"], c["W"], c["S"]
+    if step:
+        rows = B * (S + W)
+        return dict(bytes=(rows + 2 * B) * 2 * Hk * D * e + 2 * B * Hq * D * e, flops=4 * rows * Hq * D)
+    full = max(0, T - W)  # queries whose window is full
+    pairs = full * W + min(T, W) * (min(T, W) + 1) // 2 + sum(min(S, i + 1) for i in range(full))
+    io = B * T * (2 * Hq + 2 * Hk) * D * e + B * T * Hq * 4
+    return dict(bytes=2 * io if bwd else io, flops=B * Hq * pairs * D * (10 if bwd else 4))
+
+
+# ---------------------------------------------------------------- the definitions in 64 bits
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    return {"conv": _exact_conv, "scan": _exact_scan, "window": _exact_window}[case["op"]](s, case)
+
+
+def _on(s, t, B):
+    return torch.ones(B, dtype=torch.bool, device="cuda") if s["lengths"] is None else s["lengths"] > t
+
+
+def _exact_conv(s, c):
+    """Tap by tap over the whole sequence."""
+    B, T, C, K = c["B"], c["T"], c["C"], c["K"]
+    x, w = s["x"].double(), s["weight"].double()
+    xe = torch.zeros(B, T + K - 1, C, dtype=torch.float64, device="cuda")
+    xe[:, K - 1:] = x
+    if "state" in s:
+        xe[:, :K - 1] = s["state"].double()
+    z = s["bias"].double().expand(B, T, C).clone()
+    for k in range(K):
+        z += xe[:, k:k + T] * w[:, k]
+    on = torch.stack([_on(s, t, B) for t in range(T)], 1)[..., None].double()
+    sig = 1 / (1 + torch.exp(-z))
+    if c["mode"] != "bwd":
+        state = torch.stack([xe[b, n:n + K - 1] for b, n in enumerate([T] * B if s["lengths"] is None else s["lengths"].tolist())])
+        return dict(y=z * sig * on, state=state)
+    dz = s["dy"].double() * on * sig * (1 + z * (1 - sig))
+    dxe, dw = torch.zeros_like(xe), torch.zeros_like(w)
+    for k in range(K):
+        dxe[:, k:k + T] += dz * w[:, k]
+        dw[:, k] = (dz * xe[:, k:k + T]).sum((0, 1))
+    return dict(dx=dxe[:, K - 1:], dweight=dw, dbias=dz.sum((0, 1)))
+
+
+def _exact_scan(s, c):
+    """Token by token; the backward token by token in reverse from the kept states."""
+    B, T, H, P, N, G = (c[k] for k in ("B", "T", "H", "P", "N", "G"))
+    if B * H * P * N * T * (1 if c["mode"] == "bwd" else 0) * 8 > 60e9 or T > 70000:
+        return None
+    x, z = s["x"].double(), s["dt"].double() + s["dt_bias"].double()
+    Bh, Ch = (s[k].double().repeat_interleave(H // G, 2) for k in ("Bm", "Cm"))
+    A, D = s["A"].double(), s["D"].double()
+    delta = torch.logaddexp(z, torch.zeros_like(z))
+    a = torch.exp(delta * A)
+    S = s["state"].double() if "state" in s else torch.zeros(B, H, P, N, dtype=torch.float64, device="cuda")
+    y, kept = torch.zeros_like(x), []
+    for t in range(T):
+        on = _on(s, t, B)
+        if c["mode"] == "bwd":
+            kept.append(S)
+        new = a[:, t, :, None, None] * S + (delta[:, t, :, None] * x[:, t])[..., None] * Bh[:, t, :, None]
+        S = torch.where(on[:, None, None, None], new, S) if s["lengths"] is not None else new
+        y[:, t] = (torch.matmul(S, Ch[:, t, :, :, None])[..., 0] + D[:, None] * x[:, t]) * on[:, None, None]
+    if c["mode"] != "bwd":
+        return dict(y=y, state=S)
+    dx, ddelta, dB, dC = torch.zeros_like(x), torch.zeros_like(z), torch.zeros_like(Bh), torch.zeros_like(Ch)
+    dl = torch.zeros_like(z)
+    dy = s["dy"].double()
+    Gr = torch.zeros_like(S)
+    for t in reversed(range(T)):
+        on = _on(s, t, B).double()[:, None, None]
+        g = dy[:, t] * on
+        old = kept[t]
+        dx[:, t] = D[:, None] * g
+        now = a[:, t, :, None, None] * old + (delta[:, t, :, None] * x[:, t])[..., None] * Bh[:, t, :, None]
+        dC[:, t] = torch.matmul(g[..., None, :], now)[..., 0, :]
+        Gr = Gr + g[..., None] * Ch[:, t, :, None]
+        gb = torch.matmul(Gr, Bh[:, t, :, :, None])[..., 0]
+        dx[:, t] += delta[:, t, :, None] * gb * on
+        dB[:, t] = torch.matmul((delta[:, t, :, None] * x[:, t] * on)[..., None, :], Gr)[..., 0, :]
+        dl[:, t] = (Gr * old).sum((-1, -2)) * a[:, t] * on[..., 0]
+        ddelta[:, t] = ((x[:, t] * gb).sum(-1) + 0) * on[..., 0] + A * dl[:, t]
+        back = a[:, t, :, None, None] * Gr
+        Gr = torch.where(on[..., None] > 0, back, Gr) if s["lengths"] is not None else back
+    dz = ddelta / (1 + torch.exp(-z))
+    on = torch.stack([_on(s, t, B) for t in range(T)], 1)[..., None, None].double()
+    heads = lambda t: t.unflatten(2, (G, H // G)).sum(3)  # noqa: E731
+    return dict(dx=dx, ddt=dz, dB=heads(dB), dC=heads(dC), dA=(dl * delta).sum((0, 1)), dD=(dy * on * x).sum((0, 1, 3)), ddt_bias=dz.sum((0, 1)))
+
+
+def _exact_window(s, c):
+    """Sequence by sequence, in tiles of queries against all keys up to them."""
+    B, T, Hq, Hk, D, W, S = (c[k] for k in ("B", "T", "Hq", "Hk", "D", "W", "S"))
+    r, scale, dev = Hq // Hk, D ** -0.5, "cuda"
+    q, k, v = (s[n].double().transpose(1, 2) for n in ("q", "k", "v"))   # [B, heads, T, D]
+    n = [T] * B if s["lengths"] is None else s["lengths"].tolist()
+    if c["mode"] == "step":
+        ck, cv = s["ck"].double(), s["cv"].double()
+        o, lse = torch.zeros(B, 1, Hq, D, dtype=torch.float64, device=dev), torch.zeros(B, 1, Hq, dtype=torch.float64, device=dev)
+        for b, p in enumerate(s["pos"].tolist()):
+            if n[b] == 0:
+                continue
+            at = p if p < S else S + (p - S) % W
+            ck[b, at], cv[b, at] = k[b, :, 0], v[b, :, 0]
+            m = min(p + 1, S + W)
+            for h in range(Hq):
+                sc = ck[b, :m, h // r] @ q[b, h, 0] * scale
+                lse[b, 0, h] = torch.logsumexp(sc, 0)
+                o[b, 0, h] = torch.softmax(sc, 0) @ cv[b, :m, h // r]
+        return dict(o=o, lse=lse, ck=ck, cv=cv)
+    if B * Hq * T * min(T, S + W + 512) * D > 4e12:
+        return None
+    o, dq = torch.zeros_like(q), torch.zeros_like(q)
+    dk, dv = torch.zeros_like(k), torch.zeros_like(v)
+    lse = torch.zeros(B, Hq, T, dtype=torch.float64, device=dev)
+    for b in range(B):
+        for i0 in range(0, n[b], 512):
+            i = torch.arange(i0, min(n[b], i0 + 512), device=dev)
+            lo = max(0, i0 - W + 1)
+            j = torch.cat([torch.arange(min(S, lo), device=dev), torch.arange(lo, int(i[-1]) + 1, device=dev)])
+            gap = i[:, None] - j
+            see = (gap >= 0) & ((gap < W) | (j < S))
+            qs, ks, vs = q[b, :, i].unflatten(0, (Hk, r)), k[b, :, j][:, None], v[b, :, j][:, None]
+            sc = torch.matmul(qs, ks.transpose(-1, -2)) * scale
+            sc = sc.masked_fill(~see, -math.inf)
+            p = torch.softmax(sc, -1)
+            ot = torch.matmul(p, vs)
+            o[b, :, i], lse[b, :, i] = ot.flatten(0, 1), torch.logsumexp(sc, -1).flatten(0, 1)
+            if c["mode"] == "bwd":
+                do = s["do"][b, i].double().transpose(0, 1).unflatten(0, (Hk, r))
+                dp = torch.matmul(do, vs.transpose(-1, -2))
+                ds = p * (dp - (do * ot).sum(-1, keepdim=True)) * scale
+                dq[b, :, i] = torch.matmul(ds, ks).flatten(0, 1)
+                dk[b, :, j] += torch.matmul(ds.transpose(-1, -2), qs).sum(1)
+                dv[b, :, j] += torch.matmul(p.transpose(-1, -2), do).sum(1)
+    if c["mode"] == "bwd":
+        return dict(dq=dq.transpose(1, 2), dk=dk.transpose(1, 2), dv=dv.transpose(1, 2))
+    return dict(o=o.transpose(1, 2), lse=lse.transpose(1, 2))
