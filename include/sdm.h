@@ -335,6 +335,79 @@ sdm_status sdm_backward(sdm_handle h, int B, int64_t T, const void *kp, const vo
                         size_t ws_bytes, float *dkp, float *dqp, float *dv, float *dalpha,
                         float *dbeta, float *dMinit, float *dM0, void *stream);
 
+/*
+ * Sequence mixers beside the SDM core.  A hybrid stack puts sliding-window
+ * attention between its SDM layers [explainer "Sparse Delta Memory：通过稀疏性
+ * 扩展线性 RNN 的状态容量", §4.1]; a dense recurrence with a scalar decay per head
+ * and token, with a short convolution before it, is the layer that SDM takes
+ * the place of.  They share the conventions above (device pointers, stream,
+ * errors, all checks before the first HIP call, nothing allocated) with these
+ * additions:
+ *   - Types: `dtype` is the element type of every tensor not said to be
+ *     float32; outputs and gradients of such tensors have the same type.
+ *     Sums, decays, softmax statistics and recurrent states are float32;
+ *     each output is rounded once.  Products of bfloat16 tensors with
+ *     intermediate weights (softmax or decay weights) round those weights to
+ *     bfloat16 where the result is rounded to bfloat16 anyway.
+ *   - Strides: inputs given with strides (counted in elements) may be slices
+ *     of a larger tensor; their pointers need only element alignment (16-byte
+ *     rows are faster).  All other tensors are dense, 16-byte aligned.
+ *   - lengths: device [B] int32, or NULL.  Sequence b holds lengths[b] tokens
+ *     (clamped to [0, T]); the rows behind are not read, their outputs and
+ *     gradients are zeros, and the recurrent state or cache is the one after
+ *     lengths[b] tokens.  Rows that are read must be finite.
+ *   - Results are deterministic (fixed reduction orders, no atomics).
+ *   - Outputs must not alias inputs or each other, except the state and cache
+ *     buffers that a call documents as updated in place.
+ */
+
+/*
+ * Short causal depthwise convolution over the tokens, with an optional SiLU:
+ *   z_t = bias + sum_k weight[c][k] * xe[t + k],  xe = [K - 1 rows before, x]
+ *   y_t = z_t, or z_t / (1 + exp(-z_t)) with silu = 1.
+ * Limits: 2 <= K <= 8, 1 <= C; B * T * C < 2^40.
+ */
+typedef struct {
+    int B;
+    int64_t T;
+    int C, K;
+    int silu;                 /* 0 or 1 */
+    sdm_dtype dtype;          /* SDM_F32 or SDM_BF16 */
+    int64_t x_batch, x_token; /* strides of x; the channels are dense */
+} sdm_conv_desc;
+
+/*
+ *   x        device [B][T][C] (strided)
+ *   weight   device [C][K] float32;  bias  device [C] float32 or NULL
+ *   lengths  see above
+ *   flags    SDM_FLAG_CONTINUE: `state` holds the K - 1 rows before x
+ *            (otherwise they are zeros and its contents are ignored)
+ *   y        device [B][T][C]
+ *   state    device [B][K-1][C], updated in place: the last K - 1 rows.
+ * One launch, whatever T is: T = 1 with the flag is a decode step.
+ */
+sdm_status sdm_conv_forward(const sdm_conv_desc *d, const void *x, const float *weight,
+                            const float *bias, const int32_t *lengths, unsigned flags, void *y,
+                            void *state, void *stream);
+
+/*
+ * Gradients of the convolution (z is recomputed from x).
+ *   dy       device [B][T][C], dL/dy
+ *   state    device [B][K-1][C], the rows before x that the forward started
+ *            from, or NULL for zeros
+ *   dstateT  device [B][K-1][C], dL/d(final state), or NULL for zero
+ *   workspace  >= sdm_conv_backward_workspace_size bytes, 16-byte aligned
+ * Outputs: dx [B][T][C]; dweight [C][K], dbias [C] float32 (dbias NULL to
+ * skip); dstate [B][K-1][C], dL/d(state), or NULL to skip.
+ */
+sdm_status sdm_conv_backward_workspace_size(const sdm_conv_desc *d, size_t *bytes);
+
+sdm_status sdm_conv_backward(const sdm_conv_desc *d, const void *x, const float *weight,
+                             const float *bias, const int32_t *lengths, const void *dy,
+                             const void *state, const void *dstateT, void *workspace,
+                             size_t ws_bytes, void *dx, float *dweight, float *dbias,
+                             void *dstate, void *stream);
+
 /* Static description of a status code. */
 const char *sdm_status_string(sdm_status s);
 

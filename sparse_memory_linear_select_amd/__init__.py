@@ -20,7 +20,7 @@ import os
 import torch
 
 __all__ = ["SDM", "SDMError", "lib", "lib_path", "F32", "BF16", "FP8_E4M3", "AUTO", "SERIAL", "TIMEPAR",
-           "FLAG_CONTINUE", "EXPORTS", "NOALLOC_MAX_BYTES"]
+           "FLAG_CONTINUE", "EXPORTS", "NOALLOC_MAX_BYTES", "CausalConv"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libsdm.so")
@@ -37,6 +37,7 @@ EXPORTS = ("sdm_backward", "sdm_backward_workspace_size", "sdm_backward_workspac
            "sdm_create", "sdm_create_ex", "sdm_create_fp8",
            "sdm_destroy", "sdm_workspace_size", "sdm_select", "sdm_forward",
            "sdm_forward_noalloc", "sdm_prepare", "sdm_apply", "sdm_write_histogram",
+           "sdm_conv_forward", "sdm_conv_backward", "sdm_conv_backward_workspace_size",
            "sdm_status_string", "sdm_last_error")
 NOALLOC_MAX_BYTES = 64 << 20  # SDM_NOALLOC_MAX_BYTES: the static scratch of sdm_forward_noalloc
 
@@ -75,6 +76,9 @@ def lib():
         L.sdm_backward_workspace_size_ex.argtypes = [p, i, i64, i, i, ctypes.POINTER(sz)]
         L.sdm_backward.argtypes = [p, i, i64, p, p, p, p, p, i, p, p, p, p, sz, p, p, p, p, p,
                                    p, p, p]
+        L.sdm_conv_forward.argtypes = [p, p, p, p, p, ctypes.c_uint, p, p, p]
+        L.sdm_conv_backward_workspace_size.argtypes = [p, ctypes.POINTER(sz)]
+        L.sdm_conv_backward.argtypes = [p, p, p, p, p, p, p, p, p, sz, p, p, p, p, p]
         for f in EXPORTS[:-2]:
             getattr(L, f).restype = ctypes.c_int
         L.sdm_status_string.argtypes = [i]
@@ -373,3 +377,6 @@ class SDM:
                                  _ptr(beta), dt, variant, flags, _ptr(workspace),
                                  workspace.numel(), _ptr(y), _ptr(M), _stream(dev)))
         return y, M
+
+
+from .mixers import CausalConv  # noqa: E402  (uses the helpers above)

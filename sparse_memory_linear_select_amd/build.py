@@ -23,8 +23,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libsdm.so")
 
 SOURCES = ["select.hip", "init.hip", "plan.hip", "rw_serial.hip", "rw_timepar.hip", "decode.hip",
-           "backward.hip",
-           "sdm_api.cpp"]
+           "backward.hip", "causal_conv.hip",
+           "sdm_api.cpp", "mix_api.cpp"]
 
 HIPCC = os.environ.get("HIPCC", "hipcc")
 ARCH = "gfx950"

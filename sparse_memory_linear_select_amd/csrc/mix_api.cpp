@@ -1,0 +1,162 @@
+// C ABI of the sequence mixers: argument validation and launches.  Every
+// check happens before the first HIP call; see include/sdm.h for the contract.
+#include "mix_internal.h"
+
+namespace {
+
+using sdm::set_error;
+
+bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
+bool aligned_el(const void *p, sdm_dtype t) { return ((uintptr_t)p & (t == SDM_F32 ? 3u : 1u)) == 0; }
+
+sdm_status hip_fail(hipError_t e, const char *what)
+{
+    return set_error(SDM_ERR_HIP, "%s: %s (%s)", what, hipGetErrorName(e), hipGetErrorString(e));
+}
+
+// A dense tensor: required (null refused) or optional, 16-byte aligned.
+sdm_status check_dense(const void *p, const char *name, bool required = true)
+{
+    if (!p) return required ? set_error(SDM_ERR_ARG, "null %s", name) : SDM_OK;
+    if (!aligned16(p)) return set_error(SDM_ERR_ARG, "%s must be 16-byte aligned", name);
+    return SDM_OK;
+}
+
+// A strided input: element-aligned.
+sdm_status check_strided(const void *p, const char *name, sdm_dtype t)
+{
+    if (!p) return set_error(SDM_ERR_ARG, "null %s", name);
+    if (!aligned_el(p, t)) return set_error(SDM_ERR_ARG, "%s must be aligned to its elements", name);
+    return SDM_OK;
+}
+
+sdm_status check_lengths(const int32_t *p)
+{
+    if (p && ((uintptr_t)p & 3u)) return set_error(SDM_ERR_ARG, "lengths must be 4-byte aligned");
+    return SDM_OK;
+}
+
+sdm_status check_batch(int B, int64_t T, sdm_dtype dtype)
+{
+    if (B < 1) return set_error(SDM_ERR_ARG, "B must be >= 1 (got %d)", B);
+    if (T < 1) return set_error(SDM_ERR_ARG, "T must be >= 1 (got %lld)", (long long)T);
+    if (T >= (int64_t)1 << 31)
+        return set_error(SDM_ERR_UNSUPPORTED, "T must be < 2^31 (got %lld)", (long long)T);
+    if (dtype != SDM_F32 && dtype != SDM_BF16)
+        return set_error(SDM_ERR_ARG, "dtype must be SDM_F32 or SDM_BF16 (got %d)", (int)dtype);
+    return SDM_OK;
+}
+
+sdm_status check_workspace(const void *ws, size_t have, size_t need)
+{
+    if (need && !ws) return set_error(SDM_ERR_ARG, "null workspace");
+    if (!aligned16(ws)) return set_error(SDM_ERR_ARG, "workspace must be 16-byte aligned");
+    if (have < need)
+        return set_error(SDM_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", have, need);
+    return SDM_OK;
+}
+
+#define CHECK(expr)                          \
+    do {                                     \
+        const sdm_status st_ = (expr);       \
+        if (st_ != SDM_OK) return st_;       \
+    } while (0)
+
+// ------------------------------------------------------------- convolution
+
+sdm_status check_conv(const sdm_conv_desc *d)
+{
+    if (!d) return set_error(SDM_ERR_ARG, "null descriptor");
+    CHECK(check_batch(d->B, d->T, d->dtype));
+    if (d->C < 1 || d->K < 1)
+        return set_error(SDM_ERR_ARG, "C and K must be >= 1 (got %d %d)", d->C, d->K);
+    if (d->silu != 0 && d->silu != 1)
+        return set_error(SDM_ERR_ARG, "silu must be 0 or 1 (got %d)", d->silu);
+    if (d->x_batch < 0 || d->x_token < 0)
+        return set_error(SDM_ERR_ARG, "strides must be >= 0");
+    if (d->K < 2 || d->K > 8)
+        return set_error(SDM_ERR_UNSUPPORTED, "2 <= K <= 8 is supported (got %d)", d->K);
+    if ((double)d->B * (double)d->T * d->C >= 1099511627776.0)
+        return set_error(SDM_ERR_UNSUPPORTED, "B*T*C must be < 2^40");
+    // workgroups of the scalar form: one launch holds fewer than 2^31
+    if ((double)d->B * (double)((d->T + 63) / 64) * (double)((d->C + 63) / 64) >= 2147483648.0)
+        return set_error(SDM_ERR_UNSUPPORTED, "B * ceil(T/64) * ceil(C/64) must be < 2^31");
+    return SDM_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+sdm_status sdm_conv_forward(const sdm_conv_desc *d, const void *x, const float *weight,
+                            const float *bias, const int32_t *lengths, unsigned flags, void *y,
+                            void *state, void *stream)
+{
+    CHECK(check_conv(d));
+    if (flags & ~SDM_FLAG_CONTINUE) return set_error(SDM_ERR_ARG, "unknown flags 0x%x", flags);
+    CHECK(check_strided(x, "x", d->dtype));
+    CHECK(check_dense(weight, "weight"));
+    CHECK(check_dense(bias, "bias", false));
+    CHECK(check_lengths(lengths));
+    CHECK(check_dense(y, "y"));
+    CHECK(check_dense(state, "state"));
+    sdm::ConvArgs a = {};
+    a.d = *d;
+    a.x = x;
+    a.weight = weight;
+    a.bias = bias;
+    a.lengths = lengths;
+    a.cont = flags & SDM_FLAG_CONTINUE;
+    a.y = y;
+    a.state = state;
+    const hipError_t e = sdm::launch_conv_forward(a, (hipStream_t)stream);
+    return e == hipSuccess ? SDM_OK : hip_fail(e, "convolution launch");
+}
+
+sdm_status sdm_conv_backward_workspace_size(const sdm_conv_desc *d, size_t *bytes)
+{
+    if (!bytes) return set_error(SDM_ERR_ARG, "null bytes pointer");
+    *bytes = 0;
+    CHECK(check_conv(d));
+    *bytes = sdm::conv_backward_ws(*d);
+    return SDM_OK;
+}
+
+sdm_status sdm_conv_backward(const sdm_conv_desc *d, const void *x, const float *weight,
+                             const float *bias, const int32_t *lengths, const void *dy,
+                             const void *state, const void *dstateT, void *workspace,
+                             size_t ws_bytes, void *dx, float *dweight, float *dbias,
+                             void *dstate, void *stream)
+{
+    CHECK(check_conv(d));
+    CHECK(check_strided(x, "x", d->dtype));
+    CHECK(check_dense(weight, "weight"));
+    CHECK(check_dense(bias, "bias", false));
+    CHECK(check_lengths(lengths));
+    CHECK(check_dense(dy, "dy"));
+    CHECK(check_dense(state, "state", false));
+    CHECK(check_dense(dstateT, "dstateT", false));
+    CHECK(check_dense(dx, "dx"));
+    CHECK(check_dense(dweight, "dweight"));
+    CHECK(check_dense(dbias, "dbias", false));
+    CHECK(check_dense(dstate, "dstate", false));
+    CHECK(check_workspace(workspace, ws_bytes, sdm::conv_backward_ws(*d)));
+    sdm::ConvArgs a = {};
+    a.d = *d;
+    a.x = x;
+    a.dy = dy;
+    a.weight = weight;
+    a.bias = bias;
+    a.lengths = lengths;
+    a.state0 = state;
+    a.dstateT = dstateT;
+    a.dx = dx;
+    a.dstate0 = dstate;
+    a.dweight = dweight;
+    a.dbias = dbias;
+    a.partial = (float *)workspace;
+    const hipError_t e = sdm::launch_conv_backward(a, (hipStream_t)stream);
+    return e == hipSuccess ? SDM_OK : hip_fail(e, "convolution backward launch");
+}
+
+}  // extern "C"

@@ -1,0 +1,34 @@
+// Internal declarations of the sequence mixers beside the SDM core: the short
+// causal convolution, the selective state space scan and sliding-window
+// attention (not installed).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "sdm.h"
+
+namespace sdm {
+
+// Thread-local error text of the C entry points (sdm_api.cpp).
+sdm_status set_error(sdm_status s, const char *fmt, ...);
+
+struct ConvArgs {
+    sdm_conv_desc d;
+    const void *x, *dy;
+    const float *weight, *bias;
+    const int32_t *lengths;
+    bool cont;              // forward: `state` holds the rows before x
+    const void *state0;     // backward: rows before x, or null
+    const void *dstateT;    // backward: gradient of the final state, or null
+    void *y, *state;        // forward outputs
+    void *dx, *dstate0;     // backward outputs
+    float *dweight, *dbias;
+    float *partial;         // backward: [blocks][K + 1][C] sums
+};
+size_t conv_backward_ws(const sdm_conv_desc &d);
+hipError_t launch_conv_forward(const ConvArgs &a, hipStream_t stream);
+hipError_t launch_conv_backward(const ConvArgs &a, hipStream_t stream);
+
+}  // namespace sdm

@@ -10,6 +10,7 @@
 #include <new>
 #include <string>
 
+#include "mix_internal.h"
 #include "sdm_internal.h"
 
 // Scratch of sdm_forward_noalloc: the workspace of one forward call, in a
@@ -195,6 +196,16 @@ sdm_status scratch_on(hipStream_t stream, void **out)
 }
 
 }  // namespace
+
+sdm_status sdm::set_error(sdm_status s, const char *fmt, ...)
+{
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof buf, fmt, ap);
+    va_end(ap);
+    return fail(s, "%s", buf);
+}
 
 extern "C" {
 
