@@ -408,6 +408,64 @@ sdm_status sdm_conv_backward(const sdm_conv_desc *d, const void *x, const float 
                              size_t ws_bytes, void *dx, float *dweight, float *dbias,
                              void *dstate, void *stream);
 
+/*
+ * Selective state space scan, one decay per head and token; B and C are shared
+ * by the H / G heads of a group.  Per sequence and head, with
+ *   D_t = softplus(dt_t + dt_bias)   (softplus = 0: D_t = dt_t + dt_bias)
+ *   S_t = exp(D_t A) S_{t-1} + D_t x_t B_t^T      (P x N)
+ *   y_t = S_t C_t + D x_t
+ * A <= 0 and D_t >= 0 are the intended ranges (not checked).
+ * Limits: 1 <= N <= 128, 1 <= P, G divides H; B * T * H < 2^31, B * H < 65536.
+ */
+typedef struct {
+    int B;
+    int64_t T;
+    int H, P, N, G;
+    int softplus;             /* 0 or 1 */
+    sdm_dtype dtype;          /* SDM_F32 or SDM_BF16 */
+    int64_t x_batch, x_token; /* strides; heads and columns are dense */
+    int64_t B_batch, B_token;
+    int64_t C_batch, C_token;
+} sdm_scan_desc;
+
+/*
+ *   x        device [B][T][H][P] (strided)
+ *   dt       device [B][T][H]
+ *   Bm, Cm   device [B][T][G][N] (strided)
+ *   A        device [H] float32;  D, dt_bias  device [H] float32 or NULL
+ *   flags    SDM_FLAG_CONTINUE: start from `state` (otherwise from zero)
+ *   workspace  >= sdm_scan_workspace_size bytes, 16-byte aligned
+ *   y        device [B][T][H][P]
+ *   state    device [B][H][P][N] float32, updated in place: the last state.
+ */
+sdm_status sdm_scan_workspace_size(const sdm_scan_desc *d, size_t *bytes);
+
+sdm_status sdm_scan_forward(const sdm_scan_desc *d, const void *x, const void *dt, const void *Bm,
+                            const void *Cm, const float *A, const float *D, const float *dt_bias,
+                            const int32_t *lengths, unsigned flags, void *workspace,
+                            size_t ws_bytes, void *y, float *state, void *stream);
+
+/*
+ * Gradients of the scan (the states are recomputed from the inputs).
+ *   dy       device [B][T][H][P]
+ *   state    device [B][H][P][N] float32, the state the forward started from,
+ *            or NULL for zero
+ *   dstateT  device [B][H][P][N] float32, dL/d(final state), or NULL for zero
+ *   workspace  >= sdm_scan_backward_workspace_size bytes, 16-byte aligned
+ *            (two float32 states for every 64 tokens and head)
+ * Outputs: dx [B][T][H][P], ddt [B][T][H], dB, dC [B][T][G][N]; float32
+ * dA [H], dD [H], ddt_bias [H] (dD, ddt_bias NULL to skip), and dstate
+ * [B][H][P][N], dL/d(state), or NULL to skip.
+ */
+sdm_status sdm_scan_backward_workspace_size(const sdm_scan_desc *d, size_t *bytes);
+
+sdm_status sdm_scan_backward(const sdm_scan_desc *d, const void *x, const void *dt,
+                             const void *Bm, const void *Cm, const float *A, const float *D,
+                             const float *dt_bias, const int32_t *lengths, const void *dy,
+                             const float *state, const float *dstateT, void *workspace,
+                             size_t ws_bytes, void *dx, void *ddt, void *dB, void *dC, float *dA,
+                             float *dD, float *ddt_bias, float *dstate, void *stream);
+
 /* Static description of a status code. */
 const char *sdm_status_string(sdm_status s);
 

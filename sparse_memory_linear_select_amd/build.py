@@ -23,7 +23,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libsdm.so")
 
 SOURCES = ["select.hip", "init.hip", "plan.hip", "rw_serial.hip", "rw_timepar.hip", "decode.hip",
-           "backward.hip", "causal_conv.hip",
+           "backward.hip", "causal_conv.hip", "selective_scan.hip",
            "sdm_api.cpp", "mix_api.cpp"]
 
 HIPCC = os.environ.get("HIPCC", "hipcc")

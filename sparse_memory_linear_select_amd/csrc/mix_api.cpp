@@ -84,6 +84,45 @@ sdm_status check_conv(const sdm_conv_desc *d)
     return SDM_OK;
 }
 
+// -------------------------------------------------------------------- scan
+
+sdm_status check_scan(const sdm_scan_desc *d)
+{
+    if (!d) return set_error(SDM_ERR_ARG, "null descriptor");
+    CHECK(check_batch(d->B, d->T, d->dtype));
+    if (d->H < 1 || d->P < 1 || d->N < 1 || d->G < 1)
+        return set_error(SDM_ERR_ARG, "H, P, N, G must be >= 1 (got %d %d %d %d)", d->H, d->P, d->N,
+                         d->G);
+    if (d->H % d->G)
+        return set_error(SDM_ERR_ARG, "G = %d must divide H = %d", d->G, d->H);
+    if (d->softplus != 0 && d->softplus != 1)
+        return set_error(SDM_ERR_ARG, "softplus must be 0 or 1 (got %d)", d->softplus);
+    if (d->x_batch < 0 || d->x_token < 0 || d->B_batch < 0 || d->B_token < 0 || d->C_batch < 0 ||
+        d->C_token < 0)
+        return set_error(SDM_ERR_ARG, "strides must be >= 0");
+    if (d->N > 128) return set_error(SDM_ERR_UNSUPPORTED, "N <= 128 is supported (got %d)", d->N);
+    if (d->P > 65536) return set_error(SDM_ERR_UNSUPPORTED, "P <= 65536 is supported (got %d)", d->P);
+    if ((double)d->B * (double)d->T * d->H >= 2147483648.0)
+        return set_error(SDM_ERR_UNSUPPORTED, "B*T*H must be < 2^31");
+    if ((double)d->B * d->H >= 65536.0)
+        return set_error(SDM_ERR_UNSUPPORTED, "B*H must be < 65536");
+    return SDM_OK;
+}
+
+sdm_status check_scan_inputs(const sdm_scan_desc *d, const void *x, const void *dt, const void *Bm,
+                             const void *Cm, const float *A, const float *D, const float *dt_bias,
+                             const int32_t *lengths)
+{
+    CHECK(check_strided(x, "x", d->dtype));
+    CHECK(check_dense(dt, "dt"));
+    CHECK(check_strided(Bm, "Bm", d->dtype));
+    CHECK(check_strided(Cm, "Cm", d->dtype));
+    CHECK(check_dense(A, "A"));
+    CHECK(check_dense(D, "D", false));
+    CHECK(check_dense(dt_bias, "dt_bias", false));
+    return check_lengths(lengths);
+}
+
 }  // namespace
 
 extern "C" {
@@ -157,6 +196,100 @@ sdm_status sdm_conv_backward(const sdm_conv_desc *d, const void *x, const float 
     a.partial = (float *)workspace;
     const hipError_t e = sdm::launch_conv_backward(a, (hipStream_t)stream);
     return e == hipSuccess ? SDM_OK : hip_fail(e, "convolution backward launch");
+}
+
+sdm_status sdm_scan_workspace_size(const sdm_scan_desc *d, size_t *bytes)
+{
+    if (!bytes) return set_error(SDM_ERR_ARG, "null bytes pointer");
+    *bytes = 0;
+    CHECK(check_scan(d));
+    *bytes = sdm::scan_forward_ws(*d);
+    return SDM_OK;
+}
+
+sdm_status sdm_scan_forward(const sdm_scan_desc *d, const void *x, const void *dt, const void *Bm,
+                            const void *Cm, const float *A, const float *D, const float *dt_bias,
+                            const int32_t *lengths, unsigned flags, void *workspace,
+                            size_t ws_bytes, void *y, float *state, void *stream)
+{
+    CHECK(check_scan(d));
+    if (flags & ~SDM_FLAG_CONTINUE) return set_error(SDM_ERR_ARG, "unknown flags 0x%x", flags);
+    CHECK(check_scan_inputs(d, x, dt, Bm, Cm, A, D, dt_bias, lengths));
+    CHECK(check_dense(y, "y"));
+    CHECK(check_dense(state, "state"));
+    CHECK(check_workspace(workspace, ws_bytes, sdm::scan_forward_ws(*d)));
+    sdm::ScanArgs a = {};
+    a.d = *d;
+    a.x = x;
+    a.dt = dt;
+    a.Bm = Bm;
+    a.Cm = Cm;
+    a.A = A;
+    a.D = D;
+    a.dt_bias = dt_bias;
+    a.lengths = lengths;
+    a.cont = flags & SDM_FLAG_CONTINUE;
+    a.y = y;
+    a.state = state;
+    a.ws = (unsigned char *)workspace;
+    const hipError_t e = sdm::launch_scan_forward(a, (hipStream_t)stream);
+    return e == hipSuccess ? SDM_OK : hip_fail(e, "scan launch");
+}
+
+sdm_status sdm_scan_backward_workspace_size(const sdm_scan_desc *d, size_t *bytes)
+{
+    if (!bytes) return set_error(SDM_ERR_ARG, "null bytes pointer");
+    *bytes = 0;
+    CHECK(check_scan(d));
+    *bytes = sdm::scan_backward_ws(*d);
+    return SDM_OK;
+}
+
+sdm_status sdm_scan_backward(const sdm_scan_desc *d, const void *x, const void *dt,
+                             const void *Bm, const void *Cm, const float *A, const float *D,
+                             const float *dt_bias, const int32_t *lengths, const void *dy,
+                             const float *state, const float *dstateT, void *workspace,
+                             size_t ws_bytes, void *dx, void *ddt, void *dB, void *dC, float *dA,
+                             float *dD, float *ddt_bias, float *dstate, void *stream)
+{
+    CHECK(check_scan(d));
+    CHECK(check_scan_inputs(d, x, dt, Bm, Cm, A, D, dt_bias, lengths));
+    CHECK(check_dense(dy, "dy"));
+    CHECK(check_dense(state, "state", false));
+    CHECK(check_dense(dstateT, "dstateT", false));
+    CHECK(check_dense(dx, "dx"));
+    CHECK(check_dense(ddt, "ddt"));
+    CHECK(check_dense(dB, "dB"));
+    CHECK(check_dense(dC, "dC"));
+    CHECK(check_dense(dA, "dA"));
+    CHECK(check_dense(dD, "dD", false));
+    CHECK(check_dense(ddt_bias, "ddt_bias", false));
+    CHECK(check_dense(dstate, "dstate", false));
+    CHECK(check_workspace(workspace, ws_bytes, sdm::scan_backward_ws(*d)));
+    sdm::ScanArgs a = {};
+    a.d = *d;
+    a.x = x;
+    a.dt = dt;
+    a.Bm = Bm;
+    a.Cm = Cm;
+    a.A = A;
+    a.D = D;
+    a.dt_bias = dt_bias;
+    a.lengths = lengths;
+    a.dy = dy;
+    a.state0 = state;
+    a.dstateT = dstateT;
+    a.dx = dx;
+    a.ddt = ddt;
+    a.dB = dB;
+    a.dC = dC;
+    a.dA = dA;
+    a.dD = dD;
+    a.ddt_bias = ddt_bias;
+    a.dstate0 = dstate;
+    a.ws = (unsigned char *)workspace;
+    const hipError_t e = sdm::launch_scan_backward(a, (hipStream_t)stream);
+    return e == hipSuccess ? SDM_OK : hip_fail(e, "scan backward launch");
 }
 
 }  // extern "C"

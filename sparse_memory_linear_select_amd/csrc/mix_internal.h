@@ -31,4 +31,23 @@ size_t conv_backward_ws(const sdm_conv_desc &d);
 hipError_t launch_conv_forward(const ConvArgs &a, hipStream_t stream);
 hipError_t launch_conv_backward(const ConvArgs &a, hipStream_t stream);
 
+struct ScanArgs {
+    sdm_scan_desc d;
+    const void *x, *dt, *Bm, *Cm;
+    const float *A, *D, *dt_bias;
+    const int32_t *lengths;
+    bool cont;                      // forward: `state` holds the state before x
+    void *y;
+    float *state;
+    const void *dy;                 // backward
+    const float *state0, *dstateT;
+    void *dx, *ddt, *dB, *dC;
+    float *dA, *dD, *ddt_bias, *dstate0;
+    unsigned char *ws;
+};
+size_t scan_forward_ws(const sdm_scan_desc &d);
+size_t scan_backward_ws(const sdm_scan_desc &d);
+hipError_t launch_scan_forward(const ScanArgs &a, hipStream_t stream);
+hipError_t launch_scan_backward(const ScanArgs &a, hipStream_t stream);
+
 }  // namespace sdm

@@ -1,0 +1,922 @@
+// Selective state space scan: one decay per head and token, B and C shared by
+// the heads of a group.  Per head, with D_t = softplus(dt_t + bias):
+//   S_t = a_t S_{t-1} + D_t x_t B_t^T,  a_t = e^{D_t A},   y_t = S_t C_t + D x_t
+//
+// In chunks of 64 tokens, with c_t the running sum of log2 a in the chunk
+// (kept as two float32 that hold it to 48 bits, so that differences of large
+// sums stay exact) and S the state before the chunk:
+//   y_t = 2^{c_t} S C_t + sum_{s <= t} M_ts x_s,   M_ts = (C_t.B_s) 2^{c_t - c_s} D_s
+//   S  <- 2^{c_63} S + sum_s x_s (w_s B_s)^T,      w_s = 2^{c_63 - c_s} D_s
+// which are 16x16 matrix products.  Every exponent is a sum of logs of decays
+// (<= 0 for A <= 0), so nothing is divided by a decay.
+#include "mix_internal.h"
+
+#include "mix_device.h"
+
+namespace sdm {
+namespace {
+
+constexpr int Q = 64;         // tokens of a chunk
+constexpr int kSlice = 64;    // columns of x that a workgroup holds: 16 a wave
+constexpr int kThreads = 256;
+constexpr int LX = kSlice + 8;  // LDS row stride of 64-wide tiles
+
+struct ScanDims {
+    int B, H, P, N, G;
+    int64_t T;
+    int nc;                    // chunks
+    int nps;                   // slices of x's columns
+    int nseg, cps;             // segments of the time axis, chunks of each
+    int64_t xb, xt, bb, bt, cb, ct;
+};
+
+// ------------------------------------------------------------------ decays
+// delta[bh][t] = D_t and cs[bh][t] = c_t (high and low part) for whole chunks;
+// tokens behind a sequence's length have D = 0 (the state passes unchanged).
+// A wave per (sequence, chunk, head); lane = token.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void scan_prep_kernel(
+    ScanDims d, const T *__restrict__ dt, const float *__restrict__ A,
+    const float *__restrict__ bias, const int32_t *__restrict__ lengths, int softplus,
+    float *__restrict__ delta, float2 *__restrict__ cs)
+{
+    const int64_t u = (int64_t)blockIdx.x * 4 + threadIdx.y;
+    if (u >= (int64_t)d.B * d.nc * d.H) return;
+    const int h = (int)(u % d.H);
+    const int64_t bc = u / d.H;
+    const int c = (int)(bc % d.nc);
+    const int64_t b = bc / d.nc;
+    const int64_t t = (int64_t)c * Q + threadIdx.x;
+    float v = 0.f;
+    if (t < seq_len(lengths, b, d.T)) {
+        v = (float)dt[(b * d.T + t) * d.H + h] + (bias ? bias[h] : 0.f);
+        if (softplus) v = v > 20.f ? v : log1pf(expf(v));
+    }
+    double l = (double)v * (double)A[h] * 1.4426950408889634;
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) {
+        const double o = __shfl_up(l, m);
+        if ((int)threadIdx.x >= m) l += o;
+    }
+    const int64_t at = ((b * d.H + h) * d.nc + c) * Q + threadIdx.x;
+    delta[at] = v;
+    const float hi = (float)l;
+    cs[at] = make_float2(hi, (float)(l - (double)hi));
+}
+
+// 2^{c_t - c_s}
+__device__ __forceinline__ float decay(float2 t, float2 s)
+{
+    return exp2_fast((t.x - s.x) + (t.y - s.y));
+}
+
+// x of the lane n to the left in the 16-lane row, 0 for the row's first n lanes.
+template <int n>
+__device__ __forceinline__ float row_shr(float x)
+{
+    return __int_as_float(
+        __builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x110 | n, 0xF, 0xF, true));
+}
+
+// x of the row's last lane.
+__device__ __forceinline__ float row_last(float x)
+{
+    return __int_as_float(
+        __builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x150 | 15, 0xF, 0xF, true));
+}
+
+// One wave's part of a state: S^T, rows n = 16 j + (l / 16) * 4 + i of tile j,
+// column p of the lane.  In the caller's [P][N] layout or the workspace's [N][P].
+template <int NT>
+__device__ __forceinline__ void state_load(f32x4 (&S)[NT], const float *src, bool api, int p, int P, int N)
+{
+    const int g = (threadIdx.x & 63) >> 4;
+#pragma unroll
+    for (int j = 0; j < NT; j++)
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const int n = 16 * j + 4 * g + i;
+            S[j][i] = src && p < P && n < N ? src[api ? (int64_t)p * N + n : (int64_t)n * P + p] : 0.f;
+        }
+}
+
+template <int NT>
+__device__ __forceinline__ void state_store(const f32x4 (&S)[NT], float *dst, bool api, int p, int P, int N)
+{
+    const int g = (threadIdx.x & 63) >> 4;
+    if (p >= P) return;
+#pragma unroll
+    for (int j = 0; j < NT; j++)
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const int n = 16 * j + 4 * g + i;
+            if (n < N) dst[api ? (int64_t)p * N + n : (int64_t)n * P + p] = S[j][i];
+        }
+}
+
+// S <- scale S + sum_s V[s]^T (w_s U[s]) for one chunk: U [64][64], V [64][16 NT]
+// in LDS; the wave's 16 columns of U start at col0.  The weighted columns are
+// carried to 24 bits (three bfloat16 terms), so the float32 state keeps its
+// precision whatever the inputs' type.
+template <typename T, int NT>
+__device__ __forceinline__ void state_update(f32x4 (&S)[NT], const T *U, const T *V, const float *wt,
+                                             float scale, int col0)
+{
+    using M = Mat<T>;
+    constexpr int LN = NT * 16 + 8;
+    const int l = threadIdx.x & 63;
+    typename M::Frag uw[2][M::kTerms];
+#pragma unroll
+    for (int ks = 0; ks < 2; ks++) {
+        f32x8 v;
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            const int s = 32 * ks + (l >> 4) * 8 + i;
+            v[i] = (float)U[s * LX + col0 + (l & 15)] * wt[s];
+        }
+        split_frag<T>(v, uw[ks]);
+    }
+#pragma unroll
+    for (int j = 0; j < NT; j++) {
+        S[j] *= scale;
+#pragma unroll
+        for (int ks = 0; ks < 2; ks++) {
+            const auto a = frag_col<T>(V, LN, 32 * ks, 16 * j);
+#pragma unroll
+            for (int n = 0; n < M::kTerms; n++) S[j] = M::mma(a, uw[ks][n], S[j]);
+        }
+    }
+}
+
+// ----------------------------------------------------------------- forward
+// A workgroup walks the chunks of one (sequence, head, slice of 64 columns,
+// segment) in order with the state in registers: wave w owns columns 16 w ..
+// of the slice, for y and for the state.  C.B and M are shared by the waves
+// through LDS.
+template <typename T, int NT>
+__global__ __launch_bounds__(kThreads) void scan_walk_kernel(
+    ScanDims d, const T *__restrict__ x, const T *__restrict__ Bm, const T *__restrict__ Cm,
+    const float *__restrict__ D, const float *__restrict__ delta, const float2 *__restrict__ cs,
+    const int32_t *__restrict__ lengths, const float *init, int init_api, float *state,
+    T *__restrict__ y)
+{
+    using M = Mat<T>;
+    constexpr int LN = NT * 16 + 8;
+    __shared__ __align__(32) T Xs[Q * LX];
+    __shared__ __align__(32) T Bs[Q * LN];
+    __shared__ __align__(32) T Cs[Q * LN];
+    __shared__ __align__(32) T Ms[Q * LX];
+    __shared__ float dl[Q], wt[Q];
+    __shared__ float2 cc[Q];
+
+    const int seg = blockIdx.x % d.nseg;
+    const int64_t r0 = blockIdx.x / d.nseg;
+    const int ps = (int)(r0 % d.nps);
+    const int64_t bh = r0 / d.nps;
+    const int h = (int)(bh % d.H);
+    const int64_t b = bh / d.H;
+    const int grp = h / (d.H / d.G);
+    const int64_t len = seq_len(lengths, b, d.T);
+    const int l = threadIdx.x & 63, w = threadIdx.x >> 6, g = l >> 4, li = l & 15;
+    const int pcols = d.P - ps * kSlice < kSlice ? d.P - ps * kSlice : kSlice;
+    const int p = ps * kSlice + 16 * w + li;
+    const T *xp = x + b * d.xb + (int64_t)h * d.P + ps * kSlice;
+    const T *bp = Bm + b * d.bb + (int64_t)grp * d.N;
+    const T *cp = Cm + b * d.cb + (int64_t)grp * d.N;
+    const bool vx = rows_aligned(xp, d.xb, d.xt, pcols, sizeof(T));
+    const bool vb = rows_aligned(bp, d.bb, d.bt, d.N, sizeof(T));
+    const bool vc = rows_aligned(cp, d.cb, d.ct, d.N, sizeof(T));
+    const float Dh = D ? D[h] : 0.f;
+
+    f32x4 S[NT];
+    {
+        const float *src = init;
+        if (src) src += (init_api ? bh : bh * d.nseg + seg) * (int64_t)d.P * d.N;
+        state_load<NT>(S, src, init_api, p, d.P, d.N);
+    }
+    const int c0 = seg * d.cps, c1 = c0 + d.cps < d.nc ? c0 + d.cps : d.nc;
+    for (int c = c0; c < c1; c++) {
+        const int64_t t0 = (int64_t)c * Q;
+        const int rows = len - t0 < 0 ? 0 : len - t0 < Q ? (int)(len - t0) : Q;
+        load_tile<T, Q, kSlice, LX, kThreads>(Xs, xp + t0 * d.xt, d.xt, rows, pcols, vx);
+        load_tile<T, Q, NT * 16, LN, kThreads>(Bs, bp + t0 * d.bt, d.bt, rows, d.N, vb);
+        load_tile<T, Q, NT * 16, LN, kThreads>(Cs, cp + t0 * d.ct, d.ct, rows, d.N, vc);
+        if (threadIdx.x < Q) {
+            const int64_t at = (bh * d.nc + c) * Q;
+            const float2 me = cs[at + threadIdx.x];
+            const float dv = delta[at + threadIdx.x];
+            dl[threadIdx.x] = dv;
+            cc[threadIdx.x] = me;
+            wt[threadIdx.x] = decay(cs[at + Q - 1], me) * dv;
+        }
+        __syncthreads();
+        // M, rows 16 w .. + 15; tiles right of the diagonal are zero
+#pragma unroll
+        for (int ct = 0; ct < 4; ct++) {
+            if (ct > (w | 1)) break;
+            f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+            if (ct <= w)
+#pragma unroll
+                for (int ks = 0; ks < NT / 2; ks++)
+                    acc = M::mma(frag_row<T>(Cs, LN, 16 * w, 32 * ks),
+                                 frag_row<T>(Bs, LN, 16 * ct, 32 * ks), acc);
+            const int s = 16 * ct + li;
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const int t = 16 * w + 4 * g + i;
+                Ms[t * LX + s] = (T)(s <= t ? acc[i] * decay(cc[t], cc[s]) * dl[s] : 0.f);
+            }
+        }
+        __syncthreads();
+        // y for the wave's columns
+        typename M::Frag sf[NT / 2], xf[2];
+#pragma unroll
+        for (int j = 0; j < NT / 2; j++)
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                sf[j][i] = (T)S[2 * j][i];
+                sf[j][4 + i] = (T)S[2 * j + 1][i];
+            }
+#pragma unroll
+        for (int ks = 0; ks < 2; ks++) xf[ks] = frag_col<T>(Xs, LX, 32 * ks, 16 * w);
+#pragma unroll
+        for (int r = 0; r < 4; r++) {
+            f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int j = 0; j < NT / 2; j++) {
+                // C rows with k in the order the state's tiles hold n
+                const T *q = Cs + (16 * r + li) * LN + 32 * j + 4 * g;
+                const auto lo = *reinterpret_cast<const typename M::Half *>(q);
+                const auto hi = *reinterpret_cast<const typename M::Half *>(q + 16);
+                acc = M::mma(__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7), sf[j], acc);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const float2 e = cc[16 * r + 4 * g + i];
+                acc[i] *= exp2_fast(e.x + e.y);
+            }
+#pragma unroll
+            for (int ks = 0; ks <= r / 2; ks++)
+                acc = M::mma(frag_row<T>(Ms, LX, 16 * r, 32 * ks), xf[ks], acc);
+            if (p < d.P)
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    const int t = 16 * r + 4 * g + i;
+                    if (t0 + t < d.T) {
+                        const float v = acc[i] + Dh * (float)Xs[t * LX + 16 * w + li];
+                        y[((b * d.T + t0 + t) * d.H + h) * d.P + p] = (T)(t < rows ? v : 0.f);
+                    }
+                }
+        }
+        const float2 tot = cc[Q - 1];
+        state_update<T, NT>(S, Xs, Bs, wt, exp2_fast(tot.x + tot.y), 16 * w);
+        __syncthreads();
+    }
+    if (seg == d.nseg - 1) state_store<NT>(S, state + bh * (int64_t)d.P * d.N, true, p, d.P, d.N);
+}
+
+// States alone.  Forward (REV = false): U = x, V = B, weights 2^{c_63 - c_s} D_s;
+// `each` gets the state before every chunk.  Reverse: U = dy, V = C, weights
+// 2^{c_t}, chunks from last to first: the gradient G of the state,
+//   G <- 2^{c_63} G + sum_t 2^{c_t} C_t dy_t^T,
+// and `each` gets G behind every chunk.  `end` gets the last one: per segment
+// in the workspace's layout, or (end_api) the caller's gradient.
+template <typename T, int NT, bool REV>
+__global__ __launch_bounds__(kThreads) void scan_state_kernel(
+    ScanDims d, const T *__restrict__ U, int64_t ub, int64_t ut, const T *__restrict__ V, int64_t vb,
+    int64_t vt, const float *__restrict__ delta, const float2 *__restrict__ cs,
+    const int32_t *__restrict__ lengths, const float *init, int init_api, float *each, float *end,
+    int end_api)
+{
+    constexpr int LN = NT * 16 + 8;
+    __shared__ __align__(32) T Us[Q * LX];
+    __shared__ __align__(32) T Vs[Q * LN];
+    __shared__ float wt[Q];
+
+    const int seg = blockIdx.x % d.nseg;
+    const int64_t r0 = blockIdx.x / d.nseg;
+    const int ps = (int)(r0 % d.nps);
+    const int64_t bh = r0 / d.nps;
+    const int h = (int)(bh % d.H);
+    const int64_t b = bh / d.H;
+    const int grp = h / (d.H / d.G);
+    const int64_t len = seq_len(lengths, b, d.T);
+    const int l = threadIdx.x & 63, w = threadIdx.x >> 6;
+    const int pcols = d.P - ps * kSlice < kSlice ? d.P - ps * kSlice : kSlice;
+    const int p = ps * kSlice + 16 * w + (l & 15);
+    const int64_t PN = (int64_t)d.P * d.N;
+    const T *up = U + b * ub + (int64_t)h * d.P + ps * kSlice;
+    const T *vp = V + b * vb + (int64_t)grp * d.N;
+    const bool au = rows_aligned(up, ub, ut, pcols, sizeof(T));
+    const bool av = rows_aligned(vp, vb, vt, d.N, sizeof(T));
+
+    f32x4 S[NT];
+    {
+        const float *src = init;
+        if (src) src += (init_api ? bh : bh * d.nseg + seg) * PN;
+        state_load<NT>(S, src, init_api, p, d.P, d.N);
+    }
+    const int c0 = seg * d.cps, c1 = c0 + d.cps < d.nc ? c0 + d.cps : d.nc;
+    for (int k = c0; k < c1; k++) {
+        const int c = REV ? c0 + c1 - 1 - k : k;
+        if (each) state_store<NT>(S, each + (bh * d.nc + c) * PN, false, p, d.P, d.N);
+        const int64_t t0 = (int64_t)c * Q;
+        const int rows = len - t0 < 0 ? 0 : len - t0 < Q ? (int)(len - t0) : Q;
+        load_tile<T, Q, kSlice, LX, kThreads>(Us, up + t0 * ut, ut, rows, pcols, au);
+        load_tile<T, Q, NT * 16, LN, kThreads>(Vs, vp + t0 * vt, vt, rows, d.N, av);
+        const int64_t at = (bh * d.nc + c) * Q;
+        const float2 tot = cs[at + Q - 1];
+        if (threadIdx.x < Q) {
+            const float2 me = cs[at + threadIdx.x];
+            wt[threadIdx.x] = REV ? exp2_fast(me.x + me.y) : decay(tot, me) * delta[at + threadIdx.x];
+        }
+        __syncthreads();
+        state_update<T, NT>(S, Us, Vs, wt, exp2_fast(tot.x + tot.y), 16 * w);
+        __syncthreads();
+    }
+    if (!end) return;
+    if (!end_api)
+        state_store<NT>(S, end + (bh * d.nseg + seg) * PN, false, p, d.P, d.N);
+    else if (seg == (REV ? 0 : d.nseg - 1))
+        state_store<NT>(S, end + bh * PN, true, p, d.P, d.N);
+}
+
+// Joins the segments: from each segment's own contribution (`own`, computed
+// from zero) and the state before the first one, the state before every
+// segment, in the order of the walk.
+template <bool REV>
+__global__ __launch_bounds__(kThreads) void scan_join_kernel(ScanDims d, const float2 *__restrict__ cs,
+                                                             const float *first,
+                                                             const float *__restrict__ own,
+                                                             float *__restrict__ start)
+{
+    const int64_t PN = (int64_t)d.P * d.N;
+    const int64_t e = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    const int64_t bh = blockIdx.y;
+    if (e >= PN) return;
+    const int n = (int)(e / d.P), p = (int)(e % d.P);
+    float S = first ? first[bh * PN + (int64_t)p * d.N + n] : 0.f;
+    for (int k = 0; k < d.nseg; k++) {
+        const int seg = REV ? d.nseg - 1 - k : k;
+        start[(bh * d.nseg + seg) * PN + e] = S;
+        const int c0 = seg * d.cps, c1 = c0 + d.cps < d.nc ? c0 + d.cps : d.nc;
+        float sum = 0.f;
+        for (int c = c0; c < c1; c++) {
+            const float2 t = cs[(bh * d.nc + c) * Q + Q - 1];
+            sum += t.x + t.y;
+        }
+        S = fmaf(exp2_fast(sum), S, own[(bh * d.nseg + seg) * PN + e]);
+    }
+}
+
+// ---------------------------------------------------------------- backward
+// Gradients of one chunk from the state S before it, the gradient G of the
+// state behind it (both in [N][P]) and the inputs.  With E_ts = 2^{c_t - c_s},
+// for s <= t:
+//   dx_s = sum_t M_ts dy_t + w_s G B_s + D dy_s
+//   dC_t = sum_h sum_s W_ts B_s + 2^{c_t} S^T dy_t,     W_ts = (dy_t.x_s) E_ts D_s
+//   dB_s = sum_h sum_t W_ts C_t + w_s G^T x_s
+//   dD_s = sum_t e_ts + 2^{c_63 - c_s} B_s.(G^T x_s) + A dl_s,  e_ts = (C_t.B_s)(dy_t.x_s) E_ts
+// and the gradient of a token's log decay collects what flows across it: pairs
+// of a source before it (in the chunk, or S) and a target from it on (in the
+// chunk, or G),
+//   dl_r = sum_{s < r <= t} e_ts D_s + sum_{t >= r} 2^{c_t} dy_t.S C_t
+//        + sum_{s < r} w_s x_s.G B_s + 2^{c_63} <G, S>,
+// which is made of such sums alone, never of the difference of two long ones.
+// The pairs in the chunk are summed as prefixes over s of every row t, then
+// over t: a small flow across a boundary keeps its own precision beside large
+// pairs on one side of it.  S and G enter the products for dC, dB and dD to 24
+// bits.
+//
+// A workgroup owns a chunk and a block of the heads of a group, whose sums for
+// dB and dC stay in registers.  Wave w owns rows 16 w .. of the 64 x 64
+// products, columns 16 w .. of dx, and a quarter of the columns n.
+template <typename T, int NT>
+__global__ __launch_bounds__(kThreads) void scan_grad_kernel(
+    ScanDims d, int hblocks, const T *__restrict__ x, const T *__restrict__ dy,
+    const T *__restrict__ Bm, const T *__restrict__ Cm, const float *__restrict__ A,
+    const float *__restrict__ D, const float *__restrict__ delta, const float2 *__restrict__ cs,
+    const int32_t *__restrict__ lengths, int softplus, const float *__restrict__ Sws,
+    const float *__restrict__ Gws, T *__restrict__ dx, T *__restrict__ ddt, T *__restrict__ dB,
+    T *__restrict__ dC, float *__restrict__ parts, float *__restrict__ hsum)
+{
+    using M = Mat<T>;
+    constexpr int LN = NT * 16 + 8;
+    constexpr int NW = NT >= 4 ? NT / 4 : 1;  // 16-column tiles of n per wave
+    __shared__ __align__(32) T Xs[Q * LX];
+    __shared__ __align__(32) T Ys[Q * LX];
+    __shared__ __align__(32) T Bs[Q * LN];
+    __shared__ __align__(32) T Cs[Q * LN];
+    __shared__ __align__(32) T Ms[Q * LX];
+    __shared__ __align__(32) T Ws[Q * LX];
+    __shared__ float dl[Q], wt[Q], et[Q];
+    __shared__ float2 cc[Q];
+    __shared__ float colE[4][Q], colS[4][Q];  // per wave of rows t: sum_t e_ts, and pairs across s
+    __shared__ float dotC[4][Q], dotB[4][Q];  // per wave of columns: C_t.(S^T dy_t), B_s.(G^T x_s)
+    __shared__ float gs[4], dd[4];
+
+    const int hb = blockIdx.x % hblocks;
+    const int64_t r0 = blockIdx.x / hblocks;
+    const int grp = (int)(r0 % d.G);
+    const int64_t r1 = r0 / d.G;
+    const int c = (int)(r1 % d.nc);
+    const int64_t b = r1 / d.nc;
+    const int per = d.H / d.G;
+    const int h0 = grp * per + (int)((int64_t)per * hb / hblocks);
+    const int h1 = grp * per + (int)((int64_t)per * (hb + 1) / hblocks);
+    const int64_t t0 = (int64_t)c * Q;
+    const int64_t len = seq_len(lengths, b, d.T);
+    const int rows = len - t0 < 0 ? 0 : len - t0 < Q ? (int)(len - t0) : Q;
+    const int l = threadIdx.x & 63, w = threadIdx.x >> 6, g = l >> 4, li = l & 15;
+    const int64_t PN = (int64_t)d.P * d.N;
+    {
+        const T *bp = Bm + b * d.bb + (int64_t)grp * d.N;
+        const T *cp = Cm + b * d.cb + (int64_t)grp * d.N;
+        load_tile<T, Q, NT * 16, LN, kThreads>(Bs, bp + t0 * d.bt, d.bt, rows, d.N,
+                                               rows_aligned(bp, d.bb, d.bt, d.N, sizeof(T)));
+        load_tile<T, Q, NT * 16, LN, kThreads>(Cs, cp + t0 * d.ct, d.ct, rows, d.N,
+                                               rows_aligned(cp, d.cb, d.ct, d.N, sizeof(T)));
+    }
+    __syncthreads();
+    f32x4 CB[4];  // C_t.B_s, rows t = 16 w ..
+#pragma unroll
+    for (int ct = 0; ct < 4; ct++) {
+        CB[ct] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (ct <= w)
+#pragma unroll
+            for (int ks = 0; ks < NT / 2; ks++)
+                CB[ct] = M::mma(frag_row<T>(Cs, LN, 16 * w, 32 * ks),
+                                frag_row<T>(Bs, LN, 16 * ct, 32 * ks), CB[ct]);
+    }
+    const int nt0 = w * NW;                // the wave's column tiles of n
+    const bool ncols = nt0 < NT;
+    f32x4 dCa[4][NW], dBa[4][NW];
+#pragma unroll
+    for (int r = 0; r < 4; r++)
+#pragma unroll
+        for (int j = 0; j < NW; j++) dCa[r][j] = dBa[r][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    for (int h = h0; h < h1; h++) {
+        const int64_t bh = b * d.H + h;
+        const float Dh = D ? D[h] : 0.f;
+        __syncthreads();
+        if (threadIdx.x < Q) {
+            const int64_t at = (bh * d.nc + c) * Q;
+            const float2 me = cs[at + threadIdx.x];
+            const float dv = delta[at + threadIdx.x];
+            dl[threadIdx.x] = dv;
+            cc[threadIdx.x] = me;
+            et[threadIdx.x] = decay(cs[at + Q - 1], me);
+            wt[threadIdx.x] = et[threadIdx.x] * dv;
+        }
+        __syncthreads();
+        f32x4 E[4], DX[4];
+#pragma unroll
+        for (int ct = 0; ct < 4; ct++) {
+            const int s = 16 * ct + li;
+            DX[ct] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const int t = 16 * w + 4 * g + i;
+                E[ct][i] = s <= t ? decay(cc[t], cc[s]) : 0.f;
+                Ms[t * LX + s] = (T)(CB[ct][i] * E[ct][i] * dl[s]);
+            }
+        }
+        f32x4 aC[4][NW], aB[4][NW];
+#pragma unroll
+        for (int r = 0; r < 4; r++)
+#pragma unroll
+            for (int j = 0; j < NW; j++) aC[r][j] = aB[r][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+        float gdot = 0.f, ddot = 0.f;
+        const float *Sh = Sws + (bh * d.nc + c) * PN;
+        const float *Gh = Gws + (bh * d.nc + c) * PN;
+
+        for (int ps = 0; ps < d.nps; ps++) {
+            const int p0 = ps * kSlice;
+            const int pcols = d.P - p0 < kSlice ? d.P - p0 : kSlice;
+            const T *xp = x + b * d.xb + (int64_t)h * d.P + p0;
+            const T *yp = dy + b * d.T * d.H * d.P + (int64_t)h * d.P + p0;
+            const int64_t yt = (int64_t)d.H * d.P;
+            __syncthreads();
+            load_tile<T, Q, kSlice, LX, kThreads>(Xs, xp + t0 * d.xt, d.xt, rows, pcols,
+                                                  rows_aligned(xp, d.xb, d.xt, pcols, sizeof(T)));
+            load_tile<T, Q, kSlice, LX, kThreads>(Ys, yp + t0 * yt, yt, rows, pcols,
+                                                  rows_aligned(yp, 0, yt, pcols, sizeof(T)));
+            __syncthreads();
+#pragma unroll
+            for (int ks = 0; ks < 2; ks++) {
+                const auto a = frag_row<T>(Ys, LX, 16 * w, 32 * ks);
+#pragma unroll
+                for (int ct = 0; ct < 4; ct++)
+                    if (ct <= w) DX[ct] = M::mma(a, frag_row<T>(Xs, LX, 16 * ct, 32 * ks), DX[ct]);
+            }
+            if (ncols) {
+#pragma unroll
+                for (int ks = 0; ks < 2; ks++)
+#pragma unroll
+                    for (int j = 0; j < NW; j++) {
+                        const int n = 16 * (nt0 + j) + li;
+                        f32x8 sv, gv;
+#pragma unroll
+                        for (int i = 0; i < 8; i++) {
+                            const int p = p0 + 32 * ks + 8 * g + i;
+                            const bool in = p < d.P && n < d.N;
+                            sv[i] = in ? Sh[(int64_t)n * d.P + p] : 0.f;
+                            gv[i] = in ? Gh[(int64_t)n * d.P + p] : 0.f;
+                            gdot = fmaf(sv[i], gv[i], gdot);
+                        }
+                        typename M::Frag sf[M::kTerms], gf[M::kTerms];
+                        split_frag<T>(sv, sf);
+                        split_frag<T>(gv, gf);
+#pragma unroll
+                        for (int r = 0; r < 4; r++) {
+                            const auto ya = frag_row<T>(Ys, LX, 16 * r, 32 * ks);
+                            const auto xa = frag_row<T>(Xs, LX, 16 * r, 32 * ks);
+#pragma unroll
+                            for (int m = 0; m < M::kTerms; m++) {
+                                aC[r][j] = M::mma(ya, sf[m], aC[r][j]);
+                                aB[r][j] = M::mma(xa, gf[m], aB[r][j]);
+                            }
+                        }
+                    }
+            }
+            // dx, the wave's 16 columns
+            const int p = p0 + 16 * w + li;
+            typename M::Frag gn[NT / 2];
+#pragma unroll
+            for (int kk = 0; kk < NT / 2; kk++)
+#pragma unroll
+                for (int i = 0; i < 8; i++) {
+                    const int n = 32 * kk + 8 * g + i;
+                    gn[kk][i] = (T)(p < d.P && n < d.N ? Gh[(int64_t)n * d.P + p] : 0.f);
+                }
+#pragma unroll
+            for (int r = 0; r < 4; r++) {
+                f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int kk = 0; kk < NT / 2; kk++)
+                    acc = M::mma(frag_row<T>(Bs, LN, 16 * r, 32 * kk), gn[kk], acc);
+#pragma unroll
+                for (int i = 0; i < 4; i++) acc[i] *= wt[16 * r + 4 * g + i];
+#pragma unroll
+                for (int ks = r / 2; ks < 2; ks++)
+                    acc = M::mma(frag_col<T>(Ms, LX, 32 * ks, 16 * r),
+                                 frag_col<T>(Ys, LX, 32 * ks, 16 * w), acc);
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    const int s = 16 * r + 4 * g + i;
+                    const float gy = (float)Ys[s * LX + 16 * w + li];
+                    ddot = fmaf(gy, (float)Xs[s * LX + 16 * w + li], ddot);
+                    if (p < d.P && t0 + s < d.T)
+                        dx[((b * d.T + t0 + s) * d.H + h) * d.P + p] =
+                            (T)(s < rows ? fmaf(Dh, gy, acc[i]) : 0.f);
+                }
+            }
+        }
+        // W, the sums of e over t, and per column r the pairs (s < r <= t)
+        float carry[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int ct = 0; ct < 4; ct++) {
+            const int s = 16 * ct + li;
+            float cE = 0.f, cS = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const int t = 16 * w + 4 * g + i;
+                const float wv = DX[ct][i] * E[ct][i];
+                const float e = wv * CB[ct][i];
+                Ws[t * LX + s] = (T)(wv * dl[s]);
+                cE += e;
+                float q = e * dl[s];  // prefix over the tile's 16 columns
+                q += row_shr<1>(q);
+                q += row_shr<2>(q);
+                q += row_shr<4>(q);
+                q += row_shr<8>(q);
+                cS += s <= t ? carry[i] + row_shr<1>(q) : 0.f;
+                carry[i] += row_last(q);
+            }
+            cE += __shfl_xor(cE, 16);
+            cE += __shfl_xor(cE, 32);
+            cS += __shfl_xor(cS, 16);
+            cS += __shfl_xor(cS, 32);
+            if (g == 0) {
+                colE[w][s] = cE;
+                colS[w][s] = cS;
+            }
+        }
+        // the parts through S and G: row dots, then the running sums
+#pragma unroll
+        for (int r = 0; r < 4; r++)
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const int t = 16 * r + 4 * g + i;
+                float vc = 0.f, vb = 0.f;
+                const float ec = exp2_fast(cc[t].x + cc[t].y);
+                if (ncols)
+#pragma unroll
+                    for (int j = 0; j < NW; j++) {
+                        const int n = 16 * (nt0 + j) + li;
+                        vc = fmaf(aC[r][j][i], (float)Cs[t * LN + n], vc);
+                        vb = fmaf(aB[r][j][i], (float)Bs[t * LN + n], vb);
+                        dCa[r][j][i] = fmaf(ec, aC[r][j][i], dCa[r][j][i]);
+                        dBa[r][j][i] = fmaf(wt[t], aB[r][j][i], dBa[r][j][i]);
+                    }
+#pragma unroll
+                for (int m = 1; m < 16; m <<= 1) {
+                    vc += __shfl_xor(vc, m);
+                    vb += __shfl_xor(vb, m);
+                }
+                if (li == 0) {
+                    dotC[w][t] = vc;
+                    dotB[w][t] = vb;
+                }
+            }
+#pragma unroll
+        for (int m = 1; m < 64; m <<= 1) {
+            gdot += __shfl_xor(gdot, m);
+            ddot += __shfl_xor(ddot, m);
+        }
+        if (l == 0) {
+            gs[w] = gdot;
+            dd[w] = ddot;
+        }
+        __syncthreads();
+        if (ncols)
+#pragma unroll
+            for (int j = 0; j < NW; j++)
+#pragma unroll
+                for (int ks = 0; ks < 2; ks++) {
+                    const auto bf = frag_col<T>(Bs, LN, 32 * ks, 16 * (nt0 + j));
+                    const auto cf = frag_col<T>(Cs, LN, 32 * ks, 16 * (nt0 + j));
+#pragma unroll
+                    for (int r = 0; r < 4; r++) {
+                        if (ks <= r / 2)
+                            dCa[r][j] = M::mma(frag_row<T>(Ws, LX, 16 * r, 32 * ks), bf, dCa[r][j]);
+                        if (ks >= r / 2)
+                            dBa[r][j] = M::mma(frag_col<T>(Ws, LX, 32 * ks, 16 * r), cf, dBa[r][j]);
+                    }
+                }
+        if (w == 0) {  // lane = token
+            const float2 tot = cc[Q - 1];
+            const float dC_ = (dotC[0][l] + dotC[1][l]) + (dotC[2][l] + dotC[3][l]);
+            const float dB_ = (dotB[0][l] + dotB[1][l]) + (dotB[2][l] + dotB[3][l]);
+            const float ce = (colE[0][l] + colE[1][l]) + (colE[2][l] + colE[3][l]);
+            const float cst = (colS[0][l] + colS[1][l]) + (colS[2][l] + colS[3][l]);
+            float suf = exp2_fast(cc[l].x + cc[l].y) * dC_;
+            float pre = wt[l] * dB_;
+#pragma unroll
+            for (int m = 1; m < 64; m <<= 1) {
+                const float a = __shfl_down(suf, m), q = __shfl_up(pre, m);
+                if (l + m < 64) suf += a;
+                if (l >= m) pre += q;
+            }
+            const float up = __shfl_up(pre, 1), before = l ? up : 0.f;
+            const float pass = exp2_fast(tot.x + tot.y) * ((gs[0] + gs[1]) + (gs[2] + gs[3]));
+            float dlr = (cst + suf) + (before + pass);
+            if (l >= rows) dlr = 0.f;
+            float dz = fmaf(A[h], dlr, fmaf(et[l], dB_, ce));
+            if (softplus) dz *= -expm1f(-dl[l]);
+            if (l >= rows) dz = 0.f;
+            if (t0 + l < d.T) ddt[(b * d.T + t0 + l) * d.H + h] = (T)dz;
+            float pa = dl[l] * dlr, pb = dz;
+#pragma unroll
+            for (int m = 1; m < 64; m <<= 1) {
+                pa += __shfl_xor(pa, m);
+                pb += __shfl_xor(pb, m);
+            }
+            if (l == 0) {
+                float *q = parts + ((b * d.nc + c) * d.H + h) * 3;
+                q[0] = pa;
+                q[1] = (dd[0] + dd[1]) + (dd[2] + dd[3]);
+                q[2] = pb;
+            }
+        }
+    }
+    if (!ncols) return;
+#pragma unroll
+    for (int r = 0; r < 4; r++)
+#pragma unroll
+        for (int j = 0; j < NW; j++)
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const int t = 16 * r + 4 * g + i, n = 16 * (nt0 + j) + li;
+                if (n >= d.N || t0 + t >= d.T) continue;
+                const int64_t at = ((b * d.T + t0 + t) * d.G + grp) * d.N + n;
+                const float vc = t < rows ? dCa[r][j][i] : 0.f, vb = t < rows ? dBa[r][j][i] : 0.f;
+                if (hblocks == 1) {
+                    dC[at] = (T)vc;
+                    dB[at] = (T)vb;
+                } else {
+                    const int64_t all = (int64_t)d.B * d.T * d.G * d.N;
+                    hsum[(2 * hb) * all + at] = vc;
+                    hsum[(2 * hb + 1) * all + at] = vb;
+                }
+            }
+}
+
+// dC and dB from the sums of the blocks of heads.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void scan_heads_kernel(int64_t all, int hblocks,
+                                                              const float *__restrict__ hsum,
+                                                              T *__restrict__ dB, T *__restrict__ dC)
+{
+    const int64_t e = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    if (e >= all) return;
+    float c = 0.f, b = 0.f;
+    for (int k = 0; k < hblocks; k++) {
+        c += hsum[(2 * k) * all + e];
+        b += hsum[(2 * k + 1) * all + e];
+    }
+    dC[e] = (T)c;
+    dB[e] = (T)b;
+}
+
+// dA, dD and ddt_bias of a head: the sum over sequences and chunks.
+__global__ __launch_bounds__(kThreads) void scan_params_kernel(int64_t rows, int H,
+                                                               const float *__restrict__ parts,
+                                                               float *dA, float *dD, float *dbias)
+{
+    __shared__ double sums[kThreads];
+    const int h = blockIdx.x, which = blockIdx.y;
+    float *out = which == 0 ? dA : which == 1 ? dD : dbias;
+    if (!out) return;
+    double s = 0.0;
+    for (int64_t r = threadIdx.x; r < rows; r += kThreads) s += (double)parts[(r * H + h) * 3 + which];
+    sums[threadIdx.x] = s;
+    for (int n = kThreads / 2; n > 0; n >>= 1) {
+        __syncthreads();
+        if ((int)threadIdx.x < n) sums[threadIdx.x] += sums[threadIdx.x + n];
+    }
+    if (threadIdx.x == 0) out[h] = (float)sums[0];
+}
+
+// -------------------------------------------------------------------- host
+
+struct Plan {
+    ScanDims d;
+    int hblocks;
+    size_t delta, cs, own, start, S, G, parts, hsum, total;
+};
+
+constexpr int64_t kUnits = 512;  // workgroups that fill the 256 compute units twice
+
+Plan plan_of(const sdm_scan_desc &s, bool backward)
+{
+    Plan p = {};
+    ScanDims &d = p.d;
+    d.B = s.B;
+    d.H = s.H;
+    d.P = s.P;
+    d.N = s.N;
+    d.G = s.G;
+    d.T = s.T;
+    d.nc = (int)((s.T + Q - 1) / Q);
+    d.nps = (s.P + kSlice - 1) / kSlice;
+    // Few chains: the time axis is split into segments of at least 8 chunks,
+    // which first run for their states alone.
+    const int64_t units = (int64_t)s.B * s.H * d.nps;
+    int64_t seg = units >= kUnits / 2 ? 1 : (kUnits + units - 1) / units;
+    if (seg > d.nc / 8) seg = d.nc / 8;
+    if (seg < 1) seg = 1;
+    d.cps = (int)((d.nc + seg - 1) / seg);
+    d.nseg = (d.nc + d.cps - 1) / d.cps;
+    d.xb = s.x_batch;
+    d.xt = s.x_token;
+    d.bb = s.B_batch;
+    d.bt = s.B_token;
+    d.cb = s.C_batch;
+    d.ct = s.C_token;
+    const int64_t grads = (int64_t)s.B * d.nc * s.G;
+    int64_t hb = grads >= kUnits ? 1 : (kUnits + grads - 1) / grads;
+    if (hb > s.H / s.G) hb = s.H / s.G;
+    p.hblocks = (int)hb;
+
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        const size_t here = at;
+        at += (bytes + 255) & ~(size_t)255;
+        return here;
+    };
+    const size_t bh = (size_t)s.B * s.H, PN = (size_t)s.P * s.N;
+    p.delta = take(bh * d.nc * Q * 4);
+    p.cs = take(bh * d.nc * Q * 8);
+    if (d.nseg > 1) {
+        p.own = take(bh * d.nseg * PN * 4);
+        p.start = take(bh * d.nseg * PN * 4);
+    }
+    if (backward) {
+        p.S = take(bh * d.nc * PN * 4);
+        p.G = take(bh * d.nc * PN * 4);
+        p.parts = take((size_t)s.B * d.nc * s.H * 3 * 4);
+        if (p.hblocks > 1) p.hsum = take((size_t)p.hblocks * 2 * s.B * s.T * s.G * s.N * 4);
+    }
+    p.total = at;
+    return p;
+}
+
+template <typename T>
+void run_prep(const ScanArgs &a, const Plan &p, float *delta, float2 *cs, hipStream_t stream)
+{
+    const int64_t waves = (int64_t)p.d.B * p.d.nc * p.d.H;
+    scan_prep_kernel<T><<<(unsigned)((waves + 3) / 4), dim3(64, 4), 0, stream>>>(
+        p.d, (const T *)a.dt, a.A, a.dt_bias, a.lengths, a.d.softplus, delta, cs);
+}
+
+// With more than one segment: the state before each (in `start`).
+template <typename T, int NT, bool REV>
+void run_segments(const ScanArgs &a, const Plan &p, const T *U, int64_t ub, int64_t ut, const T *V,
+                  int64_t vb, int64_t vt, const float *first, const float *delta, const float2 *cs,
+                  hipStream_t stream)
+{
+    const ScanDims &d = p.d;
+    const unsigned grid = (unsigned)((int64_t)d.B * d.H * d.nps * d.nseg);
+    float *own = (float *)(a.ws + p.own), *start = (float *)(a.ws + p.start);
+    scan_state_kernel<T, NT, REV><<<grid, kThreads, 0, stream>>>(
+        d, U, ub, ut, V, vb, vt, delta, cs, a.lengths, nullptr, 0, nullptr, own, 0);
+    scan_join_kernel<REV><<<dim3((d.P * d.N + kThreads - 1) / kThreads, d.B * d.H), kThreads, 0, stream>>>(
+        d, cs, first, own, start);
+}
+
+template <typename T, int NT>
+hipError_t forward(const ScanArgs &a, hipStream_t stream)
+{
+    const Plan p = plan_of(a.d, false);
+    const ScanDims &d = p.d;
+    float *delta = (float *)(a.ws + p.delta);
+    float2 *cs = (float2 *)(a.ws + p.cs);
+    run_prep<T>(a, p, delta, cs, stream);
+    const T *x = (const T *)a.x, *Bm = (const T *)a.Bm, *Cm = (const T *)a.Cm;
+    const float *init = a.cont ? a.state : nullptr;
+    int api = 1;
+    if (d.nseg > 1) {
+        run_segments<T, NT, false>(a, p, x, d.xb, d.xt, Bm, d.bb, d.bt, init, delta, cs, stream);
+        init = (const float *)(a.ws + p.start);
+        api = 0;
+    }
+    scan_walk_kernel<T, NT><<<(unsigned)((int64_t)d.B * d.H * d.nps * d.nseg), kThreads, 0, stream>>>(
+        d, x, Bm, Cm, a.D, delta, cs, a.lengths, init, api, a.state, (T *)a.y);
+    return hipGetLastError();
+}
+
+template <typename T, int NT>
+hipError_t backward(const ScanArgs &a, hipStream_t stream)
+{
+    const Plan p = plan_of(a.d, true);
+    const ScanDims &d = p.d;
+    float *delta = (float *)(a.ws + p.delta);
+    float2 *cs = (float2 *)(a.ws + p.cs);
+    float *S = (float *)(a.ws + p.S), *G = (float *)(a.ws + p.G);
+    float *parts = (float *)(a.ws + p.parts), *hsum = (float *)(a.ws + p.hsum);
+    const float *start = (const float *)(a.ws + p.start);
+    const unsigned grid = (unsigned)((int64_t)d.B * d.H * d.nps * d.nseg);
+    const T *x = (const T *)a.x, *Bm = (const T *)a.Bm, *Cm = (const T *)a.Cm, *dy = (const T *)a.dy;
+    const int64_t yt = (int64_t)d.H * d.P, yb = d.T * yt;
+    run_prep<T>(a, p, delta, cs, stream);
+    const bool split = d.nseg > 1;
+    if (split)
+        run_segments<T, NT, false>(a, p, x, d.xb, d.xt, Bm, d.bb, d.bt, a.state0, delta, cs, stream);
+    scan_state_kernel<T, NT, false><<<grid, kThreads, 0, stream>>>(
+        d, x, d.xb, d.xt, Bm, d.bb, d.bt, delta, cs, a.lengths, split ? start : a.state0,
+        split ? 0 : 1, S, nullptr, 0);
+    if (split)
+        run_segments<T, NT, true>(a, p, dy, yb, yt, Cm, d.cb, d.ct, a.dstateT, delta, cs, stream);
+    scan_state_kernel<T, NT, true><<<grid, kThreads, 0, stream>>>(
+        d, dy, yb, yt, Cm, d.cb, d.ct, delta, cs, a.lengths, split ? start : a.dstateT, split ? 0 : 1,
+        G, a.dstate0, 1);
+    scan_grad_kernel<T, NT><<<(unsigned)((int64_t)d.B * d.nc * d.G * p.hblocks), kThreads, 0, stream>>>(
+        d, p.hblocks, x, dy, Bm, Cm, a.A, a.D, delta, cs, a.lengths, a.d.softplus, S, G, (T *)a.dx,
+        (T *)a.ddt, (T *)a.dB, (T *)a.dC, parts, hsum);
+    if (p.hblocks > 1) {
+        const int64_t all = (int64_t)d.B * d.T * d.G * d.N;
+        scan_heads_kernel<T><<<(unsigned)((all + kThreads - 1) / kThreads), kThreads, 0, stream>>>(
+            all, p.hblocks, hsum, (T *)a.dB, (T *)a.dC);
+    }
+    scan_params_kernel<<<dim3(d.H, 3), kThreads, 0, stream>>>((int64_t)d.B * d.nc, d.H, parts, a.dA,
+                                                            a.dD, a.ddt_bias);
+    return hipGetLastError();
+}
+
+template <typename T>
+hipError_t dispatch(const ScanArgs &a, bool back, hipStream_t stream)
+{
+    // the state's columns, padded to 32, 64 or 128
+    if (a.d.N <= 32) return back ? backward<T, 2>(a, stream) : forward<T, 2>(a, stream);
+    if (a.d.N <= 64) return back ? backward<T, 4>(a, stream) : forward<T, 4>(a, stream);
+    return back ? backward<T, 8>(a, stream) : forward<T, 8>(a, stream);
+}
+
+}  // namespace
+
+size_t scan_forward_ws(const sdm_scan_desc &d) { return plan_of(d, false).total; }
+size_t scan_backward_ws(const sdm_scan_desc &d) { return plan_of(d, true).total; }
+
+hipError_t launch_scan_forward(const ScanArgs &a, hipStream_t stream)
+{
+    return a.d.dtype == SDM_F32 ? dispatch<float>(a, false, stream) : dispatch<bf16>(a, false, stream);
+}
+
+hipError_t launch_scan_backward(const ScanArgs &a, hipStream_t stream)
+{
+    return a.d.dtype == SDM_F32 ? dispatch<float>(a, true, stream) : dispatch<bf16>(a, true, stream);
+}
+
+}  // namespace sdm

@@ -1,6 +1,6 @@
-"""Sequence mixers beside the SDM core: CausalConv.
+"""Sequence mixers beside the SDM core: CausalConv and SelectiveScan.
 
-Bindings of the sdm_conv_* calls of include/sdm.h.
+Bindings of the sdm_conv_* and sdm_scan_* calls of include/sdm.h.
 Like SDM, each class borrows its parameters, runs on the current stream of its
 inputs' device, raises SDMError for what the library refuses, and has no
 fallback.  Inputs may be views with any batch and token strides; outputs are
@@ -167,4 +167,122 @@ class CausalConv:
                 ctypes.byref(d), _p(x), _p(self.weight), _p(self.bias), _p(lengths), _p(dy),
                 _p(state), _p(dstate), _p(workspace), workspace.numel(), _p(out["dx"]),
                 _p(out["dweight"]), _p(out.get("dbias")), _p(out.get("dstate")), stream))
+        return out
+
+
+class _ScanDesc(ctypes.Structure):
+    _fields_ = [("B", c_int), ("T", c_int64), ("H", c_int), ("P", c_int), ("N", c_int),
+                ("G", c_int), ("softplus", c_int), ("dtype", c_int), ("x_batch", c_int64),
+                ("x_token", c_int64), ("B_batch", c_int64), ("B_token", c_int64),
+                ("C_batch", c_int64), ("C_token", c_int64)]
+
+
+class SelectiveScan:
+    """Selective state space scan with one decay per head and token.
+
+        S_t = exp(D_t A) S_{t-1} + D_t x_t B_t^T,   y_t = S_t C_t + D x_t,
+        D_t = softplus(dt_t + dt_bias)  (softplus=False: dt_t + dt_bias)
+
+    A [H], and D, dt_bias [H] or None, are float32 GPU tensors, borrowed.
+    """
+
+    def __init__(self, A, D=None, dt_bias=None, softplus: bool = True):
+        _dev_tensor(A, "A", _F32)
+        if A.dim() != 1:
+            raise SDMError(1, "A must be [H]")
+        self.H = A.shape[0]
+        for t, name in ((D, "D"), (dt_bias, "dt_bias")):
+            if t is not None:
+                _param(t, name, (self.H,), A.device)
+        self.A, self.D, self.dt_bias, self.softplus = A, D, dt_bias, bool(softplus)
+
+    def _desc(self, x, dt, Bm, Cm):
+        if not isinstance(x, torch.Tensor) or x.dim() != 4 or x.shape[2] != self.H:
+            raise SDMError(1, f"x must be [B, T, {self.H}, P]")
+        if not isinstance(Bm, torch.Tensor) or Bm.dim() != 4:
+            raise SDMError(1, "Bm must be [B, T, G, N]")
+        B, T, H, P = x.shape
+        G, N = Bm.shape[2:]
+        _view(x, "x", x, (B, T, H, P), 2)
+        _view(Bm, "Bm", x, (B, T, G, N), 2)
+        _view(Cm, "Cm", x, (B, T, G, N), 2)
+        _out_tensor(dt, "dt", (B, T, H), x.dtype, x)
+        _same_device(self.A, x, "A")
+        return _ScanDesc(B, T, H, P, N, G, int(self.softplus), _dtype(x, "x"), x.stride(0),
+                         x.stride(1), Bm.stride(0), Bm.stride(1), Cm.stride(0), Cm.stride(1))
+
+    @staticmethod
+    def _need(call, d) -> int:
+        n = ctypes.c_size_t()
+        _check(call(ctypes.byref(d), ctypes.byref(n)))
+        return n.value
+
+    def workspace_size(self, x, dt, Bm, Cm) -> int:
+        """Bytes of workspace forward needs for inputs like these."""
+        return self._need(lib().sdm_scan_workspace_size, self._desc(x, dt, Bm, Cm))
+
+    def backward_workspace_size(self, x, dt, Bm, Cm) -> int:
+        """Bytes of workspace backward needs for inputs like these."""
+        return self._need(lib().sdm_scan_backward_workspace_size, self._desc(x, dt, Bm, Cm))
+
+    def forward(self, x, dt, Bm, Cm, state=None, cont: bool = False, lengths=None, y=None,
+                workspace=None):
+        """(y, state): y [B, T, H, P] and the last state [B, H, P, N] (float32).
+
+        x [B, T, H, P], dt [B, T, H], Bm and Cm [B, T, G, N].  With cont=True
+        the scan starts from `state`, which is updated in place; otherwise from
+        zero (a given `state` is overwritten).  lengths [B] int32: tokens of
+        each sequence.
+        """
+        d = self._desc(x, dt, Bm, Cm)
+        shape = (d.B, d.H, d.P, d.N)
+        if state is None:
+            if cont:
+                raise SDMError(1, "cont=True needs the state")
+            state = torch.empty(shape, dtype=_F32, device=x.device)
+        else:
+            _out_tensor(state, "state", shape, _F32, x)
+        if y is None:
+            y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        else:
+            _out_tensor(y, "y", x.shape, x.dtype, x)
+        _lengths(lengths, d.B, x)
+        workspace = _workspace(workspace, self._need(lib().sdm_scan_workspace_size, d), x)
+        with _On(x.device) as stream:
+            _check(lib().sdm_scan_forward(
+                ctypes.byref(d), _p(x), _p(dt), _p(Bm), _p(Cm), _p(self.A), _p(self.D),
+                _p(self.dt_bias), _p(lengths), FLAG_CONTINUE if cont else 0, _p(workspace),
+                workspace.numel(), _p(y), _p(state), stream))
+        return y, state
+
+    def backward(self, x, dt, Bm, Cm, dy, state=None, dstate=None, lengths=None,
+                 workspace=None) -> dict:
+        """Gradients for dy [B, T, H, P] (and dstate, that of the final state,
+        or None for zero): dx, ddt, dB, dC, float32 dA, dD and ddt_bias (where
+        given), and, for a forward that started from `state`, dstate."""
+        d = self._desc(x, dt, Bm, Cm)
+        shape = (d.B, d.H, d.P, d.N)
+        _out_tensor(dy, "dy", x.shape, x.dtype, x)
+        for t, name in ((state, "state"), (dstate, "dstate")):
+            if t is not None:
+                _out_tensor(t, name, shape, _F32, x)
+        _lengths(lengths, d.B, x)
+        workspace = _workspace(workspace, self._need(lib().sdm_scan_backward_workspace_size, d), x)
+        new = dict(dtype=x.dtype, device=x.device)
+        out = dict(dx=torch.empty(x.shape, **new), ddt=torch.empty(dt.shape, **new),
+                   dB=torch.empty(Bm.shape, **new), dC=torch.empty(Cm.shape, **new),
+                   dA=torch.empty_like(self.A))
+        if self.D is not None:
+            out["dD"] = torch.empty_like(self.D)
+        if self.dt_bias is not None:
+            out["ddt_bias"] = torch.empty_like(self.dt_bias)
+        if state is not None:
+            out["dstate"] = torch.empty(shape, dtype=_F32, device=x.device)
+        with _On(x.device) as stream:
+            _check(lib().sdm_scan_backward(
+                ctypes.byref(d), _p(x), _p(dt), _p(Bm), _p(Cm), _p(self.A), _p(self.D),
+                _p(self.dt_bias), _p(lengths), _p(dy), _p(state), _p(dstate), _p(workspace),
+                workspace.numel(), _p(out["dx"]), _p(out["ddt"]), _p(out["dB"]), _p(out["dC"]),
+                _p(out["dA"]), _p(out.get("dD")), _p(out.get("ddt_bias")), _p(out.get("dstate")),
+                stream))
         return out

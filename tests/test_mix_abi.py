@@ -67,3 +67,67 @@ def test_conv_backward_refusals():
         assert call(**{name: None}) == 1, name
     for name in ("dy", "ws", "dx", "dweight", "bias", "state", "dstateT", "dbias", "dstate"):
         assert call(**{name: FAKE + 4}) == 1, name
+
+
+def scan_desc(**kw):
+    d = dict(B=2, T=100, H=4, P=16, N=8, G=2, softplus=1, dtype=sdm.BF16, x_batch=6400, x_token=64,
+             B_batch=1600, B_token=16, C_batch=1600, C_token=16)
+    d.update(kw)
+    return mixers._ScanDesc(**d)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(B=0), 1), (dict(T=0), 1), (dict(H=0), 1), (dict(P=0), 1), (dict(N=0), 1), (dict(G=0), 1),
+    (dict(G=3), 1), (dict(softplus=2), 1), (dict(dtype=2), 1), (dict(x_token=-1), 1),
+    (dict(B_batch=-1), 1), (dict(C_token=-1), 1), (dict(N=129), 2), (dict(P=65537), 2),
+    (dict(B=65536, H=1, G=1), 2), (dict(T=1 << 31), 2), (dict(T=1 << 30), 2),
+])
+def test_scan_descriptor_refusals(kw, status):
+    L, n = sdm.lib(), ctypes.c_size_t()
+    d = ctypes.byref(scan_desc(**kw))
+    assert L.sdm_scan_workspace_size(d, ctypes.byref(n)) == status and n.value == 0
+    assert L.sdm_scan_backward_workspace_size(d, ctypes.byref(n)) == status
+    assert L.sdm_scan_forward(d, *[FAKE] * 8, 0, FAKE, 1 << 40, FAKE, FAKE, None) == status
+    assert L.sdm_scan_backward(d, *[FAKE] * 12, 1 << 40, *[FAKE] * 8, None) == status
+    assert L.sdm_last_error()
+
+
+def test_scan_pointer_refusals():
+    L, n = sdm.lib(), ctypes.c_size_t()
+    d = ctypes.byref(scan_desc())
+    assert L.sdm_scan_workspace_size(d, None) == 1
+    assert L.sdm_scan_workspace_size(None, ctypes.byref(n)) == 1
+    assert L.sdm_scan_workspace_size(d, ctypes.byref(n)) == 0 and n.value > 0
+    # forward: x dt Bm Cm A D bias lengths | flags ws bytes | y state
+    need = n.value
+
+    def fwd(at=None, value=None, flags=0, ws=FAKE, size=need, y=FAKE, state=FAKE):
+        p = [FAKE] * 8
+        if at is not None:
+            p[at] = value
+        return L.sdm_scan_forward(d, *p, flags, ws, size, y, state, None)
+
+    for at in (0, 1, 2, 3, 4):
+        assert fwd(at, None) == 1, at
+    for at in (0, 2, 3):
+        assert fwd(at, FAKE + 1) == 1, at
+    for at in (1, 4, 5, 6):
+        assert fwd(at, FAKE + 4) == 1, at
+    assert fwd(7, FAKE + 2) == 1
+    assert fwd(flags=8) == 1 and fwd(ws=None) == 1 and fwd(ws=FAKE + 8) == 1
+    assert fwd(size=need - 1) == 3 and fwd(y=None) == 1 and fwd(state=FAKE + 4) == 1
+    assert L.sdm_scan_backward_workspace_size(d, ctypes.byref(n)) == 0 and n.value > need
+    # backward: x dt Bm Cm A D bias lengths dy state dstateT ws | bytes | 8 outputs
+    for at in (0, 1, 2, 3, 4, 8, 11):
+        p = [FAKE] * 12
+        p[at] = None
+        assert L.sdm_scan_backward(d, *p, n.value, *[FAKE] * 8, None) == 1, at
+    for at in range(5):  # dx ddt dB dC dA
+        q = [FAKE] * 8
+        q[at] = None
+        assert L.sdm_scan_backward(d, *[FAKE] * 12, n.value, *q, None) == 1, at
+    for at in range(8):
+        q = [FAKE] * 8
+        q[at] = FAKE + 4
+        assert L.sdm_scan_backward(d, *[FAKE] * 12, n.value, *q, None) == 1, at
+    assert L.sdm_scan_backward(d, *[FAKE] * 12, n.value - 1, *[FAKE] * 8, None) == 3
