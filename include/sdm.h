@@ -466,6 +466,66 @@ sdm_status sdm_scan_backward(const sdm_scan_desc *d, const void *x, const void *
                              size_t ws_bytes, void *dx, void *ddt, void *dB, void *dC, float *dA,
                              float *dD, float *ddt_bias, float *dstate, void *stream);
 
+/*
+ * Causal attention with a sliding window and sinks, the first tokens of a
+ * sequence that stay visible: the query at position i sees the key at j where
+ * j <= i and (i - j < window or j < sinks).  Hq / Hk neighbouring query heads
+ * share a key head.
+ *   s_ij = scale * q_i.k_j;  lse_i = log sum_j exp(s_ij);
+ *   o_i = sum_j exp(s_ij - lse_i) v_j   over the keys that i sees.
+ *
+ * Rolling cache.  A stream needs its sinks and its last `window` tokens:
+ * cache_k, cache_v hold sinks + window rows per sequence, the token at
+ * position p in row p (p < sinks) or sinks + (p - sinks) % window.
+ * Limits: 1 <= D <= 256, Hk divides Hq, 1 <= window < 2^31, 0 <= sinks <= 1024;
+ * B * Hq * ceil(T / 64) and B * (min(sinks, T) + min(window, T)) < 2^31.
+ */
+typedef struct {
+    int B;
+    int64_t T;
+    int Hq, Hk, D;
+    int64_t window;
+    int sinks;
+    float scale;              /* usually 1 / sqrt(D) */
+    sdm_dtype dtype;          /* SDM_F32 or SDM_BF16 */
+    int64_t q_batch, q_token, q_head; /* strides; the columns are dense */
+    int64_t k_batch, k_token, k_head;
+    int64_t v_batch, v_token, v_head;
+} sdm_window_desc;
+
+/*
+ *   q        device [B][T][Hq][D] (strided);  k, v  device [B][T][Hk][D] (strided)
+ *   flags    SDM_FLAG_CONTINUE: sequence b already holds pos[b] tokens in the
+ *            cache, and the call's tokens follow them
+ *   cache_k, cache_v  device [B][sinks + window][Hk][D], updated in place with
+ *            the call's tokens, or both NULL (not with SDM_FLAG_CONTINUE).
+ *            Rows of tokens that have not come are not read.
+ *   pos      device [B] int64 (negative values act as 0): with the flag only,
+ *            else NULL.  Not updated.
+ *   workspace  >= sdm_window_workspace_size bytes, 16-byte aligned
+ *   o        device [B][T][Hq][D];  lse  device [B][T][Hq] float32
+ * T = 1 with the flag is a decode step.
+ */
+sdm_status sdm_window_workspace_size(const sdm_window_desc *d, unsigned flags, size_t *bytes);
+
+sdm_status sdm_window_forward(const sdm_window_desc *d, const void *q, const void *k,
+                              const void *v, const int32_t *lengths, unsigned flags,
+                              void *cache_k, void *cache_v, const int64_t *pos, void *workspace,
+                              size_t ws_bytes, void *o, float *lse, void *stream);
+
+/*
+ * Gradients for dout [B][T][Hq][D], of a forward without a cache.
+ *   o, lse   what the forward returned
+ *   workspace  >= sdm_window_backward_workspace_size bytes, 16-byte aligned
+ * Outputs: dq [B][T][Hq][D]; dk, dv [B][T][Hk][D].
+ */
+sdm_status sdm_window_backward_workspace_size(const sdm_window_desc *d, size_t *bytes);
+
+sdm_status sdm_window_backward(const sdm_window_desc *d, const void *q, const void *k,
+                               const void *v, const void *o, const float *lse, const void *dout,
+                               const int32_t *lengths, void *workspace, size_t ws_bytes, void *dq,
+                               void *dk, void *dv, void *stream);
+
 /* Static description of a status code. */
 const char *sdm_status_string(sdm_status s);
 

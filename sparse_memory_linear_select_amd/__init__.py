@@ -21,7 +21,7 @@ import torch
 
 __all__ = ["SDM", "SDMError", "lib", "lib_path", "F32", "BF16", "FP8_E4M3", "AUTO", "SERIAL", "TIMEPAR",
            "FLAG_CONTINUE", "EXPORTS", "NOALLOC_MAX_BYTES", "CausalConv",
-           "SelectiveScan"]
+           "SelectiveScan", "WindowAttention"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libsdm.so")
@@ -40,7 +40,8 @@ EXPORTS = ("sdm_backward", "sdm_backward_workspace_size", "sdm_backward_workspac
            "sdm_forward_noalloc", "sdm_prepare", "sdm_apply", "sdm_write_histogram",
            "sdm_conv_forward", "sdm_conv_backward", "sdm_conv_backward_workspace_size",
            "sdm_scan_forward", "sdm_scan_backward", "sdm_scan_workspace_size",
-           "sdm_scan_backward_workspace_size",
+           "sdm_scan_backward_workspace_size", "sdm_window_forward", "sdm_window_backward",
+           "sdm_window_workspace_size", "sdm_window_backward_workspace_size",
            "sdm_status_string", "sdm_last_error")
 NOALLOC_MAX_BYTES = 64 << 20  # SDM_NOALLOC_MAX_BYTES: the static scratch of sdm_forward_noalloc
 
@@ -86,6 +87,10 @@ def lib():
         L.sdm_scan_forward.argtypes = [p] * 9 + [ctypes.c_uint, p, sz, p, p, p]
         L.sdm_scan_backward_workspace_size.argtypes = [p, ctypes.POINTER(sz)]
         L.sdm_scan_backward.argtypes = [p] * 13 + [sz] + [p] * 9
+        L.sdm_window_workspace_size.argtypes = [p, ctypes.c_uint, ctypes.POINTER(sz)]
+        L.sdm_window_forward.argtypes = [p] * 5 + [ctypes.c_uint, p, p, p, p, sz, p, p, p]
+        L.sdm_window_backward_workspace_size.argtypes = [p, ctypes.POINTER(sz)]
+        L.sdm_window_backward.argtypes = [p] * 9 + [sz, p, p, p, p]
         for f in EXPORTS[:-2]:
             getattr(L, f).restype = ctypes.c_int
         L.sdm_status_string.argtypes = [i]
@@ -386,4 +391,4 @@ class SDM:
         return y, M
 
 
-from .mixers import CausalConv, SelectiveScan  # noqa: E402  (uses the helpers above)
+from .mixers import CausalConv, SelectiveScan, WindowAttention  # noqa: E402  (uses the helpers above)

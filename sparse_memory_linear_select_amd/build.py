@@ -24,6 +24,7 @@ LIB = os.path.join(PKG, "libsdm.so")
 
 SOURCES = ["select.hip", "init.hip", "plan.hip", "rw_serial.hip", "rw_timepar.hip", "decode.hip",
            "backward.hip", "causal_conv.hip", "selective_scan.hip",
+           "window_attn.hip",
            "sdm_api.cpp", "mix_api.cpp"]
 
 HIPCC = os.environ.get("HIPCC", "hipcc")

@@ -2,6 +2,8 @@
 // check happens before the first HIP call; see include/sdm.h for the contract.
 #include "mix_internal.h"
 
+#include <math.h>
+
 namespace {
 
 using sdm::set_error;
@@ -121,6 +123,36 @@ sdm_status check_scan_inputs(const sdm_scan_desc *d, const void *x, const void *
     CHECK(check_dense(D, "D", false));
     CHECK(check_dense(dt_bias, "dt_bias", false));
     return check_lengths(lengths);
+}
+
+// --------------------------------------------------------------- attention
+
+sdm_status check_window(const sdm_window_desc *d)
+{
+    if (!d) return set_error(SDM_ERR_ARG, "null descriptor");
+    CHECK(check_batch(d->B, d->T, d->dtype));
+    if (d->Hq < 1 || d->Hk < 1 || d->D < 1)
+        return set_error(SDM_ERR_ARG, "Hq, Hk, D must be >= 1 (got %d %d %d)", d->Hq, d->Hk, d->D);
+    if (d->Hq % d->Hk)
+        return set_error(SDM_ERR_ARG, "Hk = %d must divide Hq = %d", d->Hk, d->Hq);
+    if (d->window < 1) return set_error(SDM_ERR_ARG, "window must be >= 1 (got %lld)", (long long)d->window);
+    if (d->sinks < 0) return set_error(SDM_ERR_ARG, "sinks must be >= 0 (got %d)", d->sinks);
+    if (!isfinite(d->scale)) return set_error(SDM_ERR_ARG, "scale must be finite");
+    if (d->q_batch < 0 || d->q_token < 0 || d->q_head < 0 || d->k_batch < 0 || d->k_token < 0 ||
+        d->k_head < 0 || d->v_batch < 0 || d->v_token < 0 || d->v_head < 0)
+        return set_error(SDM_ERR_ARG, "strides must be >= 0");
+    if (d->D > 256) return set_error(SDM_ERR_UNSUPPORTED, "D <= 256 is supported (got %d)", d->D);
+    if (d->sinks > 1024)
+        return set_error(SDM_ERR_UNSUPPORTED, "sinks <= 1024 is supported (got %d)", d->sinks);
+    if (d->window >= (int64_t)1 << 31)
+        return set_error(SDM_ERR_UNSUPPORTED, "window must be < 2^31");
+    const double rows = (double)(d->sinks < d->T ? d->sinks : d->T) +
+                        (double)(d->window < d->T ? d->window : d->T);
+    if ((double)d->B * d->Hq * (double)((d->T + 63) / 64) >= 2147483648.0 ||
+        (double)d->B * rows >= 2147483648.0)
+        return set_error(SDM_ERR_UNSUPPORTED,
+                         "B*Hq*ceil(T/64) and B*(min(sinks, T) + min(window, T)) must be < 2^31");
+    return SDM_OK;
 }
 
 }  // namespace
@@ -290,6 +322,96 @@ sdm_status sdm_scan_backward(const sdm_scan_desc *d, const void *x, const void *
     a.ws = (unsigned char *)workspace;
     const hipError_t e = sdm::launch_scan_backward(a, (hipStream_t)stream);
     return e == hipSuccess ? SDM_OK : hip_fail(e, "scan backward launch");
+}
+
+sdm_status sdm_window_workspace_size(const sdm_window_desc *d, unsigned flags, size_t *bytes)
+{
+    if (!bytes) return set_error(SDM_ERR_ARG, "null bytes pointer");
+    *bytes = 0;
+    CHECK(check_window(d));
+    if (flags & ~SDM_FLAG_CONTINUE) return set_error(SDM_ERR_ARG, "unknown flags 0x%x", flags);
+    *bytes = sdm::window_forward_ws(*d, flags & SDM_FLAG_CONTINUE);
+    return SDM_OK;
+}
+
+sdm_status sdm_window_forward(const sdm_window_desc *d, const void *q, const void *k,
+                              const void *v, const int32_t *lengths, unsigned flags,
+                              void *cache_k, void *cache_v, const int64_t *pos, void *workspace,
+                              size_t ws_bytes, void *o, float *lse, void *stream)
+{
+    CHECK(check_window(d));
+    if (flags & ~SDM_FLAG_CONTINUE) return set_error(SDM_ERR_ARG, "unknown flags 0x%x", flags);
+    const bool cont = flags & SDM_FLAG_CONTINUE;
+    CHECK(check_strided(q, "q", d->dtype));
+    CHECK(check_strided(k, "k", d->dtype));
+    CHECK(check_strided(v, "v", d->dtype));
+    CHECK(check_lengths(lengths));
+    CHECK(check_dense(cache_k, "cache_k", cont));
+    CHECK(check_dense(cache_v, "cache_v", cont));
+    if (!cache_k != !cache_v) return set_error(SDM_ERR_ARG, "cache_k and cache_v come together");
+    if (cont && !pos) return set_error(SDM_ERR_ARG, "SDM_FLAG_CONTINUE needs pos");
+    if (!cont && pos) return set_error(SDM_ERR_ARG, "pos needs SDM_FLAG_CONTINUE");
+    if ((uintptr_t)pos & 7u) return set_error(SDM_ERR_ARG, "pos must be 8-byte aligned");
+    CHECK(check_dense(o, "o"));
+    CHECK(check_dense(lse, "lse"));
+    CHECK(check_workspace(workspace, ws_bytes, sdm::window_forward_ws(*d, cont)));
+    sdm::WindowArgs a = {};
+    a.d = *d;
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.lengths = lengths;
+    a.pos = pos;
+    a.cache_k = cache_k;
+    a.cache_v = cache_v;
+    a.o = o;
+    a.lse = lse;
+    a.ws = (unsigned char *)workspace;
+    const hipError_t e = sdm::launch_window_forward(a, (hipStream_t)stream);
+    return e == hipSuccess ? SDM_OK : hip_fail(e, "attention launch");
+}
+
+sdm_status sdm_window_backward_workspace_size(const sdm_window_desc *d, size_t *bytes)
+{
+    if (!bytes) return set_error(SDM_ERR_ARG, "null bytes pointer");
+    *bytes = 0;
+    CHECK(check_window(d));
+    *bytes = sdm::window_backward_ws(*d);
+    return SDM_OK;
+}
+
+sdm_status sdm_window_backward(const sdm_window_desc *d, const void *q, const void *k,
+                               const void *v, const void *o, const float *lse, const void *dout,
+                               const int32_t *lengths, void *workspace, size_t ws_bytes, void *dq,
+                               void *dk, void *dv, void *stream)
+{
+    CHECK(check_window(d));
+    CHECK(check_strided(q, "q", d->dtype));
+    CHECK(check_strided(k, "k", d->dtype));
+    CHECK(check_strided(v, "v", d->dtype));
+    CHECK(check_dense(o, "o"));
+    CHECK(check_dense(lse, "lse"));
+    CHECK(check_dense(dout, "dout"));
+    CHECK(check_lengths(lengths));
+    CHECK(check_dense(dq, "dq"));
+    CHECK(check_dense(dk, "dk"));
+    CHECK(check_dense(dv, "dv"));
+    CHECK(check_workspace(workspace, ws_bytes, sdm::window_backward_ws(*d)));
+    sdm::WindowArgs a = {};
+    a.d = *d;
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.oin = o;
+    a.lse_in = lse;
+    a.dout = dout;
+    a.lengths = lengths;
+    a.dq = dq;
+    a.dk = dk;
+    a.dv = dv;
+    a.ws = (unsigned char *)workspace;
+    const hipError_t e = sdm::launch_window_backward(a, (hipStream_t)stream);
+    return e == hipSuccess ? SDM_OK : hip_fail(e, "attention backward launch");
 }
 
 }  // extern "C"

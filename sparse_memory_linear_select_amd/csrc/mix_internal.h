@@ -50,4 +50,22 @@ size_t scan_backward_ws(const sdm_scan_desc &d);
 hipError_t launch_scan_forward(const ScanArgs &a, hipStream_t stream);
 hipError_t launch_scan_backward(const ScanArgs &a, hipStream_t stream);
 
+struct WindowArgs {
+    sdm_window_desc d;
+    const void *q, *k, *v;
+    const int32_t *lengths;
+    const int64_t *pos;             // tokens before this call, or null for none
+    void *cache_k, *cache_v;        // or null
+    void *o;
+    float *lse;
+    const void *oin, *dout;         // backward
+    const float *lse_in;
+    void *dq, *dk, *dv;
+    unsigned char *ws;
+};
+size_t window_forward_ws(const sdm_window_desc &d, bool cache);
+size_t window_backward_ws(const sdm_window_desc &d);
+hipError_t launch_window_forward(const WindowArgs &a, hipStream_t stream);
+hipError_t launch_window_backward(const WindowArgs &a, hipStream_t stream);
+
 }  // namespace sdm

@@ -1,0 +1,637 @@
+// Causal attention with a sliding window and sinks: query i sees key j where
+// j <= i and (i - j < window or j < sinks).  Hq / Hk query heads share a key
+// head.
+//
+// Scores are computed transposed, S^T = K Q^T, so that a lane holds one query
+// (column) and four neighbouring keys: the softmax of a query is a reduction
+// over registers and two lane exchanges, and P^T is already the right operand
+// of O^T += V^T P^T.  One pass over the keys with the running maximum m and
+// sum l of 2^{s - m}, s in units of log2.
+#include "mix_internal.h"
+
+#include "mix_device.h"
+
+namespace sdm {
+namespace {
+
+constexpr int kRows = 64;     // queries of a workgroup: 16 a wave
+constexpr int kKeys = 64;     // keys of a tile
+constexpr int kThreads = 256;
+constexpr int kSinkRows = 512;  // queries whose sink gradients one workgroup sums
+
+struct WinDims {
+    int B, Hq, Hk, D;
+    int64_t T, W;
+    int S;
+    float c2;                   // scale * log2 e
+    float scale;
+    int64_t qb, qt, qh, kb, kt, kh, vb, vt, vh;
+    int64_t cap;                // rows of the cache: S + W
+    int nq;                     // query tiles
+};
+
+// Tokens of sequence b before the call.
+__device__ __forceinline__ int64_t seq_pos(const int64_t *pos, int64_t b)
+{
+    return pos && pos[b] > 0 ? pos[b] : 0;
+}
+
+__device__ __forceinline__ int64_t cache_slot(int64_t p, int64_t S, int64_t W)
+{
+    return p < S ? p : S + (p - S) % W;
+}
+
+// Fills a 64-row tile: row r from row_of(r) (null: zeros).  D columns, padded
+// with zeros to COLS.
+template <typename T, int COLS, int LD, typename F>
+__device__ __forceinline__ void load_rows(T *tile, F row_of, int D, bool vec)
+{
+    constexpr int V = 16 / sizeof(T);
+    constexpr int PER = COLS / V;
+    for (int e = threadIdx.x; e < 64 * PER; e += kThreads) {
+        const int r = e / PER, c = (e % PER) * V;
+        const T *src = row_of(r);
+        Vec<T, V> v;
+        if (vec && src && c < D) {
+            v = vload<T, V>(src + c);
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; i++) v.e[i] = src && c + i < D ? src[c + i] : (T)0.f;
+        }
+        vstore<T, V>(tile + r * LD + c, v);
+    }
+}
+
+// Fragment of a row in global memory: 8 elements from k, zeros from D on.
+template <typename T>
+__device__ __forceinline__ typename Mat<T>::Frag frag_global(const T *src, int k, int D, bool vec)
+{
+    typename Mat<T>::Frag f;
+    if (src && vec && k < D) {
+        constexpr int V = 16 / sizeof(T);
+#pragma unroll
+        for (int u = 0; u < 8 / V; u++) {
+            const Vec<T, V> v = vload<T, V>(src + k + u * V);
+#pragma unroll
+            for (int i = 0; i < V; i++) f[u * V + i] = v.e[i];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; i++) f[i] = src && k + i < D ? src[k + i] : (T)0.f;
+    }
+    return f;
+}
+
+// Column fragment whose k order is that of two accumulator tiles: rows
+// k0 + 4 g .. + 3 and k0 + 16 + 4 g .. + 3.
+template <typename T>
+__device__ __forceinline__ typename Mat<T>::Frag frag_col_pair(const T *tile, int ld, int k0, int col0)
+{
+    const int l = threadIdx.x & 63;
+    const T *p = tile + (k0 + (l >> 4) * 4) * ld + col0 + (l & 15);
+    typename Mat<T>::Frag f;
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        f[i] = p[i * ld];
+        f[4 + i] = p[(16 + i) * ld];
+    }
+    return f;
+}
+
+template <typename T>
+__device__ __forceinline__ typename Mat<T>::Frag pair_frag(f32x4 a, f32x4 b)
+{
+    typename Mat<T>::Frag f;
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        f[i] = (T)a[i];
+        f[4 + i] = (T)b[i];
+    }
+    return f;
+}
+
+// The key tiles that queries [i0, i1] can see: first the sinks in front of
+// every window, then the keys from `lo` on.
+struct KeyRange {
+    int64_t lo, hi;      // keys lo .. hi
+    int64_t sink_end;    // sinks 0 .. sink_end - 1 in front of lo
+    int nsink, ntiles;
+    __device__ KeyRange(int64_t i0, int64_t i1, int64_t W, int64_t S)
+    {
+        lo = i0 - W + 1 > 0 ? i0 - W + 1 : 0;
+        hi = i1;
+        sink_end = S < lo ? S : lo;
+        nsink = (int)((sink_end + kKeys - 1) / kKeys);
+        ntiles = nsink + (int)((hi - lo + kKeys) / kKeys);
+    }
+    // first key of a tile and the end of its part
+    __device__ int64_t first(int n) const { return n < nsink ? (int64_t)n * kKeys : lo + (int64_t)(n - nsink) * kKeys; }
+    __device__ int64_t end(int n) const { return n < nsink ? sink_end : hi + 1; }
+};
+
+template <typename T, int DT>
+__global__ __launch_bounds__(kThreads) void window_fwd_kernel(
+    WinDims d, const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v,
+    const T *__restrict__ ck, const T *__restrict__ cv, const int64_t *__restrict__ pos,
+    const int32_t *__restrict__ lengths, bool vq, bool vk, T *__restrict__ o, float *__restrict__ lse)
+{
+    using M = Mat<T>;
+    constexpr int LD = DT * 16 + 8;
+    __shared__ __align__(32) T Ks[kKeys * LD];
+    __shared__ __align__(32) T Vs[kKeys * LD];
+
+    const int qt = blockIdx.x % d.nq;
+    const int64_t bh = blockIdx.x / d.nq;
+    const int h = (int)(bh % d.Hq);
+    const int64_t b = bh / d.Hq;
+    const int hk = h / (d.Hq / d.Hk);
+    const int64_t len = seq_len(lengths, b, d.T);
+    const int64_t p0 = seq_pos(pos, b);
+    const int64_t t0 = (int64_t)qt * kRows;
+    const int l = threadIdx.x & 63, w = threadIdx.x >> 6, g = l >> 4;
+    const int64_t t = t0 + 16 * w + (l & 15);     // the lane's query
+    T *op = o + ((b * d.T + t) * d.Hq + h) * d.D;
+    if (t0 >= len) {
+        if (t < d.T) {
+            for (int c = g; c < d.D; c += 4) op[c] = (T)0.f;
+            if (g == 0) lse[(b * d.T + t) * d.Hq + h] = 0.f;
+        }
+        return;
+    }
+    const int64_t i = p0 + t;
+    const bool live = t < len;
+    const T *qrow = live ? q + b * d.qb + t * d.qt + h * d.qh : nullptr;
+    typename M::Frag qf[DT / 2];
+#pragma unroll
+    for (int ks = 0; ks < DT / 2; ks++) qf[ks] = frag_global<T>(qrow, 32 * ks + 8 * g, d.D, vq);
+
+    f32x4 O[DT];
+#pragma unroll
+    for (int j = 0; j < DT; j++) O[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    float m = -INFINITY, sum = 0.f;
+    const int64_t last = (t0 + kRows < len ? t0 + kRows : len) - 1;
+    const KeyRange kr(p0 + t0, p0 + last, d.W, d.S);
+    const T *kn = k + b * d.kb + hk * d.kh, *vn = v + b * d.vb + hk * d.vh;
+    for (int n = 0; n < kr.ntiles; n++) {
+        const int64_t j0 = kr.first(n), jend = kr.end(n);
+        __syncthreads();
+        load_rows<T, DT * 16, LD>(Ks, [&](int r) -> const T * {
+            const int64_t j = j0 + r;
+            if (j >= jend) return nullptr;
+            return j >= p0 ? kn + (j - p0) * d.kt
+                           : ck + ((b * d.cap + cache_slot(j, d.S, d.W)) * d.Hk + hk) * d.D;
+        }, d.D, vk);
+        load_rows<T, DT * 16, LD>(Vs, [&](int r) -> const T * {
+            const int64_t j = j0 + r;
+            if (j >= jend) return nullptr;
+            return j >= p0 ? vn + (j - p0) * d.vt
+                           : cv + ((b * d.cap + cache_slot(j, d.S, d.W)) * d.Hk + hk) * d.D;
+        }, d.D, vk);
+        __syncthreads();
+        f32x4 s[4];
+        float top = -INFINITY;
+#pragma unroll
+        for (int kt = 0; kt < 4; kt++) {
+            s[kt] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int ks = 0; ks < DT / 2; ks++)
+                s[kt] = M::mma(frag_row<T>(Ks, LD, 16 * kt, 32 * ks), qf[ks], s[kt]);
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                const int64_t j = j0 + 16 * kt + 4 * g + e;
+                const bool see = j < jend && j <= i && (i - j < d.W || j < d.S);
+                s[kt][e] = see ? s[kt][e] * d.c2 : -INFINITY;
+                top = fmaxf(top, s[kt][e]);
+            }
+        }
+        top = fmaxf(top, __shfl_xor(top, 16));
+        top = fmaxf(top, __shfl_xor(top, 32));
+        const float mn = fmaxf(m, top);
+        const float base = mn == -INFINITY ? 0.f : mn;
+        const float keep = exp2_fast(m - base);
+        float part = 0.f;
+#pragma unroll
+        for (int kt = 0; kt < 4; kt++)
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                s[kt][e] = exp2_fast(s[kt][e] - base);
+                part += s[kt][e];
+            }
+        part += __shfl_xor(part, 16);
+        part += __shfl_xor(part, 32);
+        sum = sum * keep + part;
+        m = mn;
+        // the weights are rounded to the inputs' type for the product with V
+        const auto pa = pair_frag<T>(s[0], s[1]), pb = pair_frag<T>(s[2], s[3]);
+#pragma unroll
+        for (int j = 0; j < DT; j++) {
+            O[j] *= keep;
+            O[j] = M::mma(frag_col_pair<T>(Vs, LD, 0, 16 * j), pa, O[j]);
+            O[j] = M::mma(frag_col_pair<T>(Vs, LD, 32, 16 * j), pb, O[j]);
+        }
+    }
+    if (t >= d.T) return;
+    const float inv = live ? 1.f / sum : 0.f;
+#pragma unroll
+    for (int j = 0; j < DT; j++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+            const int c = 16 * j + 4 * g + e;
+            if (c < d.D) op[c] = (T)(live ? O[j][e] * inv : 0.f);
+        }
+    if (g == 0)
+        lse[(b * d.T + t) * d.Hq + h] = live ? (m + log2f(sum)) * 0.6931471805599453f : 0.f;
+}
+
+// The call's last tokens into the rolling cache: the sinks, and the newest
+// `window` tokens behind them.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void window_cache_kernel(
+    WinDims d, int64_t span, const T *__restrict__ k, const T *__restrict__ v, T *__restrict__ ck,
+    T *__restrict__ cv, const int64_t *__restrict__ pos, const int32_t *__restrict__ lengths)
+{
+    // rows 0 .. S - 1 of `span` are the call's first S tokens, the others its last W
+    const int64_t r = blockIdx.x % span, b = blockIdx.x / span;
+    const int64_t len = seq_len(lengths, b, d.T);
+    const int64_t p0 = seq_pos(pos, b);
+    const int64_t nf = d.S < d.T ? d.S : d.T;
+    const int64_t t = r < nf ? r : len - 1 - (r - nf);
+    if (t < 0 || t >= len) return;
+    const int64_t p = p0 + t;
+    if (r < nf ? p >= d.S : p < d.S) return;
+    const int64_t at = (b * d.cap + cache_slot(p, d.S, d.W)) * d.Hk * d.D;
+    for (int e = threadIdx.x; e < d.Hk * d.D; e += kThreads) {
+        const int h = e / d.D, c = e % d.D;
+        ck[at + e] = k[b * d.kb + t * d.kt + h * d.kh + c];
+        cv[at + e] = v[b * d.vb + t * d.vt + h * d.vh + c];
+    }
+}
+
+// delta[b][t][h] = sum_c dout o: what the softmax's backward subtracts.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void window_delta_kernel(int64_t rows, int D,
+                                                                const T *__restrict__ o,
+                                                                const T *__restrict__ dout,
+                                                                float *__restrict__ delta)
+{
+    const int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    const int l = threadIdx.x & 63;
+    if (r >= rows) return;
+    float s = 0.f;
+    for (int c = l; c < D; c += 64) s = fmaf((float)o[r * D + c], (float)dout[r * D + c], s);
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) s += __shfl_xor(s, m);
+    if (l == 0) delta[r] = s;
+}
+
+// dQ^T += K^T dS^T over the keys, with P^T recomputed from lse.
+template <typename T, int DT>
+__global__ __launch_bounds__(kThreads) void window_dq_kernel(
+    WinDims d, const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v,
+    const T *__restrict__ dout, const float *__restrict__ lse, const float *__restrict__ delta,
+    const int32_t *__restrict__ lengths, bool vq, bool vk, bool vo, T *__restrict__ dq)
+{
+    using M = Mat<T>;
+    constexpr int LD = DT * 16 + 8;
+    __shared__ __align__(32) T Ks[kKeys * LD];
+    __shared__ __align__(32) T Vs[kKeys * LD];
+
+    const int qt = blockIdx.x % d.nq;
+    const int64_t bh = blockIdx.x / d.nq;
+    const int h = (int)(bh % d.Hq);
+    const int64_t b = bh / d.Hq;
+    const int hk = h / (d.Hq / d.Hk);
+    const int64_t len = seq_len(lengths, b, d.T);
+    const int64_t t0 = (int64_t)qt * kRows;
+    const int l = threadIdx.x & 63, w = threadIdx.x >> 6, g = l >> 4;
+    const int64_t i = t0 + 16 * w + (l & 15);
+    T *op = dq + ((b * d.T + i) * d.Hq + h) * d.D;
+    const bool live = i < len;
+    f32x4 O[DT];
+#pragma unroll
+    for (int j = 0; j < DT; j++) O[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (t0 < len) {
+        const T *qrow = live ? q + b * d.qb + i * d.qt + h * d.qh : nullptr;
+        const T *grow = live ? dout + ((b * d.T + i) * d.Hq + h) * d.D : nullptr;
+        typename M::Frag qf[DT / 2], gf[DT / 2];
+#pragma unroll
+        for (int ks = 0; ks < DT / 2; ks++) {
+            qf[ks] = frag_global<T>(qrow, 32 * ks + 8 * g, d.D, vq);
+            gf[ks] = frag_global<T>(grow, 32 * ks + 8 * g, d.D, vo);
+        }
+        const float L = live ? lse[(b * d.T + i) * d.Hq + h] * 1.4426950408889634f : 0.f;
+        const float dl = live ? delta[(b * d.T + i) * d.Hq + h] : 0.f;
+        const int64_t last = (t0 + kRows < len ? t0 + kRows : len) - 1;
+        const KeyRange kr(t0, last, d.W, d.S);
+        const T *kn = k + b * d.kb + hk * d.kh, *vn = v + b * d.vb + hk * d.vh;
+        for (int n = 0; n < kr.ntiles; n++) {
+            const int64_t j0 = kr.first(n), jend = kr.end(n);
+            __syncthreads();
+            load_rows<T, DT * 16, LD>(Ks, [&](int r) { return j0 + r < jend ? kn + (j0 + r) * d.kt : nullptr; }, d.D, vk);
+            load_rows<T, DT * 16, LD>(Vs, [&](int r) { return j0 + r < jend ? vn + (j0 + r) * d.vt : nullptr; }, d.D, vk);
+            __syncthreads();
+            f32x4 s[4];
+#pragma unroll
+            for (int kt = 0; kt < 4; kt++) {
+                f32x4 dp = {0.f, 0.f, 0.f, 0.f};
+                s[kt] = dp;
+#pragma unroll
+                for (int ks = 0; ks < DT / 2; ks++) {
+                    s[kt] = M::mma(frag_row<T>(Ks, LD, 16 * kt, 32 * ks), qf[ks], s[kt]);
+                    dp = M::mma(frag_row<T>(Vs, LD, 16 * kt, 32 * ks), gf[ks], dp);
+                }
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    const int64_t j = j0 + 16 * kt + 4 * g + e;
+                    const bool see = live && j < jend && j <= i && (i - j < d.W || j < d.S);
+                    const float p = exp2_fast(fmaf(s[kt][e], d.c2, -L));
+                    s[kt][e] = see ? p * (dp[e] - dl) * d.scale : 0.f;
+                }
+            }
+            const auto pa = pair_frag<T>(s[0], s[1]), pb = pair_frag<T>(s[2], s[3]);
+#pragma unroll
+            for (int j = 0; j < DT; j++) {
+                O[j] = M::mma(frag_col_pair<T>(Ks, LD, 0, 16 * j), pa, O[j]);
+                O[j] = M::mma(frag_col_pair<T>(Ks, LD, 32, 16 * j), pb, O[j]);
+            }
+        }
+    }
+    if (i >= d.T) return;
+#pragma unroll
+    for (int j = 0; j < DT; j++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+            const int c = 16 * j + 4 * g + e;
+            if (c < d.D) op[c] = (T)(live ? O[j][e] : 0.f);
+        }
+}
+
+// dK and dV of 64 keys: lane = key (column), four neighbouring queries (rows).
+// SINKS = false: the queries that some window over the tile reaches; the sums
+// of sinks go to part 0 of `parts`.  SINKS = true: the sinks for the queries
+// behind those, 512 a workgroup, into parts 1 ..
+template <typename T, int DT, bool SINKS>
+__global__ __launch_bounds__(kThreads) void window_dkv_kernel(
+    WinDims d, int ntiles, int nparts, const T *__restrict__ q, const T *__restrict__ k,
+    const T *__restrict__ v, const T *__restrict__ dout, const float *__restrict__ lse,
+    const float *__restrict__ delta, const int32_t *__restrict__ lengths, bool vq, bool vk, bool vo,
+    T *__restrict__ dk, T *__restrict__ dv, float *__restrict__ parts)
+{
+    using M = Mat<T>;
+    constexpr int LD = DT * 16 + 8;
+    __shared__ __align__(32) T Qs[kRows * LD];
+    __shared__ __align__(32) T Gs[kRows * LD];
+    __shared__ __align__(16) float Ls[kRows], Dl[kRows];
+
+    int64_t rest = blockIdx.x;
+    int part = 0;
+    if (SINKS) {
+        part = 1 + (int)(rest % (nparts - 1));
+        rest /= nparts - 1;
+    }
+    const int kt = (int)(rest % ntiles);
+    rest /= ntiles;
+    const int hk = (int)(rest % d.Hk);
+    const int64_t b = rest / d.Hk;
+    const int64_t len = seq_len(lengths, b, d.T);
+    const int l = threadIdx.x & 63, w = threadIdx.x >> 6, g = l >> 4;
+    const int64_t j0 = (int64_t)kt * kKeys;
+    const int64_t j = j0 + 16 * w + (l & 15);     // the lane's key
+    const int per = d.Hq / d.Hk;
+    f32x4 dK[DT], dV[DT];
+#pragma unroll
+    for (int n = 0; n < DT; n++) dK[n] = dV[n] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    // the queries: [first, end)
+    int64_t first = j0, end = j0 + kKeys - 1 + d.W < len ? j0 + kKeys - 1 + d.W : len;
+    if (SINKS) {
+        first = (int64_t)(part - 1) * kSinkRows;
+        end = first + kSinkRows < len ? first + kSinkRows : len;
+        // nearer queries are in part 0
+        if (first < j0 + kKeys - 1 + d.W) first = j0 + kKeys - 1 + d.W;
+    }
+    if (j0 < len && first < end) {
+        const bool live = j < len && (!SINKS || j < d.S);
+        const T *krow = live ? k + b * d.kb + j * d.kt + hk * d.kh : nullptr;
+        const T *vrow = live ? v + b * d.vb + j * d.vt + hk * d.vh : nullptr;
+        typename M::Frag kf[DT / 2], vf[DT / 2];
+#pragma unroll
+        for (int ks = 0; ks < DT / 2; ks++) {
+            kf[ks] = frag_global<T>(krow, 32 * ks + 8 * g, d.D, vk);
+            vf[ks] = frag_global<T>(vrow, 32 * ks + 8 * g, d.D, vk);
+        }
+        for (int h = hk * per; h < (hk + 1) * per; h++)
+            for (int64_t t0 = first; t0 < end; t0 += kRows) {
+                __syncthreads();
+                load_rows<T, DT * 16, LD>(Qs, [&](int r) {
+                    return t0 + r < end ? q + b * d.qb + (t0 + r) * d.qt + h * d.qh : nullptr;
+                }, d.D, vq);
+                load_rows<T, DT * 16, LD>(Gs, [&](int r) {
+                    return t0 + r < end ? dout + ((b * d.T + t0 + r) * d.Hq + h) * d.D : nullptr;
+                }, d.D, vo);
+                if (threadIdx.x < kRows) {
+                    const int64_t t = t0 + threadIdx.x;
+                    const bool in = t < end;
+                    Ls[threadIdx.x] = in ? lse[(b * d.T + t) * d.Hq + h] * 1.4426950408889634f : 0.f;
+                    Dl[threadIdx.x] = in ? delta[(b * d.T + t) * d.Hq + h] : 0.f;
+                }
+                __syncthreads();
+#pragma unroll
+                for (int half = 0; half < 2; half++) {
+                    f32x4 p[2], ds[2];
+#pragma unroll
+                    for (int u = 0; u < 2; u++) {
+                        const int r0 = 32 * half + 16 * u;
+                        f32x4 s = {0.f, 0.f, 0.f, 0.f}, dp = s;
+#pragma unroll
+                        for (int ks = 0; ks < DT / 2; ks++) {
+                            s = M::mma(frag_row<T>(Qs, LD, r0, 32 * ks), kf[ks], s);
+                            dp = M::mma(frag_row<T>(Gs, LD, r0, 32 * ks), vf[ks], dp);
+                        }
+                        const f32x4 L = *reinterpret_cast<const f32x4 *>(Ls + r0 + 4 * g);
+                        const f32x4 D = *reinterpret_cast<const f32x4 *>(Dl + r0 + 4 * g);
+#pragma unroll
+                        for (int e = 0; e < 4; e++) {
+                            const int64_t i = t0 + r0 + 4 * g + e;
+                            const bool see = live && i < end && j <= i && (i - j < d.W || j < d.S);
+                            p[u][e] = see ? exp2_fast(fmaf(s[e], d.c2, -L[e])) : 0.f;
+                            ds[u][e] = see ? p[u][e] * (dp[e] - D[e]) * d.scale : 0.f;
+                        }
+                    }
+                    const auto pf = pair_frag<T>(p[0], p[1]), sf = pair_frag<T>(ds[0], ds[1]);
+#pragma unroll
+                    for (int n = 0; n < DT; n++) {
+                        dV[n] = M::mma(frag_col_pair<T>(Gs, LD, 32 * half, 16 * n), pf, dV[n]);
+                        dK[n] = M::mma(frag_col_pair<T>(Qs, LD, 32 * half, 16 * n), sf, dK[n]);
+                    }
+                }
+            }
+    }
+    const int64_t at = ((b * d.T + j) * d.Hk + hk) * d.D;
+    const bool sink = parts && j < d.S;
+    if (j >= d.T || (SINKS && !sink)) return;
+    float *pp = parts + ((((int64_t)part * d.B + b) * d.Hk + hk) * d.S + j) * 2 * d.D;
+#pragma unroll
+    for (int n = 0; n < DT; n++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+            const int c = 16 * n + 4 * g + e;
+            if (c >= d.D) continue;
+            if (sink) {
+                pp[c] = dK[n][e];
+                pp[d.D + c] = dV[n][e];
+            } else {
+                dk[at + c] = (T)dK[n][e];
+                dv[at + c] = (T)dV[n][e];
+            }
+        }
+}
+
+// dK and dV of the sinks: the sum of their parts, in order.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void window_sinks_kernel(WinDims d, int nparts,
+                                                                const float *__restrict__ parts,
+                                                                T *__restrict__ dk, T *__restrict__ dv)
+{
+    const int64_t r = blockIdx.x;   // (b, hk, j)
+    const int64_t j = r % d.S, bh = r / d.S, hk = bh % d.Hk, b = bh / d.Hk;
+    if (j >= d.T) return;
+    const int64_t step = (int64_t)d.B * d.Hk * d.S * 2 * d.D;
+    for (int c = threadIdx.x; c < 2 * d.D; c += kThreads) {
+        float s = 0.f;
+        for (int n = 0; n < nparts; n++) s += parts[n * step + r * 2 * d.D + c];
+        T *out = c < d.D ? dk : dv;
+        out[((b * d.T + j) * d.Hk + hk) * d.D + (c < d.D ? c : c - d.D)] = (T)s;
+    }
+}
+
+// -------------------------------------------------------------------- host
+
+WinDims dims_of(const sdm_window_desc &s)
+{
+    WinDims d = {};
+    d.B = s.B;
+    d.Hq = s.Hq;
+    d.Hk = s.Hk;
+    d.D = s.D;
+    d.T = s.T;
+    d.W = s.window;
+    d.S = s.sinks;
+    d.scale = s.scale;
+    d.c2 = (float)((double)s.scale * 1.4426950408889634);
+    d.qb = s.q_batch;
+    d.qt = s.q_token;
+    d.qh = s.q_head;
+    d.kb = s.k_batch;
+    d.kt = s.k_token;
+    d.kh = s.k_head;
+    d.vb = s.v_batch;
+    d.vt = s.v_token;
+    d.vh = s.v_head;
+    d.cap = s.sinks + s.window;
+    d.nq = (int)((s.T + kRows - 1) / kRows);
+    return d;
+}
+
+// Rows on 16 bytes: D a multiple of 8 elements, base and strides aligned.
+bool rows16(const void *p, int64_t a, int64_t b, int64_t c, int D, int esize)
+{
+    return D % 8 == 0 && (((uintptr_t)p | (uintptr_t)(a * esize) | (uintptr_t)(b * esize) |
+                           (uintptr_t)(c * esize)) & 15u) == 0;
+}
+
+struct BackPlan {
+    size_t delta, parts, total;
+    int nparts, ktiles;
+};
+
+BackPlan back_plan(const sdm_window_desc &s)
+{
+    BackPlan p = {};
+    size_t at = ((size_t)s.B * s.T * s.Hq * 4 + 255) & ~(size_t)255;
+    // sinks that queries see from behind their window
+    if (s.sinks > 0 && s.T > s.window) {
+        p.nparts = 1 + (int)((s.T + kSinkRows - 1) / kSinkRows);
+        p.ktiles = (s.sinks + kKeys - 1) / kKeys;
+        if ((int64_t)p.ktiles * kKeys > s.T) p.ktiles = (int)((s.T + kKeys - 1) / kKeys);
+        p.parts = at;
+        at += (size_t)p.nparts * s.B * s.Hk * s.sinks * 2 * s.D * 4;
+    }
+    p.total = at;
+    return p;
+}
+
+template <typename T, int DT>
+hipError_t forward(const WindowArgs &a, hipStream_t stream)
+{
+    const WinDims d = dims_of(a.d);
+    const bool vq = rows16(a.q, d.qb, d.qt, d.qh, d.D, sizeof(T));
+    const bool vk = rows16(a.k, d.kb, d.kt, d.kh, d.D, sizeof(T)) &&
+                    rows16(a.v, d.vb, d.vt, d.vh, d.D, sizeof(T));
+    window_fwd_kernel<T, DT><<<(unsigned)((int64_t)d.B * d.Hq * d.nq), kThreads, 0, stream>>>(
+        d, (const T *)a.q, (const T *)a.k, (const T *)a.v, (const T *)a.cache_k, (const T *)a.cache_v,
+        a.pos, a.lengths, vq, vk, (T *)a.o, a.lse);
+    if (a.cache_k) {
+        const int64_t span = (d.S < d.T ? d.S : d.T) + (d.W < d.T ? d.W : d.T);
+        window_cache_kernel<T><<<(unsigned)(span * d.B), kThreads, 0, stream>>>(
+            d, span, (const T *)a.k, (const T *)a.v, (T *)a.cache_k, (T *)a.cache_v, a.pos, a.lengths);
+    }
+    return hipGetLastError();
+}
+
+template <typename T, int DT>
+hipError_t backward(const WindowArgs &a, hipStream_t stream)
+{
+    const WinDims d = dims_of(a.d);
+    const BackPlan p = back_plan(a.d);
+    const bool vq = rows16(a.q, d.qb, d.qt, d.qh, d.D, sizeof(T));
+    const bool vk = rows16(a.k, d.kb, d.kt, d.kh, d.D, sizeof(T)) &&
+                    rows16(a.v, d.vb, d.vt, d.vh, d.D, sizeof(T));
+    const bool vo = rows16(a.dout, 0, 0, d.D, d.D, sizeof(T));
+    const T *q = (const T *)a.q, *k = (const T *)a.k, *v = (const T *)a.v, *dout = (const T *)a.dout;
+    float *delta = (float *)a.ws, *parts = p.nparts ? (float *)(a.ws + p.parts) : nullptr;
+    const int64_t rows = (int64_t)d.B * d.T * d.Hq;
+    window_delta_kernel<T><<<(unsigned)((rows + 3) / 4), kThreads, 0, stream>>>(
+        rows, d.D, (const T *)a.oin, dout, delta);
+    window_dq_kernel<T, DT><<<(unsigned)((int64_t)d.B * d.Hq * d.nq), kThreads, 0, stream>>>(
+        d, q, k, v, dout, a.lse_in, delta, a.lengths, vq, vk, vo, (T *)a.dq);
+    window_dkv_kernel<T, DT, false><<<(unsigned)((int64_t)d.B * d.Hk * d.nq), kThreads, 0, stream>>>(
+        d, d.nq, p.nparts, q, k, v, dout, a.lse_in, delta, a.lengths, vq, vk, vo, (T *)a.dk, (T *)a.dv,
+        parts);
+    if (p.nparts) {
+        window_dkv_kernel<T, DT, true>
+            <<<(unsigned)((int64_t)d.B * d.Hk * p.ktiles * (p.nparts - 1)), kThreads, 0, stream>>>(
+                d, p.ktiles, p.nparts, q, k, v, dout, a.lse_in, delta, a.lengths, vq, vk, vo,
+                (T *)a.dk, (T *)a.dv, parts);
+        window_sinks_kernel<T><<<(unsigned)((int64_t)d.B * d.Hk * d.S), kThreads, 0, stream>>>(
+            d, p.nparts, parts, (T *)a.dk, (T *)a.dv);
+    }
+    return hipGetLastError();
+}
+
+template <typename T>
+hipError_t dispatch(const WindowArgs &a, bool back, hipStream_t stream)
+{
+    // head columns padded to 32, 64, 128 or 256
+    if (a.d.D <= 32) return back ? backward<T, 2>(a, stream) : forward<T, 2>(a, stream);
+    if (a.d.D <= 64) return back ? backward<T, 4>(a, stream) : forward<T, 4>(a, stream);
+    if (a.d.D <= 128) return back ? backward<T, 8>(a, stream) : forward<T, 8>(a, stream);
+    return back ? backward<T, 16>(a, stream) : forward<T, 16>(a, stream);
+}
+
+}  // namespace
+
+size_t window_forward_ws(const sdm_window_desc &, bool) { return 0; }
+size_t window_backward_ws(const sdm_window_desc &d) { return back_plan(d).total; }
+
+hipError_t launch_window_forward(const WindowArgs &a, hipStream_t stream)
+{
+    return a.d.dtype == SDM_F32 ? dispatch<float>(a, false, stream) : dispatch<bf16>(a, false, stream);
+}
+
+hipError_t launch_window_backward(const WindowArgs &a, hipStream_t stream)
+{
+    return a.d.dtype == SDM_F32 ? dispatch<float>(a, true, stream) : dispatch<bf16>(a, true, stream);
+}
+
+}  // namespace sdm

@@ -1,6 +1,6 @@
-"""Sequence mixers beside the SDM core: CausalConv and SelectiveScan.
+"""Sequence mixers beside the SDM core: CausalConv, SelectiveScan, WindowAttention.
 
-Bindings of the sdm_conv_* and sdm_scan_* calls of include/sdm.h.
+Bindings of the sdm_conv_*, sdm_scan_* and sdm_window_* calls of include/sdm.h.
 Like SDM, each class borrows its parameters, runs on the current stream of its
 inputs' device, raises SDMError for what the library refuses, and has no
 fallback.  Inputs may be views with any batch and token strides; outputs are
@@ -9,7 +9,7 @@ new dense tensors unless given.
 from __future__ import annotations
 
 import ctypes
-from ctypes import c_int, c_int64
+from ctypes import c_float, c_int, c_int64
 
 import torch
 
@@ -284,5 +284,120 @@ class SelectiveScan:
                 _p(self.dt_bias), _p(lengths), _p(dy), _p(state), _p(dstate), _p(workspace),
                 workspace.numel(), _p(out["dx"]), _p(out["ddt"]), _p(out["dB"]), _p(out["dC"]),
                 _p(out["dA"]), _p(out.get("dD")), _p(out.get("ddt_bias")), _p(out.get("dstate")),
+                stream))
+        return out
+
+
+class _WindowDesc(ctypes.Structure):
+    _fields_ = [("B", c_int), ("T", c_int64), ("Hq", c_int), ("Hk", c_int), ("D", c_int),
+                ("window", c_int64), ("sinks", c_int), ("scale", c_float), ("dtype", c_int)] + \
+               [(f"{t}_{s}", c_int64) for t in "qkv" for s in ("batch", "token", "head")]
+
+
+class WindowAttention:
+    """Causal attention with a sliding window and sinks.
+
+    The query at i sees the key at j where j <= i and (i - j < window or
+    j < sinks).  Hq / Hk neighbouring query heads share a key head; scale
+    defaults to 1 / sqrt(D).
+    """
+
+    def __init__(self, Hq: int, Hk: int, D: int, window: int, sinks: int = 0, scale=None):
+        self.Hq, self.Hk, self.D = int(Hq), int(Hk), int(D)
+        self.window, self.sinks = int(window), int(sinks)
+        if self.D < 1 or self.window < 1 or self.sinks < 0 or max(
+                self.D, self.window, self.sinks, abs(self.Hq), abs(self.Hk)) >= 1 << 31:
+            raise SDMError(1, "D and window must be >= 1, sinks >= 0, and all below 2^31")
+        self.scale = self.D ** -0.5 if scale is None else float(scale)
+
+    def new_cache(self, B: int, dtype=_BF16, device="cuda"):
+        """An empty rolling cache for B streams: (keys, values), each
+        [B, sinks + window, Hk, D]."""
+        shape = (B, self.sinks + self.window, self.Hk, self.D)
+        return (torch.zeros(shape, dtype=dtype, device=device),
+                torch.zeros(shape, dtype=dtype, device=device))
+
+    def _desc(self, q, k, v):
+        if not isinstance(q, torch.Tensor) or q.dim() != 4:
+            raise SDMError(1, f"q must be [B, T, {self.Hq}, {self.D}]")
+        B, T = q.shape[:2]
+        _view(q, "q", q, (B, T, self.Hq, self.D), 1)
+        _view(k, "k", q, (B, T, self.Hk, self.D), 1)
+        _view(v, "v", q, (B, T, self.Hk, self.D), 1)
+        return _WindowDesc(B, T, self.Hq, self.Hk, self.D, self.window, self.sinks, self.scale,
+                           _dtype(q, "q"), *q.stride()[:3], *k.stride()[:3], *v.stride()[:3])
+
+    def workspace_size(self, q, k, v, cont: bool = False) -> int:
+        """Bytes of workspace forward needs for inputs like these."""
+        n = ctypes.c_size_t()
+        _check(lib().sdm_window_workspace_size(ctypes.byref(self._desc(q, k, v)),
+                                               FLAG_CONTINUE if cont else 0, ctypes.byref(n)))
+        return n.value
+
+    def forward(self, q, k, v, cache=None, pos=None, cont: bool = False, lengths=None, o=None,
+                lse=None, workspace=None):
+        """(o, lse): o [B, T, Hq, D] and the log of the softmax's sum [B, T, Hq]
+        (float32), for q [B, T, Hq, D] and k, v [B, T, Hk, D].
+
+        cache: (keys, values) of new_cache, updated in place with the call's
+        tokens.  With cont=True the tokens follow the pos[b] tokens that
+        sequence b has in the cache (pos [B] int64, which the caller advances);
+        otherwise they start a sequence.  lengths [B] int32: tokens of each
+        sequence in this call.
+        """
+        d = self._desc(q, k, v)
+        ck = cv = None
+        if cache is not None:
+            ck, cv = cache
+            shape = (d.B, self.sinks + self.window, self.Hk, self.D)
+            _out_tensor(ck, "the cache's keys", shape, q.dtype, q)
+            _out_tensor(cv, "the cache's values", shape, q.dtype, q)
+        if cont and (cache is None or pos is None):
+            raise SDMError(1, "cont=True needs the cache and pos")
+        if pos is not None:
+            _out_tensor(pos, "pos", (d.B,), torch.int64, q)
+        if o is None:
+            o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        else:
+            _out_tensor(o, "o", q.shape, q.dtype, q)
+        if lse is None:
+            lse = torch.empty(q.shape[:3], dtype=_F32, device=q.device)
+        else:
+            _out_tensor(lse, "lse", q.shape[:3], _F32, q)
+        _lengths(lengths, d.B, q)
+        flags = FLAG_CONTINUE if cont else 0
+        n = ctypes.c_size_t()
+        _check(lib().sdm_window_workspace_size(ctypes.byref(d), flags, ctypes.byref(n)))
+        if n.value or workspace is not None:
+            workspace = _workspace(workspace, n.value, q)
+        with _On(q.device) as stream:
+            _check(lib().sdm_window_forward(
+                ctypes.byref(d), _p(q), _p(k), _p(v), _p(lengths), flags, _p(ck), _p(cv), _p(pos),
+                _p(workspace), 0 if workspace is None else workspace.numel(), _p(o), _p(lse),
+                stream))
+        return o, lse
+
+    def backward_workspace_size(self, q, k, v) -> int:
+        """Bytes of workspace backward needs for inputs like these."""
+        n = ctypes.c_size_t()
+        _check(lib().sdm_window_backward_workspace_size(ctypes.byref(self._desc(q, k, v)),
+                                                        ctypes.byref(n)))
+        return n.value
+
+    def backward(self, q, k, v, o, lse, do, lengths=None, workspace=None) -> dict:
+        """Gradients dq, dk, dv for do [B, T, Hq, D], with the o and lse that a
+        forward without a cache returned."""
+        d = self._desc(q, k, v)
+        _out_tensor(o, "o", q.shape, q.dtype, q)
+        _out_tensor(do, "do", q.shape, q.dtype, q)
+        _out_tensor(lse, "lse", q.shape[:3], _F32, q)
+        _lengths(lengths, d.B, q)
+        workspace = _workspace(workspace, self.backward_workspace_size(q, k, v), q)
+        out = {n: torch.empty(t.shape, dtype=q.dtype, device=q.device)
+               for n, t in (("dq", q), ("dk", k), ("dv", v))}
+        with _On(q.device) as stream:
+            _check(lib().sdm_window_backward(
+                ctypes.byref(d), _p(q), _p(k), _p(v), _p(o), _p(lse), _p(do), _p(lengths),
+                _p(workspace), workspace.numel(), _p(out["dq"]), _p(out["dk"]), _p(out["dv"]),
                 stream))
         return out

@@ -131,3 +131,64 @@ def test_scan_pointer_refusals():
         q[at] = FAKE + 4
         assert L.sdm_scan_backward(d, *[FAKE] * 12, n.value, *q, None) == 1, at
     assert L.sdm_scan_backward(d, *[FAKE] * 12, n.value - 1, *[FAKE] * 8, None) == 3
+
+
+def window_desc(**kw):
+    d = dict(B=2, T=100, Hq=4, Hk=2, D=16, window=8, sinks=2, scale=0.25, dtype=sdm.BF16,
+             q_batch=6400, q_token=64, q_head=16, k_batch=3200, k_token=32, k_head=16, v_batch=3200,
+             v_token=32, v_head=16)
+    d.update(kw)
+    return mixers._WindowDesc(**d)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(B=0), 1), (dict(T=0), 1), (dict(Hq=0), 1), (dict(Hk=0), 1), (dict(Hk=3), 1), (dict(D=0), 1),
+    (dict(window=0), 1), (dict(sinks=-1), 1), (dict(scale=float("nan")), 1), (dict(dtype=2), 1),
+    (dict(q_token=-1), 1), (dict(k_head=-1), 1), (dict(v_batch=-1), 1), (dict(D=257), 2),
+    (dict(sinks=1025), 2), (dict(window=1 << 31), 2), (dict(T=1 << 31), 2),
+    (dict(B=1 << 15, T=1 << 20), 2),
+])
+def test_window_descriptor_refusals(kw, status):
+    L, n = sdm.lib(), ctypes.c_size_t()
+    d = ctypes.byref(window_desc(**kw))
+    assert L.sdm_window_workspace_size(d, 0, ctypes.byref(n)) == status and n.value == 0
+    assert L.sdm_window_backward_workspace_size(d, ctypes.byref(n)) == status
+    assert L.sdm_window_forward(d, *[FAKE] * 4, 1, *[FAKE] * 4, 1 << 40, FAKE, FAKE, None) == status
+    assert L.sdm_window_backward(d, *[FAKE] * 8, 1 << 40, FAKE, FAKE, FAKE, None) == status
+    assert L.sdm_last_error()
+
+
+def test_window_pointer_refusals():
+    L, n = sdm.lib(), ctypes.c_size_t()
+    d = ctypes.byref(window_desc())
+    assert L.sdm_window_workspace_size(None, 0, ctypes.byref(n)) == 1
+    assert L.sdm_window_workspace_size(d, 0, None) == 1
+    assert L.sdm_window_workspace_size(d, 4, ctypes.byref(n)) == 1
+
+    def fwd(flags=1, **kw):
+        p = dict(q=FAKE, k=FAKE, v=FAKE, lengths=None, ck=FAKE, cv=FAKE, pos=FAKE, ws=FAKE, o=FAKE,
+                 lse=FAKE)
+        p.update(kw)
+        return L.sdm_window_forward(d, p["q"], p["k"], p["v"], p["lengths"], flags, p["ck"], p["cv"],
+                                    p["pos"], p["ws"], 1 << 40, p["o"], p["lse"], None)
+
+    for name in ("q", "k", "v", "ck", "cv", "pos", "o", "lse"):
+        assert fwd(**{name: None}) == 1, name
+    for name in ("q", "k", "v"):
+        assert fwd(**{name: FAKE + 1}) == 1, name
+    for name in ("ck", "cv", "o", "lse", "ws"):
+        assert fwd(**{name: FAKE + 8}) == 1, name
+    assert fwd(pos=FAKE + 4) == 1 and fwd(lengths=FAKE + 2) == 1
+    assert fwd(flags=0) == 1                      # pos without the flag
+    assert fwd(flags=0, pos=None, cv=None) == 1   # half a cache
+    assert fwd(flags=2) == 1
+    assert L.sdm_window_backward_workspace_size(d, ctypes.byref(n)) == 0 and n.value > 0
+    for at in (0, 1, 2, 3, 4, 5, 7):
+        p = [FAKE] * 8
+        p[at] = None
+        assert L.sdm_window_backward(d, *p, n.value, FAKE, FAKE, FAKE, None) == 1, at
+    assert L.sdm_window_backward(d, *[FAKE] * 8, n.value - 1, FAKE, FAKE, FAKE, None) == 3
+    for at in range(3):
+        q = [FAKE] * 3
+        q[at] = None
+        assert L.sdm_window_backward(d, *[FAKE] * 8, n.value, *q, None) == 1, at
