@@ -158,7 +158,7 @@ def _run_own(s):
         return dict(y=y, state=state)
     att = sdm.WindowAttention(c["Hq"], c["Hk"], c["D"], window=c["W"], sinks=c["S"])
     if c["mode"] == "bwd":
-        g = att.backward(s["q"], s["k"], s["v"], s["o"], s["lse"], s["do"], lengths=n)
+        g = att.backward(s["q"], s["k"], s["v"], s["o"].contiguous(), s["lse"].contiguous(), s["do"], lengths=n)
         return {k: g[k] for k in ("dq", "dk", "dv")}
     if step:
         o, lse = att.forward(s["q"], s["k"], s["v"], cache=(s["ck"], s["cv"]), pos=s["pos"], cont=True, lengths=n)
