@@ -415,7 +415,8 @@ sdm_status sdm_conv_backward(const sdm_conv_desc *d, const void *x, const float 
  *   S_t = exp(D_t A) S_{t-1} + D_t x_t B_t^T      (P x N)
  *   y_t = S_t C_t + D x_t
  * A <= 0 and D_t >= 0 are the intended ranges (not checked).
- * Limits: 1 <= N <= 128, 1 <= P, G divides H; B * T * H < 2^31, B * H < 65536.
+ * Limits: 1 <= N <= 128, 1 <= P <= 65536, G divides H; B * T * H < 2^31,
+ * B * H < 65536; H * P and the token strides below 2^22 elements.
  */
 typedef struct {
     int B;

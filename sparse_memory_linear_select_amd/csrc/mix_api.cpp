@@ -49,6 +49,15 @@ sdm_status check_batch(int B, int64_t T, sdm_dtype dtype)
     return SDM_OK;
 }
 
+// The kernels address the rows of a tile with 31-bit offsets.
+sdm_status check_stride(int64_t token)
+{
+    if (token >= (int64_t)1 << 22)
+        return set_error(SDM_ERR_UNSUPPORTED, "token strides must be < 2^22 elements (got %lld)",
+                         (long long)token);
+    return SDM_OK;
+}
+
 sdm_status check_workspace(const void *ws, size_t have, size_t need)
 {
     if (need && !ws) return set_error(SDM_ERR_ARG, "null workspace");
@@ -103,11 +112,16 @@ sdm_status check_scan(const sdm_scan_desc *d)
         d->C_token < 0)
         return set_error(SDM_ERR_ARG, "strides must be >= 0");
     if (d->N > 128) return set_error(SDM_ERR_UNSUPPORTED, "N <= 128 is supported (got %d)", d->N);
+    CHECK(check_stride(d->x_token));
+    CHECK(check_stride(d->B_token));
+    CHECK(check_stride(d->C_token));
     if (d->P > 65536) return set_error(SDM_ERR_UNSUPPORTED, "P <= 65536 is supported (got %d)", d->P);
     if ((double)d->B * (double)d->T * d->H >= 2147483648.0)
         return set_error(SDM_ERR_UNSUPPORTED, "B*T*H must be < 2^31");
     if ((double)d->B * d->H >= 65536.0)
         return set_error(SDM_ERR_UNSUPPORTED, "B*H must be < 65536");
+    if ((int64_t)d->H * d->P >= (int64_t)1 << 22)
+        return set_error(SDM_ERR_UNSUPPORTED, "H*P must be < 2^22");
     return SDM_OK;
 }
 

@@ -81,10 +81,7 @@ struct Mat<float> {
 template <typename T>
 __device__ __forceinline__ typename Mat<T>::Frag round_frag(f32x8 v)
 {
-    typename Mat<T>::Frag f;
-#pragma unroll
-    for (int i = 0; i < 8; i++) f[i] = (T)v[i];
-    return f;
+    return __builtin_convertvector(v, typename Mat<T>::Frag);
 }
 
 // 8 float32 values as kTerms fragments that add up to them (bfloat16: the
@@ -95,8 +92,7 @@ __device__ __forceinline__ void split_frag(f32x8 v, typename Mat<T>::Frag (&f)[M
 #pragma unroll
     for (int n = 0; n < Mat<T>::kTerms; n++) {
         f[n] = round_frag<T>(v);
-#pragma unroll
-        for (int i = 0; i < 8; i++) v[i] -= (float)f[n][i];
+        v -= __builtin_convertvector(f[n], f32x8);
     }
 }
 
@@ -109,49 +105,141 @@ __device__ __forceinline__ typename Mat<T>::Frag frag_row(const T *tile, int ld,
                                                             (l >> 4) * 8);
 }
 
+// Four rows of column l % 16 of a 16-column block of an LDS tile, rows from
+// row0 (the same for the 16 lanes that share l / 16).  Bfloat16: the gfx950
+// transposing read, in which lane l of the 16 fetches 8 bytes of row l / 4 and
+// receives column l of the 4 x 16 block.
+__device__ __forceinline__ bf16x4 col4(const bf16 *tile, int ld, int row0, int col0)
+{
+    typedef short s16x4 __attribute__((ext_vector_type(4)));
+    const int li = threadIdx.x & 15;
+    const bf16 *p = tile + (row0 + (li >> 2)) * ld + col0 + (li & 3) * 4;
+    return __builtin_bit_cast(
+        bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)p));
+}
+
+__device__ __forceinline__ f32x4 col4(const float *tile, int ld, int row0, int col0)
+{
+    const float *p = tile + row0 * ld + col0 + (threadIdx.x & 15);
+    return f32x4{p[0], p[ld], p[2 * ld], p[3 * ld]};
+}
+
 // Column fragment: columns col0 + l % 16, k (the tile's rows) from k0.
 template <typename T>
 __device__ __forceinline__ typename Mat<T>::Frag frag_col(const T *tile, int ld, int k0, int col0)
 {
-    const int l = threadIdx.x & 63;
-    const T *p = tile + (k0 + (l >> 4) * 8) * ld + col0 + (l & 15);
-    typename Mat<T>::Frag f;
-#pragma unroll
-    for (int i = 0; i < 8; i++) f[i] = p[i * ld];
-    return f;
+    const int r = k0 + ((threadIdx.x & 63) >> 4) * 8;
+    return __builtin_shufflevector(col4(tile, ld, r, col0), col4(tile, ld, r + 4, col0), 0, 1, 2, 3, 4,
+                                   5, 6, 7);
 }
 
-// Fills a ROWS x COLS tile in LDS (row stride LD) from rows of a strided
-// tensor; rows from `rows` and columns from `cols` on become zero and are not
-// read.  vec: every row starts on 16 bytes and cols is a multiple of 16 bytes.
-template <typename T, int ROWS, int COLS, int LD, int THREADS>
-__device__ __forceinline__ void load_tile(T *tile, const T *src, int64_t stride, int rows, int cols,
-                                          bool vec)
+// Fragments whose k order is that of two accumulator tiles, 16 apart: k0 + 4 g
+// .. + 3 and k0 + 16 + 4 g .. + 3 with g = l / 16.  A column fragment, a row
+// fragment, and the accumulator tiles themselves, rounded.
+template <typename T>
+__device__ __forceinline__ typename Mat<T>::Frag frag_col_pair(const T *tile, int ld, int k0, int col0)
 {
-    constexpr int V = 16 / sizeof(T);
-    constexpr int PER = COLS / V;
-    const int tid = threadIdx.x;
-    for (int e = tid; e < ROWS * PER; e += THREADS) {
-        const int r = e / PER, c = (e % PER) * V;
-        Vec<T, V> v;
-        if (vec && r < rows && c < cols) {
-            v = vload<T, V>(src + r * stride + c);
-        } else {
-#pragma unroll
-            for (int i = 0; i < V; i++)
-                v.e[i] = r < rows && c + i < cols ? src[r * stride + c + i] : (T)0.f;
-        }
-        vstore<T, V>(tile + r * LD + c, v);
+    const int r = k0 + ((threadIdx.x & 63) >> 4) * 4;
+    return __builtin_shufflevector(col4(tile, ld, r, col0), col4(tile, ld, r + 16, col0), 0, 1, 2, 3, 4,
+                                   5, 6, 7);
+}
+
+template <typename T>
+__device__ __forceinline__ typename Mat<T>::Frag frag_row_pair(const T *tile, int ld, int row0, int k0)
+{
+    const int l = threadIdx.x & 63;
+    const T *q = tile + (row0 + (l & 15)) * ld + k0 + (l >> 4) * 4;
+    return __builtin_shufflevector(*reinterpret_cast<const typename Mat<T>::Half *>(q),
+                                   *reinterpret_cast<const typename Mat<T>::Half *>(q + 16), 0, 1, 2, 3,
+                                   4, 5, 6, 7);
+}
+
+template <typename T>
+__device__ __forceinline__ typename Mat<T>::Frag frag_acc(f32x4 a, f32x4 b)
+{
+    return round_frag<T>(__builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+// Reads of a strided tensor through a buffer descriptor: an element offset that
+// is masked out (kOut) is not read and gives zero, with no branch around the
+// load.  VEC: 16-byte accesses (rows on 16 bytes, columns a multiple of them);
+// else element by element.  Offsets from the descriptor's base stay below
+// 2^31 bytes: the base is the tile's first row, and row strides are limited.
+constexpr uint32_t kOut = 0x80000000u;
+
+template <typename T>
+struct Source {
+    __amdgpu_buffer_rsrc_t r;
+    __device__ __forceinline__ explicit Source(const T *p)
+        : r(__builtin_amdgcn_make_buffer_rsrc((void *)p, 0, (int)kOut, 0x27000))
+    {
     }
+    // V elements from element offset `off`, `n` of them (vectors: all or none)
+    template <int V, bool VEC>
+    __device__ __forceinline__ Vec<T, V> read(uint32_t off, int n) const
+    {
+        static_assert(V * sizeof(T) == 16, "16-byte vectors");
+        if constexpr (VEC) {
+            using Out = Vec<T, V>;
+            return __builtin_bit_cast(
+                Out,
+                __builtin_amdgcn_raw_buffer_load_b128(r, n > 0 ? off * (uint32_t)sizeof(T) : kOut, 0, 0));
+        } else {
+            Vec<T, V> v;
+#pragma unroll
+            for (int i = 0; i < V; i++) {
+                const uint32_t at = i < n ? (off + i) * (uint32_t)sizeof(T) : kOut;
+                if constexpr (sizeof(T) == 2)
+                    v.e[i] = __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b16(r, at, 0, 0));
+                else
+                    v.e[i] = __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b32(r, at, 0, 0));
+            }
+            return v;
+        }
+    }
+};
+
+// A ROWS x COLS tile (LDS row stride LD) in two steps, so that a load can be in
+// flight while the previous tile is worked on: rows of a strided tensor to
+// registers, registers to LDS.  Rows from `rows` and columns from `cols` on
+// become zero and are not read.
+template <typename T, int ROWS, int COLS, int LD, int THREADS, bool VEC>
+struct TileRegs {
+    static constexpr int V = 16 / sizeof(T);
+    static constexpr int PER = COLS / V;
+    static constexpr int N = ROWS * PER / THREADS;
+    static_assert(ROWS * PER % THREADS == 0, "whole accesses per thread");
+    Vec<T, V> v[N];
+
+    __device__ __forceinline__ void load(const T *src, int64_t stride, int rows, int cols)
+    {
+        const Source<T> s(src);
+#pragma unroll
+        for (int u = 0; u < N; u++) {
+            const int e = threadIdx.x + u * THREADS;
+            const int r = e / PER, c = (e % PER) * V;
+            v[u] = s.template read<V, VEC>((uint32_t)r * (uint32_t)stride + c, r < rows ? cols - c : 0);
+        }
+    }
+    __device__ __forceinline__ void store(T *tile) const
+    {
+#pragma unroll
+        for (int u = 0; u < N; u++) {
+            const int e = threadIdx.x + u * THREADS;
+            vstore<T, V>(tile + (e / PER) * LD + (e % PER) * V, v[u]);
+        }
+    }
+};
+
+template <typename T, int ROWS, int COLS, int LD, int THREADS, bool VEC>
+__device__ __forceinline__ void load_tile(T *tile, const T *src, int64_t stride, int rows, int cols)
+{
+    TileRegs<T, ROWS, COLS, LD, THREADS, VEC> t;
+    t.load(src, stride, rows, cols);
+    t.store(tile);
 }
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
-
-__device__ __forceinline__ bool rows_aligned(const void *p, int64_t s0, int64_t s1, int cols, int esize)
-{
-    return (((uintptr_t)p | (uintptr_t)(s0 * esize) | (uintptr_t)(s1 * esize) |
-             (uintptr_t)(cols * esize)) & 15u) == 0;
-}
 
 }  // namespace
 }  // namespace sdm

@@ -14,6 +14,14 @@ namespace sdm {
 // Thread-local error text of the C entry points (sdm_api.cpp).
 sdm_status set_error(sdm_status s, const char *fmt, ...);
 
+// Whether rows of a strided tensor start on 16 bytes and hold whole 16-byte
+// vectors of `cols` elements.
+inline bool rows_on_16(const void *p, int64_t s0, int64_t s1, int64_t s2, int64_t cols, int esize)
+{
+    return (((uintptr_t)p | (uintptr_t)(s0 * esize) | (uintptr_t)(s1 * esize) |
+             (uintptr_t)(s2 * esize) | (uintptr_t)(cols * esize)) & 15u) == 0;
+}
+
 struct ConvArgs {
     sdm_conv_desc d;
     const void *x, *dy;

@@ -19,6 +19,7 @@ namespace {
 constexpr int Q = 64;         // tokens of a chunk
 constexpr int kSlice = 64;    // columns of x that a workgroup holds: 16 a wave
 constexpr int kThreads = 256;
+constexpr int kMaxSegs = 512;   // segments of the time axis
 constexpr int LX = kSlice + 8;  // LDS row stride of 64-wide tiles
 
 struct ScanDims {
@@ -124,16 +125,15 @@ __device__ __forceinline__ void state_update(f32x4 (&S)[NT], const T *U, const T
 {
     using M = Mat<T>;
     constexpr int LN = NT * 16 + 8;
-    const int l = threadIdx.x & 63;
+    const int g = (threadIdx.x & 63) >> 4;
     typename M::Frag uw[2][M::kTerms];
 #pragma unroll
     for (int ks = 0; ks < 2; ks++) {
         f32x8 v;
-#pragma unroll
-        for (int i = 0; i < 8; i++) {
-            const int s = 32 * ks + (l >> 4) * 8 + i;
-            v[i] = (float)U[s * LX + col0 + (l & 15)] * wt[s];
-        }
+        const auto u = frag_col_pair<T>(U, LX, 32 * ks, col0);
+        const f32x4 lo = *reinterpret_cast<const f32x4 *>(wt + 32 * ks + g * 4);
+        const f32x4 hi = *reinterpret_cast<const f32x4 *>(wt + 32 * ks + 16 + g * 4);
+        v = __builtin_convertvector(u, f32x8) * __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
         split_frag<T>(v, uw[ks]);
     }
 #pragma unroll
@@ -141,7 +141,7 @@ __device__ __forceinline__ void state_update(f32x4 (&S)[NT], const T *U, const T
         S[j] *= scale;
 #pragma unroll
         for (int ks = 0; ks < 2; ks++) {
-            const auto a = frag_col<T>(V, LN, 32 * ks, 16 * j);
+            const auto a = frag_col_pair<T>(V, LN, 32 * ks, 16 * j);
 #pragma unroll
             for (int n = 0; n < M::kTerms; n++) S[j] = M::mma(a, uw[ks][n], S[j]);
         }
@@ -152,8 +152,13 @@ __device__ __forceinline__ void state_update(f32x4 (&S)[NT], const T *U, const T
 // A workgroup walks the chunks of one (sequence, head, slice of 64 columns,
 // segment) in order with the state in registers: wave w owns columns 16 w ..
 // of the slice, for y and for the state.  C.B and M are shared by the waves
-// through LDS.
-template <typename T, int NT>
+// through LDS.  Products are taken transposed (M^T, y^T, S^T): a lane then
+// holds one token and four neighbouring columns, so that a token's decay is
+// one number a lane, stores take four columns, and the state's accumulators
+// are the next product's operand as they stand.  The next chunk's tiles are on
+// their way from HBM while a chunk is worked on; with kBufs = 2 they go to a
+// second set of tiles (as long as two sets fit into 160 KB of LDS).
+template <typename T, int NT, bool VEC>
 __global__ __launch_bounds__(kThreads) void scan_walk_kernel(
     ScanDims d, const T *__restrict__ x, const T *__restrict__ Bm, const T *__restrict__ Cm,
     const float *__restrict__ D, const float *__restrict__ delta, const float2 *__restrict__ cs,
@@ -162,12 +167,13 @@ __global__ __launch_bounds__(kThreads) void scan_walk_kernel(
 {
     using M = Mat<T>;
     constexpr int LN = NT * 16 + 8;
-    __shared__ __align__(32) T Xs[Q * LX];
-    __shared__ __align__(32) T Bs[Q * LN];
-    __shared__ __align__(32) T Cs[Q * LN];
+    constexpr int kBufs = sizeof(T) == 2 || NT < 8 ? 2 : 1;
+    __shared__ __align__(32) T Xs[kBufs][Q * LX];
+    __shared__ __align__(32) T Bs[kBufs][Q * LN];
+    __shared__ __align__(32) T Cs[kBufs][Q * LN];
     __shared__ __align__(32) T Ms[Q * LX];
-    __shared__ float dl[Q], wt[Q];
-    __shared__ float2 cc[Q];
+    __shared__ __align__(16) float dl[kBufs][Q], wt[kBufs][Q];
+    __shared__ __align__(16) float2 cc[kBufs][Q];
 
     const int seg = blockIdx.x % d.nseg;
     const int64_t r0 = blockIdx.x / d.nseg;
@@ -179,100 +185,126 @@ __global__ __launch_bounds__(kThreads) void scan_walk_kernel(
     const int64_t len = seq_len(lengths, b, d.T);
     const int l = threadIdx.x & 63, w = threadIdx.x >> 6, g = l >> 4, li = l & 15;
     const int pcols = d.P - ps * kSlice < kSlice ? d.P - ps * kSlice : kSlice;
-    const int p = ps * kSlice + 16 * w + li;
     const T *xp = x + b * d.xb + (int64_t)h * d.P + ps * kSlice;
     const T *bp = Bm + b * d.bb + (int64_t)grp * d.N;
     const T *cp = Cm + b * d.cb + (int64_t)grp * d.N;
-    const bool vx = rows_aligned(xp, d.xb, d.xt, pcols, sizeof(T));
-    const bool vb = rows_aligned(bp, d.bb, d.bt, d.N, sizeof(T));
-    const bool vc = rows_aligned(cp, d.cb, d.ct, d.N, sizeof(T));
+    const bool vy = ((d.P * sizeof(T)) & (4 * sizeof(T) - 1)) == 0;
     const float Dh = D ? D[h] : 0.f;
 
+    TileRegs<T, Q, kSlice, LX, kThreads, VEC> rx;
+    TileRegs<T, Q, NT * 16, LN, kThreads, VEC> rb, rc;
+    float rd;
+    float2 rme, rtot;
+    const auto rows_of = [&](int c) {
+        const int64_t n = len - (int64_t)c * Q;
+        return n < 0 ? 0 : n < Q ? (int)n : Q;
+    };
+    const auto fetch = [&](int c) {
+        const int64_t t0 = (int64_t)c * Q;
+        const int rows = rows_of(c);
+        rx.load(xp + t0 * d.xt, d.xt, rows, pcols);
+        rb.load(bp + t0 * d.bt, d.bt, rows, d.N);
+        rc.load(cp + t0 * d.ct, d.ct, rows, d.N);
+        if (threadIdx.x < Q) {
+            const int64_t at = (bh * d.nc + c) * Q;
+            rme = cs[at + threadIdx.x];
+            rtot = cs[at + Q - 1];
+            rd = delta[at + threadIdx.x];
+        }
+    };
+    const auto put = [&](int n) {
+        rx.store(Xs[n]);
+        rb.store(Bs[n]);
+        rc.store(Cs[n]);
+        if (threadIdx.x < Q) {
+            dl[n][threadIdx.x] = rd;
+            cc[n][threadIdx.x] = rme;
+            wt[n][threadIdx.x] = decay(rtot, rme) * rd;
+        }
+    };
+
+    const int c0 = seg * d.cps, c1 = c0 + d.cps < d.nc ? c0 + d.cps : d.nc;
+    fetch(c0);
     f32x4 S[NT];
+    const int pl = ps * kSlice + 16 * w + li;
     {
         const float *src = init;
         if (src) src += (init_api ? bh : bh * d.nseg + seg) * (int64_t)d.P * d.N;
-        state_load<NT>(S, src, init_api, p, d.P, d.N);
+        state_load<NT>(S, src, init_api, pl, d.P, d.N);
     }
-    const int c0 = seg * d.cps, c1 = c0 + d.cps < d.nc ? c0 + d.cps : d.nc;
+    put(0);
+    __syncthreads();
     for (int c = c0; c < c1; c++) {
+        const int n = kBufs == 2 ? (c - c0) & 1 : 0;
         const int64_t t0 = (int64_t)c * Q;
-        const int rows = len - t0 < 0 ? 0 : len - t0 < Q ? (int)(len - t0) : Q;
-        load_tile<T, Q, kSlice, LX, kThreads>(Xs, xp + t0 * d.xt, d.xt, rows, pcols, vx);
-        load_tile<T, Q, NT * 16, LN, kThreads>(Bs, bp + t0 * d.bt, d.bt, rows, d.N, vb);
-        load_tile<T, Q, NT * 16, LN, kThreads>(Cs, cp + t0 * d.ct, d.ct, rows, d.N, vc);
-        if (threadIdx.x < Q) {
-            const int64_t at = (bh * d.nc + c) * Q;
-            const float2 me = cs[at + threadIdx.x];
-            const float dv = delta[at + threadIdx.x];
-            dl[threadIdx.x] = dv;
-            cc[threadIdx.x] = me;
-            wt[threadIdx.x] = decay(cs[at + Q - 1], me) * dv;
-        }
-        __syncthreads();
-        // M, rows 16 w .. + 15; tiles right of the diagonal are zero
+        const int rows = rows_of(c);
+        if (c + 1 < c1) fetch(c + 1);
+        // M^T for tokens 16 w .. + 15 (columns); sources behind them are zero
+        {
+            const int t = 16 * w + li;
+            const float2 ct = cc[n][t];
 #pragma unroll
-        for (int ct = 0; ct < 4; ct++) {
-            if (ct > (w | 1)) break;
-            f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-            if (ct <= w)
+            for (int st = 0; st < 4; st++) {
+                if (st > (w | 1)) break;
+                f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+                if (st <= w) {
 #pragma unroll
-                for (int ks = 0; ks < NT / 2; ks++)
-                    acc = M::mma(frag_row<T>(Cs, LN, 16 * w, 32 * ks),
-                                 frag_row<T>(Bs, LN, 16 * ct, 32 * ks), acc);
-            const int s = 16 * ct + li;
+                    for (int ks = 0; ks < NT / 2; ks++)
+                        acc = M::mma(frag_row<T>(Bs[n], LN, 16 * st, 32 * ks),
+                                     frag_row<T>(Cs[n], LN, 16 * w, 32 * ks), acc);
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const int t = 16 * w + 4 * g + i;
-                Ms[t * LX + s] = (T)(s <= t ? acc[i] * decay(cc[t], cc[s]) * dl[s] : 0.f);
-            }
-        }
-        __syncthreads();
-        // y for the wave's columns
-        typename M::Frag sf[NT / 2], xf[2];
-#pragma unroll
-        for (int j = 0; j < NT / 2; j++)
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-                sf[j][i] = (T)S[2 * j][i];
-                sf[j][4 + i] = (T)S[2 * j + 1][i];
-            }
-#pragma unroll
-        for (int ks = 0; ks < 2; ks++) xf[ks] = frag_col<T>(Xs, LX, 32 * ks, 16 * w);
-#pragma unroll
-        for (int r = 0; r < 4; r++) {
-            f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int j = 0; j < NT / 2; j++) {
-                // C rows with k in the order the state's tiles hold n
-                const T *q = Cs + (16 * r + li) * LN + 32 * j + 4 * g;
-                const auto lo = *reinterpret_cast<const typename M::Half *>(q);
-                const auto hi = *reinterpret_cast<const typename M::Half *>(q + 16);
-                acc = M::mma(__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7), sf[j], acc);
-            }
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const float2 e = cc[16 * r + 4 * g + i];
-                acc[i] *= exp2_fast(e.x + e.y);
-            }
-#pragma unroll
-            for (int ks = 0; ks <= r / 2; ks++)
-                acc = M::mma(frag_row<T>(Ms, LX, 16 * r, 32 * ks), xf[ks], acc);
-            if (p < d.P)
-#pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    const int t = 16 * r + 4 * g + i;
-                    if (t0 + t < d.T) {
-                        const float v = acc[i] + Dh * (float)Xs[t * LX + 16 * w + li];
-                        y[((b * d.T + t0 + t) * d.H + h) * d.P + p] = (T)(t < rows ? v : 0.f);
+                    for (int i = 0; i < 4; i++) {
+                        const int s = 16 * st + 4 * g + i;
+                        acc[i] = s <= t ? acc[i] * decay(ct, cc[n][s]) * dl[n][s] : 0.f;
                     }
                 }
+                // the decayed scores are rounded to the inputs' type for the product with x
+                *reinterpret_cast<typename M::Half *>(Ms + t * LX + 16 * st + 4 * g) =
+                    __builtin_convertvector(acc, typename M::Half);
+            }
         }
-        const float2 tot = cc[Q - 1];
-        state_update<T, NT>(S, Xs, Bs, wt, exp2_fast(tot.x + tot.y), 16 * w);
+        __syncthreads();
+        // y^T for the wave's columns; the state is rounded to the inputs' type
+        typename M::Frag sf[NT / 2], xf[2];
+#pragma unroll
+        for (int j = 0; j < NT / 2; j++) sf[j] = frag_acc<T>(S[2 * j], S[2 * j + 1]);
+#pragma unroll
+        for (int ks = 0; ks < 2; ks++) xf[ks] = frag_col<T>(Xs[n], LX, 32 * ks, 16 * w);
+        const int p = ps * kSlice + 16 * w + 4 * g;
+#pragma unroll
+        for (int r = 0; r < 4; r++) {
+            const int t = 16 * r + li;
+            f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int j = 0; j < NT / 2; j++)
+                acc = M::mma(sf[j], frag_row_pair<T>(Cs[n], LN, 16 * r, 32 * j), acc);
+            const float2 ct = cc[n][t];
+            acc *= exp2_fast(ct.x + ct.y);
+#pragma unroll
+            for (int ks = 0; ks <= r / 2; ks++)
+                acc = M::mma(xf[ks], frag_row<T>(Ms, LX, 16 * r, 32 * ks), acc);
+            const auto xv = *reinterpret_cast<const typename M::Half *>(Xs[n] + t * LX + 16 * w + 4 * g);
+            acc += __builtin_convertvector(xv, f32x4) * Dh;
+            if (t >= rows) acc = f32x4{0.f, 0.f, 0.f, 0.f};
+            if (t0 + t < d.T && p < d.P) {
+                const auto out = __builtin_convertvector(acc, typename M::Half);
+                T *q = y + ((b * d.T + t0 + t) * d.H + h) * d.P + p;
+                if (vy) {
+                    *reinterpret_cast<typename M::Half *>(q) = out;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; i++)
+                        if (p + i < d.P) q[i] = out[i];
+                }
+            }
+        }
+        const float2 tot = cc[n][Q - 1];
+        state_update<T, NT>(S, Xs[n], Bs[n], wt[n], exp2_fast(tot.x + tot.y), 16 * w);
+        if (kBufs == 1) __syncthreads();
+        if (c + 1 < c1) put(kBufs == 2 ? n ^ 1 : 0);
         __syncthreads();
     }
-    if (seg == d.nseg - 1) state_store<NT>(S, state + bh * (int64_t)d.P * d.N, true, p, d.P, d.N);
+    if (seg == d.nseg - 1) state_store<NT>(S, state + bh * (int64_t)d.P * d.N, true, pl, d.P, d.N);
 }
 
 // States alone.  Forward (REV = false): U = x, V = B, weights 2^{c_63 - c_s} D_s;
@@ -281,7 +313,7 @@ __global__ __launch_bounds__(kThreads) void scan_walk_kernel(
 //   G <- 2^{c_63} G + sum_t 2^{c_t} C_t dy_t^T,
 // and `each` gets G behind every chunk.  `end` gets the last one: per segment
 // in the workspace's layout, or (end_api) the caller's gradient.
-template <typename T, int NT, bool REV>
+template <typename T, int NT, bool REV, bool VEC>
 __global__ __launch_bounds__(kThreads) void scan_state_kernel(
     ScanDims d, const T *__restrict__ U, int64_t ub, int64_t ut, const T *__restrict__ V, int64_t vb,
     int64_t vt, const float *__restrict__ delta, const float2 *__restrict__ cs,
@@ -289,9 +321,10 @@ __global__ __launch_bounds__(kThreads) void scan_state_kernel(
     int end_api)
 {
     constexpr int LN = NT * 16 + 8;
-    __shared__ __align__(32) T Us[Q * LX];
-    __shared__ __align__(32) T Vs[Q * LN];
-    __shared__ float wt[Q];
+    __shared__ __align__(32) T Us[2][Q * LX];
+    __shared__ __align__(32) T Vs[2][Q * LN];
+    __shared__ __align__(16) float wt[2][Q];
+    __shared__ float scale[2];
 
     const int seg = blockIdx.x % d.nseg;
     const int64_t r0 = blockIdx.x / d.nseg;
@@ -307,8 +340,6 @@ __global__ __launch_bounds__(kThreads) void scan_state_kernel(
     const int64_t PN = (int64_t)d.P * d.N;
     const T *up = U + b * ub + (int64_t)h * d.P + ps * kSlice;
     const T *vp = V + b * vb + (int64_t)grp * d.N;
-    const bool au = rows_aligned(up, ub, ut, pcols, sizeof(T));
-    const bool av = rows_aligned(vp, vb, vt, d.N, sizeof(T));
 
     f32x4 S[NT];
     {
@@ -317,21 +348,37 @@ __global__ __launch_bounds__(kThreads) void scan_state_kernel(
         state_load<NT>(S, src, init_api, p, d.P, d.N);
     }
     const int c0 = seg * d.cps, c1 = c0 + d.cps < d.nc ? c0 + d.cps : d.nc;
-    for (int k = c0; k < c1; k++) {
-        const int c = REV ? c0 + c1 - 1 - k : k;
-        if (each) state_store<NT>(S, each + (bh * d.nc + c) * PN, false, p, d.P, d.N);
+    TileRegs<T, Q, kSlice, LX, kThreads, VEC> ru;
+    TileRegs<T, Q, NT * 16, LN, kThreads, VEC> rv;
+    float rw, rs;
+    const auto chunk = [&](int k) { return REV ? c0 + c1 - 1 - k : k; };
+    const auto fetch = [&](int c) {
         const int64_t t0 = (int64_t)c * Q;
         const int rows = len - t0 < 0 ? 0 : len - t0 < Q ? (int)(len - t0) : Q;
-        load_tile<T, Q, kSlice, LX, kThreads>(Us, up + t0 * ut, ut, rows, pcols, au);
-        load_tile<T, Q, NT * 16, LN, kThreads>(Vs, vp + t0 * vt, vt, rows, d.N, av);
-        const int64_t at = (bh * d.nc + c) * Q;
-        const float2 tot = cs[at + Q - 1];
+        ru.load(up + t0 * ut, ut, rows, pcols);
+        rv.load(vp + t0 * vt, vt, rows, d.N);
         if (threadIdx.x < Q) {
-            const float2 me = cs[at + threadIdx.x];
-            wt[threadIdx.x] = REV ? exp2_fast(me.x + me.y) : decay(tot, me) * delta[at + threadIdx.x];
+            const int64_t at = (bh * d.nc + c) * Q;
+            const float2 me = cs[at + threadIdx.x], tot = cs[at + Q - 1];
+            rw = REV ? exp2_fast(me.x + me.y) : decay(tot, me) * delta[at + threadIdx.x];
+            rs = exp2_fast(tot.x + tot.y);
         }
-        __syncthreads();
-        state_update<T, NT>(S, Us, Vs, wt, exp2_fast(tot.x + tot.y), 16 * w);
+    };
+    const auto put = [&](int n) {
+        ru.store(Us[n]);
+        rv.store(Vs[n]);
+        if (threadIdx.x < Q) wt[n][threadIdx.x] = rw;
+        if (threadIdx.x == 0) scale[n] = rs;
+    };
+    fetch(chunk(c0));
+    put(0);
+    __syncthreads();
+    for (int k = c0; k < c1; k++) {
+        const int n = (k - c0) & 1;
+        if (k + 1 < c1) fetch(chunk(k + 1));
+        if (each) state_store<NT>(S, each + (bh * d.nc + chunk(k)) * PN, false, p, d.P, d.N);
+        state_update<T, NT>(S, Us[n], Vs[n], wt[n], scale[n], 16 * w);
+        if (k + 1 < c1) put(n ^ 1);
         __syncthreads();
     }
     if (!end) return;
@@ -350,22 +397,28 @@ __global__ __launch_bounds__(kThreads) void scan_join_kernel(ScanDims d, const f
                                                              const float *__restrict__ own,
                                                              float *__restrict__ start)
 {
+    __shared__ float keep[kMaxSegs];
     const int64_t PN = (int64_t)d.P * d.N;
     const int64_t e = (int64_t)blockIdx.x * kThreads + threadIdx.x;
     const int64_t bh = blockIdx.y;
+    for (int seg = threadIdx.x; seg < d.nseg; seg += kThreads) {
+        const int c0 = seg * d.cps, c1 = c0 + d.cps < d.nc ? c0 + d.cps : d.nc;
+        double sum = 0.0;
+        for (int c = c0; c < c1; c++) {
+            const float2 t = cs[(bh * d.nc + c) * Q + Q - 1];
+            sum += (double)t.x + (double)t.y;
+        }
+        keep[seg] = exp2_fast((float)sum);
+    }
+    __syncthreads();
     if (e >= PN) return;
     const int n = (int)(e / d.P), p = (int)(e % d.P);
     float S = first ? first[bh * PN + (int64_t)p * d.N + n] : 0.f;
+#pragma unroll 8
     for (int k = 0; k < d.nseg; k++) {
         const int seg = REV ? d.nseg - 1 - k : k;
         start[(bh * d.nseg + seg) * PN + e] = S;
-        const int c0 = seg * d.cps, c1 = c0 + d.cps < d.nc ? c0 + d.cps : d.nc;
-        float sum = 0.f;
-        for (int c = c0; c < c1; c++) {
-            const float2 t = cs[(bh * d.nc + c) * Q + Q - 1];
-            sum += t.x + t.y;
-        }
-        S = fmaf(exp2_fast(sum), S, own[(bh * d.nseg + seg) * PN + e]);
+        S = fmaf(keep[seg], S, own[(bh * d.nseg + seg) * PN + e]);
     }
 }
 
@@ -391,7 +444,7 @@ __global__ __launch_bounds__(kThreads) void scan_join_kernel(ScanDims d, const f
 // A workgroup owns a chunk and a block of the heads of a group, whose sums for
 // dB and dC stay in registers.  Wave w owns rows 16 w .. of the 64 x 64
 // products, columns 16 w .. of dx, and a quarter of the columns n.
-template <typename T, int NT>
+template <typename T, int NT, bool VEC>
 __global__ __launch_bounds__(kThreads) void scan_grad_kernel(
     ScanDims d, int hblocks, const T *__restrict__ x, const T *__restrict__ dy,
     const T *__restrict__ Bm, const T *__restrict__ Cm, const float *__restrict__ A,
@@ -432,10 +485,8 @@ __global__ __launch_bounds__(kThreads) void scan_grad_kernel(
     {
         const T *bp = Bm + b * d.bb + (int64_t)grp * d.N;
         const T *cp = Cm + b * d.cb + (int64_t)grp * d.N;
-        load_tile<T, Q, NT * 16, LN, kThreads>(Bs, bp + t0 * d.bt, d.bt, rows, d.N,
-                                               rows_aligned(bp, d.bb, d.bt, d.N, sizeof(T)));
-        load_tile<T, Q, NT * 16, LN, kThreads>(Cs, cp + t0 * d.ct, d.ct, rows, d.N,
-                                               rows_aligned(cp, d.cb, d.ct, d.N, sizeof(T)));
+        load_tile<T, Q, NT * 16, LN, kThreads, VEC>(Bs, bp + t0 * d.bt, d.bt, rows, d.N);
+        load_tile<T, Q, NT * 16, LN, kThreads, VEC>(Cs, cp + t0 * d.ct, d.ct, rows, d.N);
     }
     __syncthreads();
     f32x4 CB[4];  // C_t.B_s, rows t = 16 w ..
@@ -498,10 +549,8 @@ __global__ __launch_bounds__(kThreads) void scan_grad_kernel(
             const T *yp = dy + b * d.T * d.H * d.P + (int64_t)h * d.P + p0;
             const int64_t yt = (int64_t)d.H * d.P;
             __syncthreads();
-            load_tile<T, Q, kSlice, LX, kThreads>(Xs, xp + t0 * d.xt, d.xt, rows, pcols,
-                                                  rows_aligned(xp, d.xb, d.xt, pcols, sizeof(T)));
-            load_tile<T, Q, kSlice, LX, kThreads>(Ys, yp + t0 * yt, yt, rows, pcols,
-                                                  rows_aligned(yp, 0, yt, pcols, sizeof(T)));
+            load_tile<T, Q, kSlice, LX, kThreads, VEC>(Xs, xp + t0 * d.xt, d.xt, rows, pcols);
+            load_tile<T, Q, kSlice, LX, kThreads, VEC>(Ys, yp + t0 * yt, yt, rows, pcols);
             __syncthreads();
 #pragma unroll
             for (int ks = 0; ks < 2; ks++) {
@@ -757,7 +806,7 @@ struct Plan {
     size_t delta, cs, own, start, S, G, parts, hsum, total;
 };
 
-constexpr int64_t kUnits = 512;  // workgroups that fill the 256 compute units twice
+constexpr int64_t kUnits = kMaxSegs;  // workgroups that fill the 256 compute units twice
 
 Plan plan_of(const sdm_scan_desc &s, bool backward)
 {
@@ -822,7 +871,7 @@ void run_prep(const ScanArgs &a, const Plan &p, float *delta, float2 *cs, hipStr
 }
 
 // With more than one segment: the state before each (in `start`).
-template <typename T, int NT, bool REV>
+template <typename T, int NT, bool VEC, bool REV>
 void run_segments(const ScanArgs &a, const Plan &p, const T *U, int64_t ub, int64_t ut, const T *V,
                   int64_t vb, int64_t vt, const float *first, const float *delta, const float2 *cs,
                   hipStream_t stream)
@@ -830,13 +879,13 @@ void run_segments(const ScanArgs &a, const Plan &p, const T *U, int64_t ub, int6
     const ScanDims &d = p.d;
     const unsigned grid = (unsigned)((int64_t)d.B * d.H * d.nps * d.nseg);
     float *own = (float *)(a.ws + p.own), *start = (float *)(a.ws + p.start);
-    scan_state_kernel<T, NT, REV><<<grid, kThreads, 0, stream>>>(
+    scan_state_kernel<T, NT, REV, VEC><<<grid, kThreads, 0, stream>>>(
         d, U, ub, ut, V, vb, vt, delta, cs, a.lengths, nullptr, 0, nullptr, own, 0);
     scan_join_kernel<REV><<<dim3((d.P * d.N + kThreads - 1) / kThreads, d.B * d.H), kThreads, 0, stream>>>(
         d, cs, first, own, start);
 }
 
-template <typename T, int NT>
+template <typename T, int NT, bool VEC>
 hipError_t forward(const ScanArgs &a, hipStream_t stream)
 {
     const Plan p = plan_of(a.d, false);
@@ -848,16 +897,16 @@ hipError_t forward(const ScanArgs &a, hipStream_t stream)
     const float *init = a.cont ? a.state : nullptr;
     int api = 1;
     if (d.nseg > 1) {
-        run_segments<T, NT, false>(a, p, x, d.xb, d.xt, Bm, d.bb, d.bt, init, delta, cs, stream);
+        run_segments<T, NT, VEC, false>(a, p, x, d.xb, d.xt, Bm, d.bb, d.bt, init, delta, cs, stream);
         init = (const float *)(a.ws + p.start);
         api = 0;
     }
-    scan_walk_kernel<T, NT><<<(unsigned)((int64_t)d.B * d.H * d.nps * d.nseg), kThreads, 0, stream>>>(
+    scan_walk_kernel<T, NT, VEC><<<(unsigned)((int64_t)d.B * d.H * d.nps * d.nseg), kThreads, 0, stream>>>(
         d, x, Bm, Cm, a.D, delta, cs, a.lengths, init, api, a.state, (T *)a.y);
     return hipGetLastError();
 }
 
-template <typename T, int NT>
+template <typename T, int NT, bool VEC>
 hipError_t backward(const ScanArgs &a, hipStream_t stream)
 {
     const Plan p = plan_of(a.d, true);
@@ -873,16 +922,16 @@ hipError_t backward(const ScanArgs &a, hipStream_t stream)
     run_prep<T>(a, p, delta, cs, stream);
     const bool split = d.nseg > 1;
     if (split)
-        run_segments<T, NT, false>(a, p, x, d.xb, d.xt, Bm, d.bb, d.bt, a.state0, delta, cs, stream);
-    scan_state_kernel<T, NT, false><<<grid, kThreads, 0, stream>>>(
+        run_segments<T, NT, VEC, false>(a, p, x, d.xb, d.xt, Bm, d.bb, d.bt, a.state0, delta, cs, stream);
+    scan_state_kernel<T, NT, false, VEC><<<grid, kThreads, 0, stream>>>(
         d, x, d.xb, d.xt, Bm, d.bb, d.bt, delta, cs, a.lengths, split ? start : a.state0,
         split ? 0 : 1, S, nullptr, 0);
     if (split)
-        run_segments<T, NT, true>(a, p, dy, yb, yt, Cm, d.cb, d.ct, a.dstateT, delta, cs, stream);
-    scan_state_kernel<T, NT, true><<<grid, kThreads, 0, stream>>>(
+        run_segments<T, NT, VEC, true>(a, p, dy, yb, yt, Cm, d.cb, d.ct, a.dstateT, delta, cs, stream);
+    scan_state_kernel<T, NT, true, VEC><<<grid, kThreads, 0, stream>>>(
         d, dy, yb, yt, Cm, d.cb, d.ct, delta, cs, a.lengths, split ? start : a.dstateT, split ? 0 : 1,
         G, a.dstate0, 1);
-    scan_grad_kernel<T, NT><<<(unsigned)((int64_t)d.B * d.nc * d.G * p.hblocks), kThreads, 0, stream>>>(
+    scan_grad_kernel<T, NT, VEC><<<(unsigned)((int64_t)d.B * d.nc * d.G * p.hblocks), kThreads, 0, stream>>>(
         d, p.hblocks, x, dy, Bm, Cm, a.A, a.D, delta, cs, a.lengths, a.d.softplus, S, G, (T *)a.dx,
         (T *)a.ddt, (T *)a.dB, (T *)a.dC, parts, hsum);
     if (p.hblocks > 1) {
@@ -895,13 +944,23 @@ hipError_t backward(const ScanArgs &a, hipStream_t stream)
     return hipGetLastError();
 }
 
+template <typename T, bool VEC>
+hipError_t dispatch_n(const ScanArgs &a, bool back, hipStream_t stream)
+{
+    // the state's columns, padded to 32, 64 or 128
+    if (a.d.N <= 32) return back ? backward<T, 2, VEC>(a, stream) : forward<T, 2, VEC>(a, stream);
+    if (a.d.N <= 64) return back ? backward<T, 4, VEC>(a, stream) : forward<T, 4, VEC>(a, stream);
+    return back ? backward<T, 8, VEC>(a, stream) : forward<T, 8, VEC>(a, stream);
+}
+
 template <typename T>
 hipError_t dispatch(const ScanArgs &a, bool back, hipStream_t stream)
 {
-    // the state's columns, padded to 32, 64 or 128
-    if (a.d.N <= 32) return back ? backward<T, 2>(a, stream) : forward<T, 2>(a, stream);
-    if (a.d.N <= 64) return back ? backward<T, 4>(a, stream) : forward<T, 4>(a, stream);
-    return back ? backward<T, 8>(a, stream) : forward<T, 8>(a, stream);
+    const sdm_scan_desc &d = a.d;
+    const bool vec = rows_on_16(a.x, d.x_batch, d.x_token, 0, d.P, sizeof(T)) &&
+                     rows_on_16(a.Bm, d.B_batch, d.B_token, 0, d.N, sizeof(T)) &&
+                     rows_on_16(a.Cm, d.C_batch, d.C_token, 0, d.N, sizeof(T));
+    return vec ? dispatch_n<T, true>(a, back, stream) : dispatch_n<T, false>(a, back, stream);
 }
 
 }  // namespace

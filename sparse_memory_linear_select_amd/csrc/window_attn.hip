@@ -82,34 +82,6 @@ __device__ __forceinline__ typename Mat<T>::Frag frag_global(const T *src, int k
     return f;
 }
 
-// Column fragment whose k order is that of two accumulator tiles: rows
-// k0 + 4 g .. + 3 and k0 + 16 + 4 g .. + 3.
-template <typename T>
-__device__ __forceinline__ typename Mat<T>::Frag frag_col_pair(const T *tile, int ld, int k0, int col0)
-{
-    const int l = threadIdx.x & 63;
-    const T *p = tile + (k0 + (l >> 4) * 4) * ld + col0 + (l & 15);
-    typename Mat<T>::Frag f;
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-        f[i] = p[i * ld];
-        f[4 + i] = p[(16 + i) * ld];
-    }
-    return f;
-}
-
-template <typename T>
-__device__ __forceinline__ typename Mat<T>::Frag pair_frag(f32x4 a, f32x4 b)
-{
-    typename Mat<T>::Frag f;
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-        f[i] = (T)a[i];
-        f[4 + i] = (T)b[i];
-    }
-    return f;
-}
-
 // The key tiles that queries [i0, i1] can see: first the sinks in front of
 // every window, then the keys from `lo` on.
 struct KeyRange {
@@ -222,7 +194,7 @@ __global__ __launch_bounds__(kThreads) void window_fwd_kernel(
         sum = sum * keep + part;
         m = mn;
         // the weights are rounded to the inputs' type for the product with V
-        const auto pa = pair_frag<T>(s[0], s[1]), pb = pair_frag<T>(s[2], s[3]);
+        const auto pa = frag_acc<T>(s[0], s[1]), pb = frag_acc<T>(s[2], s[3]);
 #pragma unroll
         for (int j = 0; j < DT; j++) {
             O[j] *= keep;
@@ -348,7 +320,7 @@ __global__ __launch_bounds__(kThreads) void window_dq_kernel(
                     s[kt][e] = see ? p * (dp[e] - dl) * d.scale : 0.f;
                 }
             }
-            const auto pa = pair_frag<T>(s[0], s[1]), pb = pair_frag<T>(s[2], s[3]);
+            const auto pa = frag_acc<T>(s[0], s[1]), pb = frag_acc<T>(s[2], s[3]);
 #pragma unroll
             for (int j = 0; j < DT; j++) {
                 O[j] = M::mma(frag_col_pair<T>(Ks, LD, 0, 16 * j), pa, O[j]);
@@ -458,7 +430,7 @@ __global__ __launch_bounds__(kThreads) void window_dkv_kernel(
                             ds[u][e] = see ? p[u][e] * (dp[e] - D[e]) * d.scale : 0.f;
                         }
                     }
-                    const auto pf = pair_frag<T>(p[0], p[1]), sf = pair_frag<T>(ds[0], ds[1]);
+                    const auto pf = frag_acc<T>(p[0], p[1]), sf = frag_acc<T>(ds[0], ds[1]);
 #pragma unroll
                     for (int n = 0; n < DT; n++) {
                         dV[n] = M::mma(frag_col_pair<T>(Gs, LD, 32 * half, 16 * n), pf, dV[n]);
@@ -533,13 +505,6 @@ WinDims dims_of(const sdm_window_desc &s)
     return d;
 }
 
-// Rows on 16 bytes: D a multiple of 8 elements, base and strides aligned.
-bool rows16(const void *p, int64_t a, int64_t b, int64_t c, int D, int esize)
-{
-    return D % 8 == 0 && (((uintptr_t)p | (uintptr_t)(a * esize) | (uintptr_t)(b * esize) |
-                           (uintptr_t)(c * esize)) & 15u) == 0;
-}
-
 struct BackPlan {
     size_t delta, parts, total;
     int nparts, ktiles;
@@ -565,9 +530,9 @@ template <typename T, int DT>
 hipError_t forward(const WindowArgs &a, hipStream_t stream)
 {
     const WinDims d = dims_of(a.d);
-    const bool vq = rows16(a.q, d.qb, d.qt, d.qh, d.D, sizeof(T));
-    const bool vk = rows16(a.k, d.kb, d.kt, d.kh, d.D, sizeof(T)) &&
-                    rows16(a.v, d.vb, d.vt, d.vh, d.D, sizeof(T));
+    const bool vq = rows_on_16(a.q, d.qb, d.qt, d.qh, d.D, sizeof(T));
+    const bool vk = rows_on_16(a.k, d.kb, d.kt, d.kh, d.D, sizeof(T)) &&
+                    rows_on_16(a.v, d.vb, d.vt, d.vh, d.D, sizeof(T));
     window_fwd_kernel<T, DT><<<(unsigned)((int64_t)d.B * d.Hq * d.nq), kThreads, 0, stream>>>(
         d, (const T *)a.q, (const T *)a.k, (const T *)a.v, (const T *)a.cache_k, (const T *)a.cache_v,
         a.pos, a.lengths, vq, vk, (T *)a.o, a.lse);
@@ -584,10 +549,10 @@ hipError_t backward(const WindowArgs &a, hipStream_t stream)
 {
     const WinDims d = dims_of(a.d);
     const BackPlan p = back_plan(a.d);
-    const bool vq = rows16(a.q, d.qb, d.qt, d.qh, d.D, sizeof(T));
-    const bool vk = rows16(a.k, d.kb, d.kt, d.kh, d.D, sizeof(T)) &&
-                    rows16(a.v, d.vb, d.vt, d.vh, d.D, sizeof(T));
-    const bool vo = rows16(a.dout, 0, 0, d.D, d.D, sizeof(T));
+    const bool vq = rows_on_16(a.q, d.qb, d.qt, d.qh, d.D, sizeof(T));
+    const bool vk = rows_on_16(a.k, d.kb, d.kt, d.kh, d.D, sizeof(T)) &&
+                    rows_on_16(a.v, d.vb, d.vt, d.vh, d.D, sizeof(T));
+    const bool vo = rows_on_16(a.dout, 0, 0, d.D, d.D, sizeof(T));
     const T *q = (const T *)a.q, *k = (const T *)a.k, *v = (const T *)a.v, *dout = (const T *)a.dout;
     float *delta = (float *)a.ws, *parts = p.nparts ? (float *)(a.ws + p.parts) : nullptr;
     const int64_t rows = (int64_t)d.B * d.T * d.Hq;
