@@ -207,8 +207,8 @@ template <typename T, int ROWS, int COLS, int LD, int THREADS, bool VEC>
 struct TileRegs {
     static constexpr int V = 16 / sizeof(T);
     static constexpr int PER = COLS / V;
-    static constexpr int N = ROWS * PER / THREADS;
-    static_assert(ROWS * PER % THREADS == 0, "whole accesses per thread");
+    static constexpr int N = (ROWS * PER + THREADS - 1) / THREADS;
+    static constexpr bool kWhole = ROWS * PER % THREADS == 0;
     Vec<T, V> v[N];
 
     __device__ __forceinline__ void load(const T *src, int64_t stride, int rows, int cols)
@@ -218,7 +218,7 @@ struct TileRegs {
         for (int u = 0; u < N; u++) {
             const int e = threadIdx.x + u * THREADS;
             const int r = e / PER, c = (e % PER) * V;
-            v[u] = s.template read<V, VEC>((uint32_t)r * (uint32_t)stride + c, r < rows ? cols - c : 0);
+            v[u] = s.template read<V, VEC>((uint32_t)r * (uint32_t)stride + c, r < rows && r < ROWS ? cols - c : 0);
         }
     }
     __device__ __forceinline__ void store(T *tile) const
@@ -226,7 +226,7 @@ struct TileRegs {
 #pragma unroll
         for (int u = 0; u < N; u++) {
             const int e = threadIdx.x + u * THREADS;
-            vstore<T, V>(tile + (e / PER) * LD + (e % PER) * V, v[u]);
+            if (kWhole || e < ROWS * PER) vstore<T, V>(tile + (e / PER) * LD + (e % PER) * V, v[u]);
         }
     }
 };

@@ -86,92 +86,106 @@ __device__ __forceinline__ float row_last(float x)
         __builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x150 | 15, 0xF, 0xF, true));
 }
 
-// One wave's part of a state: S^T, rows n = 16 j + (l / 16) * 4 + i of tile j,
-// column p of the lane.  In the caller's [P][N] layout or the workspace's [N][P].
-template <int NT>
-__device__ __forceinline__ void state_load(f32x4 (&S)[NT], const float *src, bool api, int p, int P, int N)
+// One wave's part of a state: S^T, tiles j0 .. j0 + NJ - 1 of 16 rows n, rows
+// (l / 16) * 4 + i of each, column p of the lane.  In the caller's [P][N]
+// layout or the workspace's [N][P].
+template <int NJ>
+__device__ __forceinline__ void state_load(f32x4 (&S)[NJ], const float *src, bool api, int j0, int p, int P,
+                                           int N)
 {
-    const int g = (threadIdx.x & 63) >> 4;
+    const int n0 = 16 * j0 + 4 * ((threadIdx.x & 63) >> 4);
+    const int64_t sp = api ? N : 1, sn = api ? 1 : P;
+    const float *q = src ? src + p * sp + n0 * sn : nullptr;
 #pragma unroll
-    for (int j = 0; j < NT; j++)
+    for (int j = 0; j < NJ; j++)
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-            const int n = 16 * j + 4 * g + i;
-            S[j][i] = src && p < P && n < N ? src[api ? (int64_t)p * N + n : (int64_t)n * P + p] : 0.f;
-        }
+        for (int i = 0; i < 4; i++)
+            S[j][i] = src && p < P && n0 + 16 * j + i < N ? q[(16 * j + i) * sn] : 0.f;
 }
 
-template <int NT>
-__device__ __forceinline__ void state_store(const f32x4 (&S)[NT], float *dst, bool api, int p, int P, int N)
+template <int NJ>
+__device__ __forceinline__ void state_store(const f32x4 (&S)[NJ], float *dst, bool api, int j0, int p, int P,
+                                            int N)
 {
-    const int g = (threadIdx.x & 63) >> 4;
+    const int n0 = 16 * j0 + 4 * ((threadIdx.x & 63) >> 4);
     if (p >= P) return;
+    const int64_t sp = api ? N : 1, sn = api ? 1 : P;
+    float *q = dst + p * sp + n0 * sn;
 #pragma unroll
-    for (int j = 0; j < NT; j++)
+    for (int j = 0; j < NJ; j++)
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-            const int n = 16 * j + 4 * g + i;
-            if (n < N) dst[api ? (int64_t)p * N + n : (int64_t)n * P + p] = S[j][i];
-        }
+        for (int i = 0; i < 4; i++)
+            if (n0 + 16 * j + i < N) q[(16 * j + i) * sn] = S[j][i];
 }
 
-// S <- scale S + sum_s V[s]^T (w_s U[s]) for one chunk: U [64][64], V [64][16 NT]
-// in LDS; the wave's 16 columns of U start at col0.  The weighted columns are
-// carried to 24 bits (three bfloat16 terms), so the float32 state keeps its
-// precision whatever the inputs' type.
-template <typename T, int NT>
-__device__ __forceinline__ void state_update(f32x4 (&S)[NT], const T *U, const T *V, const float *wt,
-                                             float scale, int col0)
+// The weighted columns w_s U[s], columns col0 .. + 15 of U, for state_add.
+// They are carried to 24 bits (three bfloat16 terms), so the float32 state
+// keeps its precision whatever the inputs' type.
+template <typename T>
+struct Weighted {
+    typename Mat<T>::Frag f[2][Mat<T>::kTerms];
+    __device__ __forceinline__ Weighted(const T *U, const float *wt, int col0)
+    {
+        const int g = (threadIdx.x & 63) >> 4;
+#pragma unroll
+        for (int ks = 0; ks < 2; ks++) {
+            const auto u = frag_col_pair<T>(U, LX, 32 * ks, col0);
+            const f32x4 lo = *reinterpret_cast<const f32x4 *>(wt + 32 * ks + g * 4);
+            const f32x4 hi = *reinterpret_cast<const f32x4 *>(wt + 32 * ks + 16 + g * 4);
+            split_frag<T>(__builtin_convertvector(u, f32x8) *
+                              __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7),
+                          f[ks]);
+        }
+    }
+};
+
+// S <- scale S + sum_s V[s]^T (w_s U[s]) for one chunk, tiles j0 .. of the rows n.
+template <typename T, int NJ, int LN>
+__device__ __forceinline__ void state_add(f32x4 *S, const T *V, const Weighted<T> &u, float scale, int j0)
 {
     using M = Mat<T>;
-    constexpr int LN = NT * 16 + 8;
-    const int g = (threadIdx.x & 63) >> 4;
-    typename M::Frag uw[2][M::kTerms];
 #pragma unroll
-    for (int ks = 0; ks < 2; ks++) {
-        f32x8 v;
-        const auto u = frag_col_pair<T>(U, LX, 32 * ks, col0);
-        const f32x4 lo = *reinterpret_cast<const f32x4 *>(wt + 32 * ks + g * 4);
-        const f32x4 hi = *reinterpret_cast<const f32x4 *>(wt + 32 * ks + 16 + g * 4);
-        v = __builtin_convertvector(u, f32x8) * __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-        split_frag<T>(v, uw[ks]);
-    }
-#pragma unroll
-    for (int j = 0; j < NT; j++) {
+    for (int j = 0; j < NJ; j++) {
         S[j] *= scale;
 #pragma unroll
         for (int ks = 0; ks < 2; ks++) {
-            const auto a = frag_col_pair<T>(V, LN, 32 * ks, 16 * j);
+            const auto a = frag_col_pair<T>(V, LN, 32 * ks, 16 * (j0 + j));
 #pragma unroll
-            for (int n = 0; n < M::kTerms; n++) S[j] = M::mma(a, uw[ks][n], S[j]);
+            for (int n = 0; n < M::kTerms; n++) S[j] = M::mma(a, u.f[ks][n], S[j]);
         }
     }
 }
 
 // ----------------------------------------------------------------- forward
 // A workgroup walks the chunks of one (sequence, head, slice of 64 columns,
-// segment) in order with the state in registers: wave w owns columns 16 w ..
-// of the slice, for y and for the state.  C.B and M are shared by the waves
-// through LDS.  Products are taken transposed (M^T, y^T, S^T): a lane then
+// segment) in order.  Its eight waves work in two roles, so that every SIMD
+// has two waves whose waits fall at different times: waves 0 .. 3 hold the
+// state in registers, 16 columns each, update it and hand it to the others
+// through LDS, rounded; waves 4 .. 7 compute M (shared through LDS) and y, 16
+// columns each.  Products are taken transposed (M^T, y^T, S^T): a lane then
 // holds one token and four neighbouring columns, so that a token's decay is
 // one number a lane, stores take four columns, and the state's accumulators
 // are the next product's operand as they stand.  The next chunk's tiles are on
 // their way from HBM while a chunk is worked on; with kBufs = 2 they go to a
 // second set of tiles (as long as two sets fit into 160 KB of LDS).
 template <typename T, int NT, bool VEC>
-__global__ __launch_bounds__(kThreads) void scan_walk_kernel(
+__global__ __launch_bounds__(2 * kThreads) void scan_walk_kernel(
     ScanDims d, const T *__restrict__ x, const T *__restrict__ Bm, const T *__restrict__ Cm,
     const float *__restrict__ D, const float *__restrict__ delta, const float2 *__restrict__ cs,
     const int32_t *__restrict__ lengths, const float *init, int init_api, float *state,
     T *__restrict__ y)
 {
     using M = Mat<T>;
+    using Frag = typename M::Frag;
+    using Half = typename M::Half;
     constexpr int LN = NT * 16 + 8;
-    constexpr int kBufs = sizeof(T) == 2 || NT < 8 ? 2 : 1;
+    constexpr int kBufs = sizeof(T) == 2 || NT == 2 ? 2 : 1;
+    constexpr int NF = NT / 2;
     __shared__ __align__(32) T Xs[kBufs][Q * LX];
     __shared__ __align__(32) T Bs[kBufs][Q * LN];
     __shared__ __align__(32) T Cs[kBufs][Q * LN];
     __shared__ __align__(32) T Ms[Q * LX];
+    __shared__ __align__(32) Frag Sf[kBufs][4][NF][64];
     __shared__ __align__(16) float dl[kBufs][Q], wt[kBufs][Q];
     __shared__ __align__(16) float2 cc[kBufs][Q];
 
@@ -183,16 +197,17 @@ __global__ __launch_bounds__(kThreads) void scan_walk_kernel(
     const int64_t b = bh / d.H;
     const int grp = h / (d.H / d.G);
     const int64_t len = seq_len(lengths, b, d.T);
-    const int l = threadIdx.x & 63, w = threadIdx.x >> 6, g = l >> 4, li = l & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), w = wave & 3;
+    const bool keeper = wave < 4;
+    const int l = threadIdx.x & 63, g = l >> 4, li = l & 15;
     const int pcols = d.P - ps * kSlice < kSlice ? d.P - ps * kSlice : kSlice;
     const T *xp = x + b * d.xb + (int64_t)h * d.P + ps * kSlice;
     const T *bp = Bm + b * d.bb + (int64_t)grp * d.N;
     const T *cp = Cm + b * d.cb + (int64_t)grp * d.N;
-    const bool vy = ((d.P * sizeof(T)) & (4 * sizeof(T) - 1)) == 0;
     const float Dh = D ? D[h] : 0.f;
 
-    TileRegs<T, Q, kSlice, LX, kThreads, VEC> rx;
-    TileRegs<T, Q, NT * 16, LN, kThreads, VEC> rb, rc;
+    TileRegs<T, Q, kSlice, LX, 2 * kThreads, VEC> rx;
+    TileRegs<T, Q, NT * 16, LN, 2 * kThreads, VEC> rb, rc;
     float rd;
     float2 rme, rtot;
     const auto rows_of = [&](int c) {
@@ -227,10 +242,20 @@ __global__ __launch_bounds__(kThreads) void scan_walk_kernel(
     fetch(c0);
     f32x4 S[NT];
     const int pl = ps * kSlice + 16 * w + li;
-    {
+    const auto hand_over = [&](int n) {
+#pragma unroll
+        for (int j = 0; j < NF; j++) Sf[n][w][j][l] = frag_acc<T>(S[2 * j], S[2 * j + 1]);
+    };
+    if (keeper) {
         const float *src = init;
         if (src) src += (init_api ? bh : bh * d.nseg + seg) * (int64_t)d.P * d.N;
-        state_load<NT>(S, src, init_api, pl, d.P, d.N);
+        state_load<NT>(S, src, init_api, 0, pl, d.P, d.N);
+        hand_over(0);
+    } else if (w < 2) {
+        // the two tiles right of the diagonal that products read: sources behind the tokens
+        const int t = 32 * w + li;
+        const Half zero = __builtin_convertvector(f32x4{0.f, 0.f, 0.f, 0.f}, Half);
+        *reinterpret_cast<Half *>(Ms + t * LX + 32 * w + 16 + 4 * g) = zero;
     }
     put(0);
     __syncthreads();
@@ -239,72 +264,82 @@ __global__ __launch_bounds__(kThreads) void scan_walk_kernel(
         const int64_t t0 = (int64_t)c * Q;
         const int rows = rows_of(c);
         if (c + 1 < c1) fetch(c + 1);
-        // M^T for tokens 16 w .. + 15 (columns); sources behind them are zero
-        {
-            const int t = 16 * w + li;
-            const float2 ct = cc[n][t];
+        if (keeper) {
+            const float2 tot = cc[n][Q - 1];
+            const float scale = exp2_fast(tot.x + tot.y);
+            const Weighted<T> u(Xs[n], wt[n], 16 * w);
+            state_add<T, NF, LN>(S, Bs[n], u, scale, 0);
+            __syncthreads();
+            state_add<T, NF, LN>(S + NF, Bs[n], u, scale, NF);
+            if (kBufs == 2) hand_over(n ^ 1);
+        } else {
+            // M^T: the ten 16 x 16 tiles on and under the diagonal, tokens in columns
 #pragma unroll
-            for (int st = 0; st < 4; st++) {
-                if (st > (w | 1)) break;
+            for (int k = 0; k < 3; k++) {
+                const int id = w + 4 * k;  // (0,0) (1,0) (1,1) (2,0) ..
+                if (id > 9) break;
+                const int tt = id < 1 ? 0 : id < 3 ? 1 : id < 6 ? 2 : 3, st = id - tt * (tt + 1) / 2;
+                const int t = 16 * tt + li;
                 f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-                if (st <= w) {
 #pragma unroll
-                    for (int ks = 0; ks < NT / 2; ks++)
-                        acc = M::mma(frag_row<T>(Bs[n], LN, 16 * st, 32 * ks),
-                                     frag_row<T>(Cs[n], LN, 16 * w, 32 * ks), acc);
+                for (int ks = 0; ks < NF; ks++)
+                    acc = M::mma(frag_row<T>(Bs[n], LN, 16 * st, 32 * ks),
+                                 frag_row<T>(Cs[n], LN, 16 * tt, 32 * ks), acc);
+                const float2 ct = cc[n][t];
 #pragma unroll
-                    for (int i = 0; i < 4; i++) {
-                        const int s = 16 * st + 4 * g + i;
-                        acc[i] = s <= t ? acc[i] * decay(ct, cc[n][s]) * dl[n][s] : 0.f;
-                    }
+                for (int i = 0; i < 4; i++) {
+                    const int s = 16 * st + 4 * g + i;
+                    acc[i] = s <= t ? acc[i] * decay(ct, cc[n][s]) * dl[n][s] : 0.f;
                 }
                 // the decayed scores are rounded to the inputs' type for the product with x
-                *reinterpret_cast<typename M::Half *>(Ms + t * LX + 16 * st + 4 * g) =
-                    __builtin_convertvector(acc, typename M::Half);
+                *reinterpret_cast<Half *>(Ms + t * LX + 16 * st + 4 * g) = __builtin_convertvector(acc, Half);
             }
-        }
-        __syncthreads();
-        // y^T for the wave's columns; the state is rounded to the inputs' type
-        typename M::Frag sf[NT / 2], xf[2];
+            __syncthreads();
+            // y^T for the wave's columns; the state came rounded to the inputs' type
+            Frag sf[NF], xf[2];
 #pragma unroll
-        for (int j = 0; j < NT / 2; j++) sf[j] = frag_acc<T>(S[2 * j], S[2 * j + 1]);
+            for (int j = 0; j < NF; j++) sf[j] = Sf[n][w][j][l];
 #pragma unroll
-        for (int ks = 0; ks < 2; ks++) xf[ks] = frag_col<T>(Xs[n], LX, 32 * ks, 16 * w);
-        const int p = ps * kSlice + 16 * w + 4 * g;
+            for (int ks = 0; ks < 2; ks++) xf[ks] = frag_col<T>(Xs[n], LX, 32 * ks, 16 * w);
+            const int p = ps * kSlice + 16 * w + 4 * g;
+            T *yp = y + ((b * d.T + t0 + li) * d.H + h) * d.P + p;
 #pragma unroll
-        for (int r = 0; r < 4; r++) {
-            const int t = 16 * r + li;
-            f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+            for (int r = 0; r < 4; r++) {
+                const int t = 16 * r + li;
+                f32x4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int j = 0; j < NT / 2; j++)
-                acc = M::mma(sf[j], frag_row_pair<T>(Cs[n], LN, 16 * r, 32 * j), acc);
-            const float2 ct = cc[n][t];
-            acc *= exp2_fast(ct.x + ct.y);
+                for (int j = 0; j < NF; j++)
+                    acc = M::mma(sf[j], frag_row_pair<T>(Cs[n], LN, 16 * r, 32 * j), acc);
+                const float2 ct = cc[n][t];
+                acc *= exp2_fast(ct.x + ct.y);
 #pragma unroll
-            for (int ks = 0; ks <= r / 2; ks++)
-                acc = M::mma(xf[ks], frag_row<T>(Ms, LX, 16 * r, 32 * ks), acc);
-            const auto xv = *reinterpret_cast<const typename M::Half *>(Xs[n] + t * LX + 16 * w + 4 * g);
-            acc += __builtin_convertvector(xv, f32x4) * Dh;
-            if (t >= rows) acc = f32x4{0.f, 0.f, 0.f, 0.f};
-            if (t0 + t < d.T && p < d.P) {
-                const auto out = __builtin_convertvector(acc, typename M::Half);
-                T *q = y + ((b * d.T + t0 + t) * d.H + h) * d.P + p;
-                if (vy) {
-                    *reinterpret_cast<typename M::Half *>(q) = out;
-                } else {
+                for (int ks = 0; ks <= r / 2; ks++)
+                    acc = M::mma(xf[ks], frag_row<T>(Ms, LX, 16 * r, 32 * ks), acc);
+                const auto xv = *reinterpret_cast<const Half *>(Xs[n] + t * LX + 16 * w + 4 * g);
+                acc += __builtin_convertvector(xv, f32x4) * Dh;
+                if (t >= rows) acc = f32x4{0.f, 0.f, 0.f, 0.f};
+                if (t0 + t < d.T && p < d.P) {
+                    const auto out = __builtin_convertvector(acc, Half);
+                    T *q = yp + (int64_t)(16 * r) * d.H * d.P;
+                    if constexpr (VEC) {
+                        *reinterpret_cast<Half *>(q) = out;
+                    } else {
 #pragma unroll
-                    for (int i = 0; i < 4; i++)
-                        if (p + i < d.P) q[i] = out[i];
+                        for (int i = 0; i < 4; i++)
+                            if (p + i < d.P) q[i] = out[i];
+                    }
                 }
             }
         }
-        const float2 tot = cc[n][Q - 1];
-        state_update<T, NT>(S, Xs[n], Bs[n], wt[n], exp2_fast(tot.x + tot.y), 16 * w);
-        if (kBufs == 1) __syncthreads();
+        if (kBufs == 1) {
+            __syncthreads();
+            if (keeper) hand_over(0);
+        }
         if (c + 1 < c1) put(kBufs == 2 ? n ^ 1 : 0);
         __syncthreads();
     }
-    if (seg == d.nseg - 1) state_store<NT>(S, state + bh * (int64_t)d.P * d.N, true, pl, d.P, d.N);
+    if (keeper && seg == d.nseg - 1)
+        state_store<NT>(S, state + bh * (int64_t)d.P * d.N, true, 0, pl, d.P, d.N);
 }
 
 // States alone.  Forward (REV = false): U = x, V = B, weights 2^{c_63 - c_s} D_s;
@@ -312,15 +347,17 @@ __global__ __launch_bounds__(kThreads) void scan_walk_kernel(
 // 2^{c_t}, chunks from last to first: the gradient G of the state,
 //   G <- 2^{c_63} G + sum_t 2^{c_t} C_t dy_t^T,
 // and `each` gets G behind every chunk.  `end` gets the last one: per segment
-// in the workspace's layout, or (end_api) the caller's gradient.
+// in the workspace's layout, or (end_api) the caller's gradient.  Waves w and
+// w + 4 hold the same 16 columns, each one half of the rows n.
 template <typename T, int NT, bool REV, bool VEC>
-__global__ __launch_bounds__(kThreads) void scan_state_kernel(
+__global__ __launch_bounds__(2 * kThreads) void scan_state_kernel(
     ScanDims d, const T *__restrict__ U, int64_t ub, int64_t ut, const T *__restrict__ V, int64_t vb,
     int64_t vt, const float *__restrict__ delta, const float2 *__restrict__ cs,
     const int32_t *__restrict__ lengths, const float *init, int init_api, float *each, float *end,
     int end_api)
 {
     constexpr int LN = NT * 16 + 8;
+    constexpr int NJ = NT / 2;
     __shared__ __align__(32) T Us[2][Q * LX];
     __shared__ __align__(32) T Vs[2][Q * LN];
     __shared__ __align__(16) float wt[2][Q];
@@ -334,22 +371,16 @@ __global__ __launch_bounds__(kThreads) void scan_state_kernel(
     const int64_t b = bh / d.H;
     const int grp = h / (d.H / d.G);
     const int64_t len = seq_len(lengths, b, d.T);
-    const int l = threadIdx.x & 63, w = threadIdx.x >> 6;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), w = wave & 3, j0 = (wave >> 2) * NJ;
     const int pcols = d.P - ps * kSlice < kSlice ? d.P - ps * kSlice : kSlice;
-    const int p = ps * kSlice + 16 * w + (l & 15);
+    const int p = ps * kSlice + 16 * w + (threadIdx.x & 15);
     const int64_t PN = (int64_t)d.P * d.N;
     const T *up = U + b * ub + (int64_t)h * d.P + ps * kSlice;
     const T *vp = V + b * vb + (int64_t)grp * d.N;
 
-    f32x4 S[NT];
-    {
-        const float *src = init;
-        if (src) src += (init_api ? bh : bh * d.nseg + seg) * PN;
-        state_load<NT>(S, src, init_api, p, d.P, d.N);
-    }
     const int c0 = seg * d.cps, c1 = c0 + d.cps < d.nc ? c0 + d.cps : d.nc;
-    TileRegs<T, Q, kSlice, LX, kThreads, VEC> ru;
-    TileRegs<T, Q, NT * 16, LN, kThreads, VEC> rv;
+    TileRegs<T, Q, kSlice, LX, 2 * kThreads, VEC> ru;
+    TileRegs<T, Q, NT * 16, LN, 2 * kThreads, VEC> rv;
     float rw, rs;
     const auto chunk = [&](int k) { return REV ? c0 + c1 - 1 - k : k; };
     const auto fetch = [&](int c) {
@@ -371,21 +402,28 @@ __global__ __launch_bounds__(kThreads) void scan_state_kernel(
         if (threadIdx.x == 0) scale[n] = rs;
     };
     fetch(chunk(c0));
+    f32x4 S[NJ];
+    {
+        const float *src = init;
+        if (src) src += (init_api ? bh : bh * d.nseg + seg) * PN;
+        state_load<NJ>(S, src, init_api, j0, p, d.P, d.N);
+    }
     put(0);
     __syncthreads();
     for (int k = c0; k < c1; k++) {
         const int n = (k - c0) & 1;
         if (k + 1 < c1) fetch(chunk(k + 1));
-        if (each) state_store<NT>(S, each + (bh * d.nc + chunk(k)) * PN, false, p, d.P, d.N);
-        state_update<T, NT>(S, Us[n], Vs[n], wt[n], scale[n], 16 * w);
+        if (each) state_store<NJ>(S, each + (bh * d.nc + chunk(k)) * PN, false, j0, p, d.P, d.N);
+        const Weighted<T> u(Us[n], wt[n], 16 * w);
+        state_add<T, NJ, LN>(S, Vs[n], u, scale[n], j0);
         if (k + 1 < c1) put(n ^ 1);
         __syncthreads();
     }
     if (!end) return;
     if (!end_api)
-        state_store<NT>(S, end + (bh * d.nseg + seg) * PN, false, p, d.P, d.N);
+        state_store<NJ>(S, end + (bh * d.nseg + seg) * PN, false, j0, p, d.P, d.N);
     else if (seg == (REV ? 0 : d.nseg - 1))
-        state_store<NT>(S, end + bh * PN, true, p, d.P, d.N);
+        state_store<NJ>(S, end + bh * PN, true, j0, p, d.P, d.N);
 }
 
 // Joins the segments: from each segment's own contribution (`own`, computed
@@ -879,7 +917,7 @@ void run_segments(const ScanArgs &a, const Plan &p, const T *U, int64_t ub, int6
     const ScanDims &d = p.d;
     const unsigned grid = (unsigned)((int64_t)d.B * d.H * d.nps * d.nseg);
     float *own = (float *)(a.ws + p.own), *start = (float *)(a.ws + p.start);
-    scan_state_kernel<T, NT, REV, VEC><<<grid, kThreads, 0, stream>>>(
+    scan_state_kernel<T, NT, REV, VEC><<<grid, 2 * kThreads, 0, stream>>>(
         d, U, ub, ut, V, vb, vt, delta, cs, a.lengths, nullptr, 0, nullptr, own, 0);
     scan_join_kernel<REV><<<dim3((d.P * d.N + kThreads - 1) / kThreads, d.B * d.H), kThreads, 0, stream>>>(
         d, cs, first, own, start);
@@ -901,7 +939,7 @@ hipError_t forward(const ScanArgs &a, hipStream_t stream)
         init = (const float *)(a.ws + p.start);
         api = 0;
     }
-    scan_walk_kernel<T, NT, VEC><<<(unsigned)((int64_t)d.B * d.H * d.nps * d.nseg), kThreads, 0, stream>>>(
+    scan_walk_kernel<T, NT, VEC><<<(unsigned)((int64_t)d.B * d.H * d.nps * d.nseg), 2 * kThreads, 0, stream>>>(
         d, x, Bm, Cm, a.D, delta, cs, a.lengths, init, api, a.state, (T *)a.y);
     return hipGetLastError();
 }
@@ -923,12 +961,12 @@ hipError_t backward(const ScanArgs &a, hipStream_t stream)
     const bool split = d.nseg > 1;
     if (split)
         run_segments<T, NT, VEC, false>(a, p, x, d.xb, d.xt, Bm, d.bb, d.bt, a.state0, delta, cs, stream);
-    scan_state_kernel<T, NT, false, VEC><<<grid, kThreads, 0, stream>>>(
+    scan_state_kernel<T, NT, false, VEC><<<grid, 2 * kThreads, 0, stream>>>(
         d, x, d.xb, d.xt, Bm, d.bb, d.bt, delta, cs, a.lengths, split ? start : a.state0,
         split ? 0 : 1, S, nullptr, 0);
     if (split)
         run_segments<T, NT, VEC, true>(a, p, dy, yb, yt, Cm, d.cb, d.ct, a.dstateT, delta, cs, stream);
-    scan_state_kernel<T, NT, true, VEC><<<grid, kThreads, 0, stream>>>(
+    scan_state_kernel<T, NT, true, VEC><<<grid, 2 * kThreads, 0, stream>>>(
         d, dy, yb, yt, Cm, d.cb, d.ct, delta, cs, a.lengths, split ? start : a.dstateT, split ? 0 : 1,
         G, a.dstate0, 1);
     scan_grad_kernel<T, NT, VEC><<<(unsigned)((int64_t)d.B * d.nc * d.G * p.hblocks), kThreads, 0, stream>>>(
