@@ -239,6 +239,20 @@ __device__ __forceinline__ void load_tile(T *tile, const T *src, int64_t stride,
     t.store(tile);
 }
 
+// Columns c .. c + 3 of a row of D, rounded; those from D on are not stored.
+template <typename T, bool VEC>
+__device__ __forceinline__ void store4(T *row, int c, int D, f32x4 v)
+{
+    const auto out = __builtin_convertvector(v, typename Mat<T>::Half);
+    if constexpr (VEC) {
+        if (c < D) *reinterpret_cast<typename Mat<T>::Half *>(row + c) = out;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            if (c + i < D) row[c + i] = out[i];
+    }
+}
+
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
 }  // namespace

@@ -9,6 +9,7 @@
 // sum l of 2^{s - m}, s in units of log2.
 #include "mix_internal.h"
 
+#include "lane_ops.h"
 #include "mix_device.h"
 
 namespace sdm {
@@ -82,137 +83,279 @@ __device__ __forceinline__ typename Mat<T>::Frag frag_global(const T *src, int k
     return f;
 }
 
-// The key tiles that queries [i0, i1] can see: first the sinks in front of
-// every window, then the keys from `lo` on.
-struct KeyRange {
-    int64_t lo, hi;      // keys lo .. hi
-    int64_t sink_end;    // sinks 0 .. sink_end - 1 in front of lo
-    int nsink, ntiles;
-    __device__ KeyRange(int64_t i0, int64_t i1, int64_t W, int64_t S)
+// The keys that the queries i0 .. i1 (positions) can see, as one list: the
+// sinks in front of every window, then the keys from lo on.  Entry v is a sink
+// that is always seen where v < S; jr(v) = its position - i0 (for entries in
+// front of lo some number below that of lo: they precede every query).
+struct KeyList {
+    int64_t lo;     // first key of the window part
+    int ns, total;  // sinks in front of it; entries
+    int shift;      // jr(v) = v + shift
+    __device__ KeyList(int64_t i0, int64_t i1, int64_t W, int S)
     {
         lo = i0 - W + 1 > 0 ? i0 - W + 1 : 0;
-        hi = i1;
-        sink_end = S < lo ? S : lo;
-        nsink = (int)((sink_end + kKeys - 1) / kKeys);
-        ntiles = nsink + (int)((hi - lo + kKeys) / kKeys);
+        ns = S < lo ? S : (int)lo;
+        total = ns + (int)(i1 - lo + 1);
+        shift = (int)(lo - i0) - ns;
     }
-    // first key of a tile and the end of its part
-    __device__ int64_t first(int n) const { return n < nsink ? (int64_t)n * kKeys : lo + (int64_t)(n - nsink) * kKeys; }
-    __device__ int64_t end(int n) const { return n < nsink ? sink_end : hi + 1; }
+    __device__ int64_t key(int v) const { return v < ns ? v : lo + (v - ns); }
 };
 
-template <typename T, int DT>
-__global__ __launch_bounds__(kThreads) void window_fwd_kernel(
+// What 16 neighbouring entries from v0 are to 16 neighbouring queries from ir0
+// (relative to i0): 0 none is seen, 1 some are, 2 all are.
+__device__ __forceinline__ int block_sight(int v0, int shift, int ir0, int W, int S)
+{
+    const int j0 = v0 + shift, j1 = j0 + 15, ir1 = ir0 + 15;
+    if (j0 > ir1 || (v0 >= S && j1 <= ir0 - W)) return 0;
+    return j1 <= ir0 && (j0 > ir1 - W || v0 + 15 < S) ? 2 : 1;
+}
+
+// A 64-row tile in two steps, as TileRegs, from rows given by pointers.  Every
+// access is to a row that exists: columns from D on hold the row's first ones
+// (finite numbers that meet zeros in the other operand, or columns nobody
+// stores).
+template <typename T, int COLS, int LD, bool VEC>
+struct RowRegs {
+    static constexpr int V = 16 / sizeof(T);
+    static constexpr int PER = COLS / V;
+    static constexpr int N = 64 * PER / kThreads;
+    Vec<T, V> v[N];
+
+    template <typename F>
+    __device__ __forceinline__ void load(F row_of, int D)
+    {
+#pragma unroll
+        for (int u = 0; u < N; u++) {
+            const int e = threadIdx.x + u * kThreads;
+            const int c = (e % PER) * V;
+            const T *src = row_of(e / PER);
+            if constexpr (VEC) {
+                v[u] = vload<T, V>(src + (c < D ? c : 0));
+            } else {
+#pragma unroll
+                for (int i = 0; i < V; i++) v[u].e[i] = src[c + i < D ? c + i : 0];
+            }
+        }
+    }
+    __device__ __forceinline__ void store(T *tile) const
+    {
+#pragma unroll
+        for (int u = 0; u < N; u++) {
+            const int e = threadIdx.x + u * kThreads;
+            vstore<T, V>(tile + (e / PER) * LD + (e % PER) * V, v[u]);
+        }
+    }
+};
+
+// Workgroups are dealt to the 8 XCDs in turn; a run of neighbouring indexes on
+// one XCD shares its L2.
+__device__ __forceinline__ int64_t xcd_index(int64_t id, int64_t n)
+{
+    const int64_t per = n / 8, cut = per * 8;
+    return id < cut ? (id % 8) * per + id / 8 : id;
+}
+
+__device__ __forceinline__ float pair_max(float x, int m)
+{
+    uint32_t lo, hi;
+    pair_vals(__float_as_uint(x), m, lo, hi);
+    return fmaxf(__uint_as_float(lo), __uint_as_float(hi));
+}
+
+// A wave holds QN blocks of 16 queries, over which it uses each fragment of K
+// and V twice: the same queries of two heads that share a key head (HP = 2),
+// or 32 neighbouring queries.  A workgroup is four waves: 64 queries of two
+// heads, or 64 QN queries of one.
+template <typename T, int DT, int QN, int HP, bool VEC, bool CACHE>
+__global__ __launch_bounds__(kThreads, sizeof(T) == 2 && DT <= 8 ? 2 : 1) void window_fwd_kernel(
     WinDims d, const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v,
     const T *__restrict__ ck, const T *__restrict__ cv, const int64_t *__restrict__ pos,
-    const int32_t *__restrict__ lengths, bool vq, bool vk, T *__restrict__ o, float *__restrict__ lse)
+    const int32_t *__restrict__ lengths, T *__restrict__ o, float *__restrict__ lse)
 {
     using M = Mat<T>;
+    using Half = typename M::Half;
     constexpr int LD = DT * 16 + 8;
-    __shared__ __align__(32) T Ks[kKeys * LD];
-    __shared__ __align__(32) T Vs[kKeys * LD];
+    constexpr int QR = HP == 2 ? 16 : 16 * QN;   // queries of a wave
+    constexpr int kBufs = 4 * 64 * LD * (int)sizeof(T) <= 160 * 1024 ? 2 : 1;
+    __shared__ __align__(32) T Ks[kBufs][kKeys * LD];
+    __shared__ __align__(32) T Vs[kBufs][kKeys * LD];
 
-    const int qt = blockIdx.x % d.nq;
-    const int64_t bh = blockIdx.x / d.nq;
-    const int h = (int)(bh % d.Hq);
-    const int64_t b = bh / d.Hq;
-    const int hk = h / (d.Hq / d.Hk);
+    const int64_t blk = xcd_index(blockIdx.x, gridDim.x);
+    const int qt = (int)(blk % d.nq);
+    const int64_t bh = blk / d.nq;
+    const int h0 = (int)(bh % (d.Hq / HP)) * HP;
+    const int64_t b = bh / (d.Hq / HP);
+    const int hk = h0 / (d.Hq / d.Hk);
     const int64_t len = seq_len(lengths, b, d.T);
-    const int64_t p0 = seq_pos(pos, b);
-    const int64_t t0 = (int64_t)qt * kRows;
-    const int l = threadIdx.x & 63, w = threadIdx.x >> 6, g = l >> 4;
-    const int64_t t = t0 + 16 * w + (l & 15);     // the lane's query
-    T *op = o + ((b * d.T + t) * d.Hq + h) * d.D;
-    if (t0 >= len) {
-        if (t < d.T) {
-            for (int c = g; c < d.D; c += 4) op[c] = (T)0.f;
-            if (g == 0) lse[(b * d.T + t) * d.Hq + h] = 0.f;
-        }
-        return;
+    const int64_t p0 = CACHE ? seq_pos(pos, b) : 0;
+    const int64_t t0 = (int64_t)qt * 4 * QR;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int l = threadIdx.x & 63, g = l >> 4;
+    const int W = (int)d.W, S = d.S;
+    int ir[QN];                  // the lane's queries, relative to t0
+    int64_t at[QN];              // their rows of o and lse
+#pragma unroll
+    for (int u = 0; u < QN; u++) {
+        ir[u] = QR * w + (HP == 2 ? 0 : 16 * u) + (l & 15);
+        at[u] = (b * d.T + t0 + ir[u]) * d.Hq + h0 + (HP == 2 ? u : 0);
     }
-    const int64_t i = p0 + t;
-    const bool live = t < len;
-    const T *qrow = live ? q + b * d.qb + t * d.qt + h * d.qh : nullptr;
-    typename M::Frag qf[DT / 2];
+    f32x4 O[QN][DT];
+    float m[QN], sum[QN];
 #pragma unroll
-    for (int ks = 0; ks < DT / 2; ks++) qf[ks] = frag_global<T>(qrow, 32 * ks + 8 * g, d.D, vq);
-
-    f32x4 O[DT];
+    for (int u = 0; u < QN; u++) {
+        m[u] = -INFINITY;
+        sum[u] = 0.f;
 #pragma unroll
-    for (int j = 0; j < DT; j++) O[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    float m = -INFINITY, sum = 0.f;
-    const int64_t last = (t0 + kRows < len ? t0 + kRows : len) - 1;
-    const KeyRange kr(p0 + t0, p0 + last, d.W, d.S);
-    const T *kn = k + b * d.kb + hk * d.kh, *vn = v + b * d.vb + hk * d.vh;
-    for (int n = 0; n < kr.ntiles; n++) {
-        const int64_t j0 = kr.first(n), jend = kr.end(n);
-        __syncthreads();
-        load_rows<T, DT * 16, LD>(Ks, [&](int r) -> const T * {
-            const int64_t j = j0 + r;
-            if (j >= jend) return nullptr;
-            return j >= p0 ? kn + (j - p0) * d.kt
-                           : ck + ((b * d.cap + cache_slot(j, d.S, d.W)) * d.Hk + hk) * d.D;
-        }, d.D, vk);
-        load_rows<T, DT * 16, LD>(Vs, [&](int r) -> const T * {
-            const int64_t j = j0 + r;
-            if (j >= jend) return nullptr;
-            return j >= p0 ? vn + (j - p0) * d.vt
-                           : cv + ((b * d.cap + cache_slot(j, d.S, d.W)) * d.Hk + hk) * d.D;
-        }, d.D, vk);
-        __syncthreads();
-        f32x4 s[4];
-        float top = -INFINITY;
+        for (int j = 0; j < DT; j++) O[u][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+    if (t0 < len) {
+        typename M::Frag qf[QN][DT / 2];
 #pragma unroll
-        for (int kt = 0; kt < 4; kt++) {
-            s[kt] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int u = 0; u < QN; u++) {
+            const T *row = t0 + ir[u] < len ? q + b * d.qb + (t0 + ir[u]) * d.qt +
+                                                  (h0 + (HP == 2 ? u : 0)) * d.qh
+                                            : nullptr;
 #pragma unroll
-            for (int ks = 0; ks < DT / 2; ks++)
-                s[kt] = M::mma(frag_row<T>(Ks, LD, 16 * kt, 32 * ks), qf[ks], s[kt]);
-#pragma unroll
-            for (int e = 0; e < 4; e++) {
-                const int64_t j = j0 + 16 * kt + 4 * g + e;
-                const bool see = j < jend && j <= i && (i - j < d.W || j < d.S);
-                s[kt][e] = see ? s[kt][e] * d.c2 : -INFINITY;
-                top = fmaxf(top, s[kt][e]);
-            }
+            for (int ks = 0; ks < DT / 2; ks++) qf[u][ks] = frag_global<T>(row, 32 * ks + 8 * g, d.D, VEC);
         }
-        top = fmaxf(top, __shfl_xor(top, 16));
-        top = fmaxf(top, __shfl_xor(top, 32));
-        const float mn = fmaxf(m, top);
-        const float base = mn == -INFINITY ? 0.f : mn;
-        const float keep = exp2_fast(m - base);
-        float part = 0.f;
+        const int64_t last = (t0 + 4 * QR < len ? t0 + 4 * QR : len) - 1;
+        const KeyList kl(p0 + t0, p0 + last, d.W, S);
+        const int nt = (kl.total + kKeys - 1) / kKeys;
+        const T *kn = k + b * d.kb + hk * d.kh, *vn = v + b * d.vb + hk * d.vh;
+        RowRegs<T, DT * 16, LD, VEC> rk, rv;
+        const auto fetch = [&](int n) {
+            const auto key = [&](int r) {
+                const int e = n * kKeys + r;
+                return kl.key(e < kl.total ? e : kl.total - 1);
+            };
+            rk.load([&](int r) {
+                const int64_t j = key(r);
+                if (CACHE && j < p0) return ck + ((b * d.cap + cache_slot(j, S, W)) * d.Hk + hk) * d.D;
+                return kn + (j - p0) * d.kt;
+            }, d.D);
+            rv.load([&](int r) {
+                const int64_t j = key(r);
+                if (CACHE && j < p0) return cv + ((b * d.cap + cache_slot(j, S, W)) * d.Hk + hk) * d.D;
+                return vn + (j - p0) * d.vt;
+            }, d.D);
+        };
+        fetch(0);
+        rk.store(Ks[0]);
+        rv.store(Vs[0]);
+        __syncthreads();
+        for (int n = 0; n < nt; n++) {
+            const int buf = kBufs == 2 ? n & 1 : 0;
+            if (n + 1 < nt) fetch(n + 1);
+            const int v0 = n * kKeys;
+            int sight[QN][4];
+            bool any = false;
 #pragma unroll
-        for (int kt = 0; kt < 4; kt++)
+            for (int u = 0; u < QN; u++)
 #pragma unroll
-            for (int e = 0; e < 4; e++) {
-                s[kt][e] = exp2_fast(s[kt][e] - base);
-                part += s[kt][e];
+                for (int kt = 0; kt < 4; kt++) {
+                    sight[u][kt] = HP == 2 && u ? sight[0][kt]
+                                                : block_sight(v0 + 16 * kt, kl.shift,
+                                                              QR * w + (HP == 2 ? 0 : 16 * u), W, S);
+                    any = any || sight[u][kt];
+                }
+            if (any) {
+                f32x4 s[QN][4];
+#pragma unroll
+                for (int kt = 0; kt < 4; kt++) {
+                    bool need = false;
+#pragma unroll
+                    for (int u = 0; u < QN; u++) {
+                        s[u][kt] = f32x4{0.f, 0.f, 0.f, 0.f};
+                        need = need || sight[u][kt];
+                    }
+                    if (need)
+#pragma unroll
+                        for (int ks = 0; ks < DT / 2; ks++) {
+                            const auto a = frag_row<T>(Ks[buf], LD, 16 * kt, 32 * ks);
+#pragma unroll
+                            for (int u = 0; u < QN; u++) s[u][kt] = M::mma(a, qf[u][ks], s[u][kt]);
+                        }
+                }
+                typename M::Frag pf[QN][2];
+#pragma unroll
+                for (int u = 0; u < QN; u++) {
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int kt = 0; kt < 4; kt++) {
+                        if (sight[u][kt] == 2) {
+                            s[u][kt] *= d.c2;
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 4; e++) {
+                                const int ve = v0 + 16 * kt + 4 * g + e, jr = ve + kl.shift;
+                                const bool see = jr <= ir[u] && (ve < S || jr > ir[u] - W);
+                                s[u][kt][e] = see ? s[u][kt][e] * d.c2 : -INFINITY;
+                            }
+                        }
+#pragma unroll
+                        for (int e = 0; e < 4; e++) top = fmaxf(top, s[u][kt][e]);
+                    }
+                    top = pair_max(pair_max(top, 16), 32);
+                    // The sums are held relative to m, which follows the maximum only where
+                    // it has grown by more than 2^8: weights up to 2^8 lose nothing.
+                    if (__any(top > m[u] + 8.f)) {
+                        const float mn = fmaxf(m[u], top);
+                        const float keep = mn == -INFINITY ? 0.f : exp2_fast(m[u] - mn);
+                        m[u] = mn;
+                        sum[u] *= keep;
+#pragma unroll
+                        for (int j = 0; j < DT; j++) O[u][j] *= keep;
+                    }
+                    const float base = m[u] == -INFINITY ? 0.f : m[u];
+#pragma unroll
+                    for (int kt = 0; kt < 4; kt++)
+#pragma unroll
+                        for (int e = 0; e < 4; e++) {
+                            s[u][kt][e] = exp2_fast(s[u][kt][e] - base);
+                            sum[u] += s[u][kt][e];
+                        }
+                    // the weights are rounded to the inputs' type for the product with V
+                    pf[u][0] = frag_acc<T>(s[u][0], s[u][1]);
+                    pf[u][1] = frag_acc<T>(s[u][2], s[u][3]);
+                }
+#pragma unroll
+                for (int kp = 0; kp < 2; kp++) {
+                    bool need = false;
+#pragma unroll
+                    for (int u = 0; u < QN; u++) need = need || sight[u][2 * kp] || sight[u][2 * kp + 1];
+                    if (!need) continue;
+#pragma unroll
+                    for (int j = 0; j < DT; j++) {
+                        const auto a = frag_col_pair<T>(Vs[buf], LD, 32 * kp, 16 * j);
+#pragma unroll
+                        for (int u = 0; u < QN; u++) O[u][j] = M::mma(a, pf[u][kp], O[u][j]);
+                    }
+                }
             }
-        part += __shfl_xor(part, 16);
-        part += __shfl_xor(part, 32);
-        sum = sum * keep + part;
-        m = mn;
-        // the weights are rounded to the inputs' type for the product with V
-        const auto pa = frag_acc<T>(s[0], s[1]), pb = frag_acc<T>(s[2], s[3]);
+            if (kBufs == 1) __syncthreads();
+            if (n + 1 < nt) {
+                rk.store(Ks[kBufs == 2 ? buf ^ 1 : 0]);
+                rv.store(Vs[kBufs == 2 ? buf ^ 1 : 0]);
+            }
+            __syncthreads();
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < QN; u++) {
+        const int64_t t = t0 + ir[u];
+        float all = xor_add(xor_add(sum[u], 16), 32);
+        if (t >= d.T) continue;
+        const bool live = t < len;
+        const float inv = live ? 1.f / all : 0.f;
+        T *op = o + at[u] * d.D;
 #pragma unroll
         for (int j = 0; j < DT; j++) {
-            O[j] *= keep;
-            O[j] = M::mma(frag_col_pair<T>(Vs, LD, 0, 16 * j), pa, O[j]);
-            O[j] = M::mma(frag_col_pair<T>(Vs, LD, 32, 16 * j), pb, O[j]);
+            const int c = 16 * j + 4 * g;
+            const f32x4 r = live ? O[u][j] * inv : f32x4{0.f, 0.f, 0.f, 0.f};
+            store4<T, VEC>(op, c, d.D, r);
         }
+        if (g == 0) lse[at[u]] = live ? (m[u] + log2f(all)) * 0.6931471805599453f : 0.f;
     }
-    if (t >= d.T) return;
-    const float inv = live ? 1.f / sum : 0.f;
-#pragma unroll
-    for (int j = 0; j < DT; j++)
-#pragma unroll
-        for (int e = 0; e < 4; e++) {
-            const int c = 16 * j + 4 * g + e;
-            if (c < d.D) op[c] = (T)(live ? O[j][e] * inv : 0.f);
-        }
-    if (g == 0)
-        lse[(b * d.T + t) * d.Hq + h] = live ? (m + log2f(sum)) * 0.6931471805599453f : 0.f;
 }
 
 // The call's last tokens into the rolling cache: the sinks, and the newest
@@ -255,6 +398,25 @@ __global__ __launch_bounds__(kThreads) void window_delta_kernel(int64_t rows, in
     for (int m = 1; m < 64; m <<= 1) s += __shfl_xor(s, m);
     if (l == 0) delta[r] = s;
 }
+
+// The key tiles that queries [i0, i1] can see: first the sinks in front of
+// every window, then the keys from `lo` on.
+struct KeyRange {
+    int64_t lo, hi;      // keys lo .. hi
+    int64_t sink_end;    // sinks 0 .. sink_end - 1 in front of lo
+    int nsink, ntiles;
+    __device__ KeyRange(int64_t i0, int64_t i1, int64_t W, int64_t S)
+    {
+        lo = i0 - W + 1 > 0 ? i0 - W + 1 : 0;
+        hi = i1;
+        sink_end = S < lo ? S : lo;
+        nsink = (int)((sink_end + kKeys - 1) / kKeys);
+        ntiles = nsink + (int)((hi - lo + kKeys) / kKeys);
+    }
+    // first key of a tile and the end of its part
+    __device__ int64_t first(int n) const { return n < nsink ? (int64_t)n * kKeys : lo + (int64_t)(n - nsink) * kKeys; }
+    __device__ int64_t end(int n) const { return n < nsink ? sink_end : hi + 1; }
+};
 
 // dQ^T += K^T dS^T over the keys, with P^T recomputed from lse.
 template <typename T, int DT>
@@ -526,16 +688,25 @@ BackPlan back_plan(const sdm_window_desc &s)
     return p;
 }
 
-template <typename T, int DT>
+template <typename T, int DT, bool VEC>
 hipError_t forward(const WindowArgs &a, hipStream_t stream)
 {
-    const WinDims d = dims_of(a.d);
-    const bool vq = rows_on_16(a.q, d.qb, d.qt, d.qh, d.D, sizeof(T));
-    const bool vk = rows_on_16(a.k, d.kb, d.kt, d.kh, d.D, sizeof(T)) &&
-                    rows_on_16(a.v, d.vb, d.vt, d.vh, d.D, sizeof(T));
-    window_fwd_kernel<T, DT><<<(unsigned)((int64_t)d.B * d.Hq * d.nq), kThreads, 0, stream>>>(
-        d, (const T *)a.q, (const T *)a.k, (const T *)a.v, (const T *)a.cache_k, (const T *)a.cache_v,
-        a.pos, a.lengths, vq, vk, (T *)a.o, a.lse);
+    WinDims d = dims_of(a.d);
+    constexpr int QN = DT == 16 ? 1 : 2;  // D = 256 fills the registers with one
+    const auto run = [&](auto kernel, int hp, int queries) {
+        d.nq = (int)((d.T + queries - 1) / queries);
+        kernel<<<(unsigned)((int64_t)d.B * (d.Hq / hp) * d.nq), kThreads, 0, stream>>>(
+            d, (const T *)a.q, (const T *)a.k, (const T *)a.v, (const T *)a.cache_k,
+            (const T *)a.cache_v, a.pos, a.lengths, (T *)a.o, a.lse);
+    };
+    // heads in pairs where an even number of them shares a key head
+    const bool pairs = QN == 2 && (d.Hq / d.Hk) % 2 == 0;
+    if (a.pos)
+        pairs ? run(window_fwd_kernel<T, DT, QN, QN, VEC, true>, 2, 64)
+              : run(window_fwd_kernel<T, DT, QN, 1, VEC, true>, 1, 64 * QN);
+    else
+        pairs ? run(window_fwd_kernel<T, DT, QN, QN, VEC, false>, 2, 64)
+              : run(window_fwd_kernel<T, DT, QN, 1, VEC, false>, 1, 64 * QN);
     if (a.cache_k) {
         const int64_t span = (d.S < d.T ? d.S : d.T) + (d.W < d.T ? d.W : d.T);
         window_cache_kernel<T><<<(unsigned)(span * d.B), kThreads, 0, stream>>>(
@@ -574,14 +745,25 @@ hipError_t backward(const WindowArgs &a, hipStream_t stream)
     return hipGetLastError();
 }
 
+template <typename T, bool VEC>
+hipError_t dispatch_d(const WindowArgs &a, bool back, hipStream_t stream)
+{
+    // head columns padded to 32, 64, 128 or 256
+    if (a.d.D <= 32) return back ? backward<T, 2>(a, stream) : forward<T, 2, VEC>(a, stream);
+    if (a.d.D <= 64) return back ? backward<T, 4>(a, stream) : forward<T, 4, VEC>(a, stream);
+    if (a.d.D <= 128) return back ? backward<T, 8>(a, stream) : forward<T, 8, VEC>(a, stream);
+    return back ? backward<T, 16>(a, stream) : forward<T, 16, VEC>(a, stream);
+}
+
 template <typename T>
 hipError_t dispatch(const WindowArgs &a, bool back, hipStream_t stream)
 {
-    // head columns padded to 32, 64, 128 or 256
-    if (a.d.D <= 32) return back ? backward<T, 2>(a, stream) : forward<T, 2>(a, stream);
-    if (a.d.D <= 64) return back ? backward<T, 4>(a, stream) : forward<T, 4>(a, stream);
-    if (a.d.D <= 128) return back ? backward<T, 8>(a, stream) : forward<T, 8>(a, stream);
-    return back ? backward<T, 16>(a, stream) : forward<T, 16>(a, stream);
+    const sdm_window_desc &d = a.d;
+    const bool vec = d.D % 8 == 0 &&
+                     rows_on_16(a.q, d.q_batch, d.q_token, d.q_head, d.D, sizeof(T)) &&
+                     rows_on_16(a.k, d.k_batch, d.k_token, d.k_head, d.D, sizeof(T)) &&
+                     rows_on_16(a.v, d.v_batch, d.v_token, d.v_head, d.D, sizeof(T));
+    return vec ? dispatch_d<T, true>(a, back, stream) : dispatch_d<T, false>(a, back, stream);
 }
 
 }  // namespace
