@@ -382,142 +382,182 @@ __global__ __launch_bounds__(kThreads) void window_cache_kernel(
     }
 }
 
-// delta[b][t][h] = sum_c dout o: what the softmax's backward subtracts.
-template <typename T>
-__global__ __launch_bounds__(kThreads) void window_delta_kernel(int64_t rows, int D,
-                                                                const T *__restrict__ o,
-                                                                const T *__restrict__ dout,
-                                                                float *__restrict__ delta)
-{
-    const int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    const int l = threadIdx.x & 63;
-    if (r >= rows) return;
-    float s = 0.f;
-    for (int c = l; c < D; c += 64) s = fmaf((float)o[r * D + c], (float)dout[r * D + c], s);
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) s += __shfl_xor(s, m);
-    if (l == 0) delta[r] = s;
-}
-
-// The key tiles that queries [i0, i1] can see: first the sinks in front of
-// every window, then the keys from `lo` on.
-struct KeyRange {
-    int64_t lo, hi;      // keys lo .. hi
-    int64_t sink_end;    // sinks 0 .. sink_end - 1 in front of lo
-    int nsink, ntiles;
-    __device__ KeyRange(int64_t i0, int64_t i1, int64_t W, int64_t S)
-    {
-        lo = i0 - W + 1 > 0 ? i0 - W + 1 : 0;
-        hi = i1;
-        sink_end = S < lo ? S : lo;
-        nsink = (int)((sink_end + kKeys - 1) / kKeys);
-        ntiles = nsink + (int)((hi - lo + kKeys) / kKeys);
-    }
-    // first key of a tile and the end of its part
-    __device__ int64_t first(int n) const { return n < nsink ? (int64_t)n * kKeys : lo + (int64_t)(n - nsink) * kKeys; }
-    __device__ int64_t end(int n) const { return n < nsink ? sink_end : hi + 1; }
-};
-
-// dQ^T += K^T dS^T over the keys, with P^T recomputed from lse.
-template <typename T, int DT>
-__global__ __launch_bounds__(kThreads) void window_dq_kernel(
+// dQ^T += K^T dS^T over the keys, with P^T recomputed from lse and
+// dS = P (dP - delta) scale, dP^T = V dO^T, delta = sum_c dO o (also left in
+// the workspace for the other kernel).  Blocks and tiles as in the forward.
+template <typename T, int DT, int QN, int HP, bool VEC>
+__global__ __launch_bounds__(kThreads, sizeof(T) == 2 && DT <= 8 ? 2 : 1) void window_dq_kernel(
     WinDims d, const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v,
-    const T *__restrict__ dout, const float *__restrict__ lse, const float *__restrict__ delta,
-    const int32_t *__restrict__ lengths, bool vq, bool vk, bool vo, T *__restrict__ dq)
+    const T *__restrict__ o, const T *__restrict__ dout, const float *__restrict__ lse,
+    const int32_t *__restrict__ lengths, float *__restrict__ delta, T *__restrict__ dq)
 {
     using M = Mat<T>;
     constexpr int LD = DT * 16 + 8;
-    __shared__ __align__(32) T Ks[kKeys * LD];
-    __shared__ __align__(32) T Vs[kKeys * LD];
+    constexpr int QR = HP == 2 ? 16 : 16 * QN;
+    constexpr int kBufs = 4 * 64 * LD * (int)sizeof(T) <= 160 * 1024 ? 2 : 1;
+    __shared__ __align__(32) T Ks[kBufs][kKeys * LD];
+    __shared__ __align__(32) T Vs[kBufs][kKeys * LD];
 
-    const int qt = blockIdx.x % d.nq;
-    const int64_t bh = blockIdx.x / d.nq;
-    const int h = (int)(bh % d.Hq);
-    const int64_t b = bh / d.Hq;
-    const int hk = h / (d.Hq / d.Hk);
+    const int64_t blk = xcd_index(blockIdx.x, gridDim.x);
+    const int qt = (int)(blk % d.nq);
+    const int64_t bh = blk / d.nq;
+    const int h0 = (int)(bh % (d.Hq / HP)) * HP;
+    const int64_t b = bh / (d.Hq / HP);
+    const int hk = h0 / (d.Hq / d.Hk);
     const int64_t len = seq_len(lengths, b, d.T);
-    const int64_t t0 = (int64_t)qt * kRows;
-    const int l = threadIdx.x & 63, w = threadIdx.x >> 6, g = l >> 4;
-    const int64_t i = t0 + 16 * w + (l & 15);
-    T *op = dq + ((b * d.T + i) * d.Hq + h) * d.D;
-    const bool live = i < len;
-    f32x4 O[DT];
+    const int64_t t0 = (int64_t)qt * 4 * QR;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int l = threadIdx.x & 63, g = l >> 4;
+    const int W = (int)d.W, S = d.S;
+    int ir[QN];
+    int64_t at[QN];
+    f32x4 O[QN][DT];
 #pragma unroll
-    for (int j = 0; j < DT; j++) O[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int u = 0; u < QN; u++) {
+        ir[u] = QR * w + (HP == 2 ? 0 : 16 * u) + (l & 15);
+        at[u] = (b * d.T + t0 + ir[u]) * d.Hq + h0 + (HP == 2 ? u : 0);
+#pragma unroll
+        for (int j = 0; j < DT; j++) O[u][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
     if (t0 < len) {
-        const T *qrow = live ? q + b * d.qb + i * d.qt + h * d.qh : nullptr;
-        const T *grow = live ? dout + ((b * d.T + i) * d.Hq + h) * d.D : nullptr;
-        typename M::Frag qf[DT / 2], gf[DT / 2];
+        typename M::Frag qf[QN][DT / 2], gf[QN][DT / 2];
+        float L[QN], dl[QN];
 #pragma unroll
-        for (int ks = 0; ks < DT / 2; ks++) {
-            qf[ks] = frag_global<T>(qrow, 32 * ks + 8 * g, d.D, vq);
-            gf[ks] = frag_global<T>(grow, 32 * ks + 8 * g, d.D, vo);
+        for (int u = 0; u < QN; u++) {
+            const bool live = t0 + ir[u] < len;
+            const T *row = live ? q + b * d.qb + (t0 + ir[u]) * d.qt + (h0 + (HP == 2 ? u : 0)) * d.qh
+                                : nullptr;
+            const T *grow = live ? dout + at[u] * d.D : nullptr;
+            const T *orow = live ? o + at[u] * d.D : nullptr;
+            float s = 0.f;
+#pragma unroll
+            for (int ks = 0; ks < DT / 2; ks++) {
+                qf[u][ks] = frag_global<T>(row, 32 * ks + 8 * g, d.D, VEC);
+                gf[u][ks] = frag_global<T>(grow, 32 * ks + 8 * g, d.D, VEC);
+                const auto of = frag_global<T>(orow, 32 * ks + 8 * g, d.D, VEC);
+#pragma unroll
+                for (int i = 0; i < 8; i++) s = fmaf((float)gf[u][ks][i], (float)of[i], s);
+            }
+            dl[u] = xor_add(xor_add(s, 16), 32);
+            if (live && g == 0) delta[at[u]] = dl[u];
+            L[u] = live ? lse[at[u]] * 1.4426950408889634f : 0.f;
         }
-        const float L = live ? lse[(b * d.T + i) * d.Hq + h] * 1.4426950408889634f : 0.f;
-        const float dl = live ? delta[(b * d.T + i) * d.Hq + h] : 0.f;
-        const int64_t last = (t0 + kRows < len ? t0 + kRows : len) - 1;
-        const KeyRange kr(t0, last, d.W, d.S);
+        const int64_t last = (t0 + 4 * QR < len ? t0 + 4 * QR : len) - 1;
+        const KeyList kl(t0, last, d.W, S);
+        const int nt = (kl.total + kKeys - 1) / kKeys;
         const T *kn = k + b * d.kb + hk * d.kh, *vn = v + b * d.vb + hk * d.vh;
-        for (int n = 0; n < kr.ntiles; n++) {
-            const int64_t j0 = kr.first(n), jend = kr.end(n);
-            __syncthreads();
-            load_rows<T, DT * 16, LD>(Ks, [&](int r) { return j0 + r < jend ? kn + (j0 + r) * d.kt : nullptr; }, d.D, vk);
-            load_rows<T, DT * 16, LD>(Vs, [&](int r) { return j0 + r < jend ? vn + (j0 + r) * d.vt : nullptr; }, d.D, vk);
-            __syncthreads();
-            f32x4 s[4];
+        RowRegs<T, DT * 16, LD, VEC> rk, rv;
+        const auto fetch = [&](int n) {
+            const auto key = [&](int r) {
+                const int e = n * kKeys + r;
+                return kl.key(e < kl.total ? e : kl.total - 1);
+            };
+            rk.load([&](int r) { return kn + key(r) * d.kt; }, d.D);
+            rv.load([&](int r) { return vn + key(r) * d.vt; }, d.D);
+        };
+        fetch(0);
+        rk.store(Ks[0]);
+        rv.store(Vs[0]);
+        __syncthreads();
+        for (int n = 0; n < nt; n++) {
+            const int buf = kBufs == 2 ? n & 1 : 0;
+            if (n + 1 < nt) fetch(n + 1);
+            const int v0 = n * kKeys;
 #pragma unroll
-            for (int kt = 0; kt < 4; kt++) {
-                f32x4 dp = {0.f, 0.f, 0.f, 0.f};
-                s[kt] = dp;
+            for (int kp = 0; kp < 2; kp++) {
+                int sight[QN][2];
+                bool any = false;
 #pragma unroll
-                for (int ks = 0; ks < DT / 2; ks++) {
-                    s[kt] = M::mma(frag_row<T>(Ks, LD, 16 * kt, 32 * ks), qf[ks], s[kt]);
-                    dp = M::mma(frag_row<T>(Vs, LD, 16 * kt, 32 * ks), gf[ks], dp);
+                for (int u = 0; u < QN; u++)
+#pragma unroll
+                    for (int e = 0; e < 2; e++) {
+                        sight[u][e] = HP == 2 && u ? sight[0][e]
+                                                   : block_sight(v0 + 32 * kp + 16 * e, kl.shift,
+                                                                 QR * w + (HP == 2 ? 0 : 16 * u), W, S);
+                        any = any || sight[u][e];
+                    }
+                if (!any) continue;
+                f32x4 s[QN][2], dp[QN][2];
+#pragma unroll
+                for (int kt = 0; kt < 2; kt++) {
+#pragma unroll
+                    for (int u = 0; u < QN; u++) s[u][kt] = dp[u][kt] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int ks = 0; ks < DT / 2; ks++) {
+                        const auto ka = frag_row<T>(Ks[buf], LD, 32 * kp + 16 * kt, 32 * ks);
+                        const auto va = frag_row<T>(Vs[buf], LD, 32 * kp + 16 * kt, 32 * ks);
+#pragma unroll
+                        for (int u = 0; u < QN; u++) {
+                            s[u][kt] = M::mma(ka, qf[u][ks], s[u][kt]);
+                            dp[u][kt] = M::mma(va, gf[u][ks], dp[u][kt]);
+                        }
+                    }
+                }
+                typename M::Frag sf[QN];
+#pragma unroll
+                for (int u = 0; u < QN; u++) {
+#pragma unroll
+                    for (int kt = 0; kt < 2; kt++)
+#pragma unroll
+                        for (int e = 0; e < 4; e++) {
+                            const float p = exp2_fast(fmaf(s[u][kt][e], d.c2, -L[u]));
+                            float ds = p * (dp[u][kt][e] - dl[u]) * d.scale;
+                            if (sight[u][kt] != 2) {
+                                const int ve = v0 + 32 * kp + 16 * kt + 4 * g + e, jr = ve + kl.shift;
+                                ds = jr <= ir[u] && (ve < S || jr > ir[u] - W) ? ds : 0.f;
+                            }
+                            s[u][kt][e] = ds;
+                        }
+                    // dS is rounded to the inputs' type for the product with K
+                    sf[u] = frag_acc<T>(s[u][0], s[u][1]);
                 }
 #pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    const int64_t j = j0 + 16 * kt + 4 * g + e;
-                    const bool see = live && j < jend && j <= i && (i - j < d.W || j < d.S);
-                    const float p = exp2_fast(fmaf(s[kt][e], d.c2, -L));
-                    s[kt][e] = see ? p * (dp[e] - dl) * d.scale : 0.f;
+                for (int j = 0; j < DT; j++) {
+                    const auto a = frag_col_pair<T>(Ks[buf], LD, 32 * kp, 16 * j);
+#pragma unroll
+                    for (int u = 0; u < QN; u++) O[u][j] = M::mma(a, sf[u], O[u][j]);
                 }
             }
-            const auto pa = frag_acc<T>(s[0], s[1]), pb = frag_acc<T>(s[2], s[3]);
-#pragma unroll
-            for (int j = 0; j < DT; j++) {
-                O[j] = M::mma(frag_col_pair<T>(Ks, LD, 0, 16 * j), pa, O[j]);
-                O[j] = M::mma(frag_col_pair<T>(Ks, LD, 32, 16 * j), pb, O[j]);
+            if (kBufs == 1) __syncthreads();
+            if (n + 1 < nt) {
+                rk.store(Ks[kBufs == 2 ? buf ^ 1 : 0]);
+                rv.store(Vs[kBufs == 2 ? buf ^ 1 : 0]);
             }
+            __syncthreads();
         }
     }
-    if (i >= d.T) return;
 #pragma unroll
-    for (int j = 0; j < DT; j++)
+    for (int u = 0; u < QN; u++) {
+        const int64_t t = t0 + ir[u];
+        if (t >= d.T) continue;
 #pragma unroll
-        for (int e = 0; e < 4; e++) {
-            const int c = 16 * j + 4 * g + e;
-            if (c < d.D) op[c] = (T)(live ? O[j][e] : 0.f);
-        }
+        for (int j = 0; j < DT; j++)
+            store4<T, VEC>(dq + at[u] * d.D, 16 * j + 4 * g, d.D,
+                           t < len ? O[u][j] : f32x4{0.f, 0.f, 0.f, 0.f});
+    }
 }
 
-// dK and dV of 64 keys: lane = key (column), four neighbouring queries (rows).
-// SINKS = false: the queries that some window over the tile reaches; the sums
-// of sinks go to part 0 of `parts`.  SINKS = true: the sinks for the queries
-// behind those, 512 a workgroup, into parts 1 ..
-template <typename T, int DT, bool SINKS>
+// dK and dV: a lane holds one key of KN blocks of 16 (columns) and four
+// neighbouring queries (rows), a workgroup 64 KN keys, over the query heads of
+// their key head.  SINKS = false: the queries that some window over the keys
+// reaches; the sums of sinks go to part 0 of `parts`.  SINKS = true: the sinks
+// for the queries behind those, 512 a workgroup, into parts 1 ..
+template <typename T, int DT, int KN, bool VEC, bool SINKS>
 __global__ __launch_bounds__(kThreads) void window_dkv_kernel(
     WinDims d, int ntiles, int nparts, const T *__restrict__ q, const T *__restrict__ k,
     const T *__restrict__ v, const T *__restrict__ dout, const float *__restrict__ lse,
-    const float *__restrict__ delta, const int32_t *__restrict__ lengths, bool vq, bool vk, bool vo,
-    T *__restrict__ dk, T *__restrict__ dv, float *__restrict__ parts)
+    const float *__restrict__ delta, const int32_t *__restrict__ lengths, T *__restrict__ dk,
+    T *__restrict__ dv, float *__restrict__ parts)
 {
     using M = Mat<T>;
     constexpr int LD = DT * 16 + 8;
-    __shared__ __align__(32) T Qs[kRows * LD];
-    __shared__ __align__(32) T Gs[kRows * LD];
-    __shared__ __align__(16) float Ls[kRows], Dl[kRows];
+    constexpr int KR = 64 * KN;                   // keys of a workgroup
+    constexpr int kBufs = 4 * 64 * LD * (int)sizeof(T) <= 156 * 1024 ? 2 : 1;
+    __shared__ __align__(32) T Qs[kBufs][kRows * LD];
+    __shared__ __align__(32) T Gs[kBufs][kRows * LD];
+    __shared__ __align__(16) float Ls[kBufs][kRows], Dl[kBufs][kRows];
 
-    int64_t rest = blockIdx.x;
+    int64_t rest = xcd_index(blockIdx.x, gridDim.x);
     int part = 0;
     if (SINKS) {
         part = 1 + (int)(rest % (nparts - 1));
@@ -528,97 +568,165 @@ __global__ __launch_bounds__(kThreads) void window_dkv_kernel(
     const int hk = (int)(rest % d.Hk);
     const int64_t b = rest / d.Hk;
     const int64_t len = seq_len(lengths, b, d.T);
-    const int l = threadIdx.x & 63, w = threadIdx.x >> 6, g = l >> 4;
-    const int64_t j0 = (int64_t)kt * kKeys;
-    const int64_t j = j0 + 16 * w + (l & 15);     // the lane's key
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int l = threadIdx.x & 63, g = l >> 4;
+    const int W = (int)d.W, S = d.S;
+    const int64_t j0 = (int64_t)kt * KR;
+    const int k0 = 16 * KN * w;                   // the wave's keys, relative to j0
+    const int sinks = (int)(S > j0 ? S - j0 : 0);   // keys below this one are sinks
     const int per = d.Hq / d.Hk;
-    f32x4 dK[DT], dV[DT];
+    f32x4 dK[KN][DT], dV[KN][DT];
 #pragma unroll
-    for (int n = 0; n < DT; n++) dK[n] = dV[n] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int u = 0; u < KN; u++)
+#pragma unroll
+        for (int n = 0; n < DT; n++) dK[u][n] = dV[u][n] = f32x4{0.f, 0.f, 0.f, 0.f};
 
     // the queries: [first, end)
-    int64_t first = j0, end = j0 + kKeys - 1 + d.W < len ? j0 + kKeys - 1 + d.W : len;
+    const int64_t reach = j0 + KR - 1 + d.W;
+    int64_t first = j0, end = reach < len ? reach : len;
     if (SINKS) {
         first = (int64_t)(part - 1) * kSinkRows;
         end = first + kSinkRows < len ? first + kSinkRows : len;
-        // nearer queries are in part 0
-        if (first < j0 + kKeys - 1 + d.W) first = j0 + kKeys - 1 + d.W;
+        if (first < reach) first = reach;   // nearer queries are in part 0
     }
     if (j0 < len && first < end) {
-        const bool live = j < len && (!SINKS || j < d.S);
-        const T *krow = live ? k + b * d.kb + j * d.kt + hk * d.kh : nullptr;
-        const T *vrow = live ? v + b * d.vb + j * d.vt + hk * d.vh : nullptr;
-        typename M::Frag kf[DT / 2], vf[DT / 2];
+        typename M::Frag kf[KN][DT / 2], vf[KN][DT / 2];
 #pragma unroll
-        for (int ks = 0; ks < DT / 2; ks++) {
-            kf[ks] = frag_global<T>(krow, 32 * ks + 8 * g, d.D, vk);
-            vf[ks] = frag_global<T>(vrow, 32 * ks + 8 * g, d.D, vk);
+        for (int u = 0; u < KN; u++) {
+            const int64_t j = j0 + k0 + 16 * u + (l & 15);
+            const T *krow = j < len ? k + b * d.kb + j * d.kt + hk * d.kh : nullptr;
+            const T *vrow = j < len ? v + b * d.vb + j * d.vt + hk * d.vh : nullptr;
+#pragma unroll
+            for (int ks = 0; ks < DT / 2; ks++) {
+                kf[u][ks] = frag_global<T>(krow, 32 * ks + 8 * g, d.D, VEC);
+                vf[u][ks] = frag_global<T>(vrow, 32 * ks + 8 * g, d.D, VEC);
+            }
         }
-        for (int h = hk * per; h < (hk + 1) * per; h++)
-            for (int64_t t0 = first; t0 < end; t0 += kRows) {
-                __syncthreads();
-                load_rows<T, DT * 16, LD>(Qs, [&](int r) {
-                    return t0 + r < end ? q + b * d.qb + (t0 + r) * d.qt + h * d.qh : nullptr;
-                }, d.D, vq);
-                load_rows<T, DT * 16, LD>(Gs, [&](int r) {
-                    return t0 + r < end ? dout + ((b * d.T + t0 + r) * d.Hq + h) * d.D : nullptr;
-                }, d.D, vo);
-                if (threadIdx.x < kRows) {
-                    const int64_t t = t0 + threadIdx.x;
-                    const bool in = t < end;
-                    Ls[threadIdx.x] = in ? lse[(b * d.T + t) * d.Hq + h] * 1.4426950408889634f : 0.f;
-                    Dl[threadIdx.x] = in ? delta[(b * d.T + t) * d.Hq + h] : 0.f;
+        const int nq = (int)((end - first + kRows - 1) / kRows);
+        RowRegs<T, DT * 16, LD, VEC> rq, rg;
+        float rl, rd;
+        const auto fetch = [&](int n) {
+            const int h = hk * per + n / nq;
+            const int64_t t0 = first + (int64_t)(n % nq) * kRows;
+            const auto row = [&](int r) { return t0 + r < end ? t0 + r : end - 1; };
+            rq.load([&](int r) { return q + b * d.qb + row(r) * d.qt + h * d.qh; }, d.D);
+            rg.load([&](int r) { return dout + ((b * d.T + row(r)) * d.Hq + h) * d.D; }, d.D);
+            if (threadIdx.x < kRows) {
+                const int64_t at = (b * d.T + row(threadIdx.x)) * d.Hq + h;
+                rl = lse[at] * 1.4426950408889634f;
+                rd = delta[at];
+            }
+        };
+        const auto put = [&](int buf) {
+            rq.store(Qs[buf]);
+            rg.store(Gs[buf]);
+            if (threadIdx.x < kRows) {
+                Ls[buf][threadIdx.x] = rl;
+                Dl[buf][threadIdx.x] = rd;
+            }
+        };
+        fetch(0);
+        put(0);
+        __syncthreads();
+        for (int n = 0; n < per * nq; n++) {
+            const int buf = kBufs == 2 ? n & 1 : 0;
+            if (n + 1 < per * nq) fetch(n + 1);
+            // first query of the tile relative to j0 (sinks: any number behind all keys will do)
+            const int64_t t0 = first + (int64_t)(n % nq) * kRows;
+            const int q0 = SINKS ? KR : (int)(t0 - j0);
+            const int qend = q0 + (int)(end - t0);
+#pragma unroll
+            for (int half = 0; half < 2; half++) {
+                const int r0 = 32 * half;
+                int sight[KN];
+                bool any = false;
+#pragma unroll
+                for (int u = 0; u < KN; u++) {  // as block_sight, for 16 keys and 32 queries
+                    const int c0 = k0 + 16 * u, c1 = c0 + 15, s0 = q0 + r0, s1 = s0 + 31;
+                    const bool none = c0 > s1 || s0 >= qend ||
+                                      (SINKS ? c0 >= sinks : c0 >= sinks && s0 - c1 >= W);
+                    const bool all = c1 <= s0 && s1 < qend && (c1 < sinks || (!SINKS && s1 - c0 < W));
+                    sight[u] = none ? 0 : all ? 2 : 1;
+                    any = any || sight[u];
                 }
-                __syncthreads();
+                if (!any) continue;
+                f32x4 p[KN][2], ds[KN][2];
 #pragma unroll
-                for (int half = 0; half < 2; half++) {
-                    f32x4 p[2], ds[2];
+                for (int e2 = 0; e2 < 2; e2++) {
+                    f32x4 s[KN], dp[KN];
 #pragma unroll
-                    for (int u = 0; u < 2; u++) {
-                        const int r0 = 32 * half + 16 * u;
-                        f32x4 s = {0.f, 0.f, 0.f, 0.f}, dp = s;
+                    for (int u = 0; u < KN; u++) s[u] = dp[u] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                        for (int ks = 0; ks < DT / 2; ks++) {
-                            s = M::mma(frag_row<T>(Qs, LD, r0, 32 * ks), kf[ks], s);
-                            dp = M::mma(frag_row<T>(Gs, LD, r0, 32 * ks), vf[ks], dp);
+                    for (int ks = 0; ks < DT / 2; ks++) {
+                        const auto qa = frag_row<T>(Qs[buf], LD, r0 + 16 * e2, 32 * ks);
+                        const auto ga = frag_row<T>(Gs[buf], LD, r0 + 16 * e2, 32 * ks);
+#pragma unroll
+                        for (int u = 0; u < KN; u++) {
+                            s[u] = M::mma(qa, kf[u][ks], s[u]);
+                            dp[u] = M::mma(ga, vf[u][ks], dp[u]);
                         }
-                        const f32x4 L = *reinterpret_cast<const f32x4 *>(Ls + r0 + 4 * g);
-                        const f32x4 D = *reinterpret_cast<const f32x4 *>(Dl + r0 + 4 * g);
+                    }
+                    const f32x4 L = *reinterpret_cast<const f32x4 *>(Ls[buf] + r0 + 16 * e2 + 4 * g);
+                    const f32x4 D = *reinterpret_cast<const f32x4 *>(Dl[buf] + r0 + 16 * e2 + 4 * g);
+#pragma unroll
+                    for (int u = 0; u < KN; u++)
 #pragma unroll
                         for (int e = 0; e < 4; e++) {
-                            const int64_t i = t0 + r0 + 4 * g + e;
-                            const bool see = live && i < end && j <= i && (i - j < d.W || j < d.S);
-                            p[u][e] = see ? exp2_fast(fmaf(s[e], d.c2, -L[e])) : 0.f;
-                            ds[u][e] = see ? p[u][e] * (dp[e] - D[e]) * d.scale : 0.f;
+                            float pe = exp2_fast(fmaf(s[u][e], d.c2, -L[e]));
+                            float de = pe * (dp[u][e] - D[e]) * d.scale;
+                            if (sight[u] != 2) {
+                                const int kr = k0 + 16 * u + (l & 15), qr = q0 + r0 + 16 * e2 + 4 * g + e;
+                                const bool see = kr <= qr && qr < qend &&
+                                                 (kr < sinks || (!SINKS && qr - kr < W));
+                                pe = see ? pe : 0.f;
+                                de = see ? de : 0.f;
+                            }
+                            p[u][e2][e] = pe;
+                            ds[u][e2][e] = de;
                         }
-                    }
-                    const auto pf = frag_acc<T>(p[0], p[1]), sf = frag_acc<T>(ds[0], ds[1]);
+                }
+                // P and dS are rounded to the inputs' type for the products with dO and Q
+                typename M::Frag pf[KN], sf[KN];
 #pragma unroll
-                    for (int n = 0; n < DT; n++) {
-                        dV[n] = M::mma(frag_col_pair<T>(Gs, LD, 32 * half, 16 * n), pf, dV[n]);
-                        dK[n] = M::mma(frag_col_pair<T>(Qs, LD, 32 * half, 16 * n), sf, dK[n]);
+                for (int u = 0; u < KN; u++) {
+                    pf[u] = frag_acc<T>(p[u][0], p[u][1]);
+                    sf[u] = frag_acc<T>(ds[u][0], ds[u][1]);
+                }
+#pragma unroll
+                for (int c = 0; c < DT; c++) {
+                    const auto ga = frag_col_pair<T>(Gs[buf], LD, r0, 16 * c);
+                    const auto qa = frag_col_pair<T>(Qs[buf], LD, r0, 16 * c);
+#pragma unroll
+                    for (int u = 0; u < KN; u++) {
+                        dV[u][c] = M::mma(ga, pf[u], dV[u][c]);
+                        dK[u][c] = M::mma(qa, sf[u], dK[u][c]);
                     }
                 }
             }
+            if (kBufs == 1) __syncthreads();
+            if (n + 1 < per * nq) put(kBufs == 2 ? buf ^ 1 : 0);
+            __syncthreads();
+        }
     }
-    const int64_t at = ((b * d.T + j) * d.Hk + hk) * d.D;
-    const bool sink = parts && j < d.S;
-    if (j >= d.T || (SINKS && !sink)) return;
-    float *pp = parts + ((((int64_t)part * d.B + b) * d.Hk + hk) * d.S + j) * 2 * d.D;
 #pragma unroll
-    for (int n = 0; n < DT; n++)
+    for (int u = 0; u < KN; u++) {
+        const int kr = k0 + 16 * u + (l & 15);
+        const int64_t j = j0 + kr;
+        const bool sink = parts && kr < sinks;
+        if (j >= d.T || (SINKS && !sink)) continue;
+        const int64_t at = ((b * d.T + j) * d.Hk + hk) * d.D;
+        float *pp = sink ? parts + ((((int64_t)part * d.B + b) * d.Hk + hk) * d.S + j) * 2 * d.D : nullptr;
 #pragma unroll
-        for (int e = 0; e < 4; e++) {
-            const int c = 16 * n + 4 * g + e;
-            if (c >= d.D) continue;
+        for (int c = 0; c < DT; c++) {
             if (sink) {
-                pp[c] = dK[n][e];
-                pp[d.D + c] = dV[n][e];
+                store4<float, false>(pp, 16 * c + 4 * g, d.D, dK[u][c]);
+                store4<float, false>(pp + d.D, 16 * c + 4 * g, d.D, dV[u][c]);
             } else {
-                dk[at + c] = (T)dK[n][e];
-                dv[at + c] = (T)dV[n][e];
+                store4<T, VEC>(dk + at, 16 * c + 4 * g, d.D, dK[u][c]);
+                store4<T, VEC>(dv + at, 16 * c + 4 * g, d.D, dV[u][c]);
             }
         }
+    }
 }
 
 // dK and dV of the sinks: the sum of their parts, in order.
@@ -667,6 +775,10 @@ WinDims dims_of(const sdm_window_desc &s)
     return d;
 }
 
+// Keys of a wave of the dK, dV kernel in blocks of 16: two, so that each
+// fragment of Q and dO serves 32 keys, unless D = 256 fills the registers.
+constexpr int key_blocks(int D) { return D <= 128 ? 2 : 1; }
+
 struct BackPlan {
     size_t delta, parts, total;
     int nparts, ktiles;
@@ -678,9 +790,9 @@ BackPlan back_plan(const sdm_window_desc &s)
     size_t at = ((size_t)s.B * s.T * s.Hq * 4 + 255) & ~(size_t)255;
     // sinks that queries see from behind their window
     if (s.sinks > 0 && s.T > s.window) {
+        const int64_t keys = 64 * key_blocks(s.D), rows = s.sinks < s.T ? s.sinks : s.T;
         p.nparts = 1 + (int)((s.T + kSinkRows - 1) / kSinkRows);
-        p.ktiles = (s.sinks + kKeys - 1) / kKeys;
-        if ((int64_t)p.ktiles * kKeys > s.T) p.ktiles = (int)((s.T + kKeys - 1) / kKeys);
+        p.ktiles = (int)((rows + keys - 1) / keys);
         p.parts = at;
         at += (size_t)p.nparts * s.B * s.Hk * s.sinks * 2 * s.D * 4;
     }
@@ -715,30 +827,31 @@ hipError_t forward(const WindowArgs &a, hipStream_t stream)
     return hipGetLastError();
 }
 
-template <typename T, int DT>
+template <typename T, int DT, bool VEC>
 hipError_t backward(const WindowArgs &a, hipStream_t stream)
 {
-    const WinDims d = dims_of(a.d);
+    WinDims d = dims_of(a.d);
     const BackPlan p = back_plan(a.d);
-    const bool vq = rows_on_16(a.q, d.qb, d.qt, d.qh, d.D, sizeof(T));
-    const bool vk = rows_on_16(a.k, d.kb, d.kt, d.kh, d.D, sizeof(T)) &&
-                    rows_on_16(a.v, d.vb, d.vt, d.vh, d.D, sizeof(T));
-    const bool vo = rows_on_16(a.dout, 0, 0, d.D, d.D, sizeof(T));
+    constexpr int QN = DT == 16 ? 1 : 2, KN = key_blocks(DT * 16);
     const T *q = (const T *)a.q, *k = (const T *)a.k, *v = (const T *)a.v, *dout = (const T *)a.dout;
     float *delta = (float *)a.ws, *parts = p.nparts ? (float *)(a.ws + p.parts) : nullptr;
-    const int64_t rows = (int64_t)d.B * d.T * d.Hq;
-    window_delta_kernel<T><<<(unsigned)((rows + 3) / 4), kThreads, 0, stream>>>(
-        rows, d.D, (const T *)a.oin, dout, delta);
-    window_dq_kernel<T, DT><<<(unsigned)((int64_t)d.B * d.Hq * d.nq), kThreads, 0, stream>>>(
-        d, q, k, v, dout, a.lse_in, delta, a.lengths, vq, vk, vo, (T *)a.dq);
-    window_dkv_kernel<T, DT, false><<<(unsigned)((int64_t)d.B * d.Hk * d.nq), kThreads, 0, stream>>>(
-        d, d.nq, p.nparts, q, k, v, dout, a.lse_in, delta, a.lengths, vq, vk, vo, (T *)a.dk, (T *)a.dv,
-        parts);
+    const auto run = [&](auto kernel, int hp, int queries) {
+        d.nq = (int)((d.T + queries - 1) / queries);
+        kernel<<<(unsigned)((int64_t)d.B * (d.Hq / hp) * d.nq), kThreads, 0, stream>>>(
+            d, q, k, v, (const T *)a.oin, dout, a.lse_in, a.lengths, delta, (T *)a.dq);
+    };
+    if (QN == 2 && (d.Hq / d.Hk) % 2 == 0)
+        run(window_dq_kernel<T, DT, QN, QN, VEC>, 2, 64);
+    else
+        run(window_dq_kernel<T, DT, QN, 1, VEC>, 1, 64 * QN);
+    const int ntiles = (int)((d.T + 64 * KN - 1) / (64 * KN));
+    window_dkv_kernel<T, DT, KN, VEC, false><<<(unsigned)((int64_t)d.B * d.Hk * ntiles), kThreads, 0, stream>>>(
+        d, ntiles, p.nparts, q, k, v, dout, a.lse_in, delta, a.lengths, (T *)a.dk, (T *)a.dv, parts);
     if (p.nparts) {
-        window_dkv_kernel<T, DT, true>
+        window_dkv_kernel<T, DT, KN, VEC, true>
             <<<(unsigned)((int64_t)d.B * d.Hk * p.ktiles * (p.nparts - 1)), kThreads, 0, stream>>>(
-                d, p.ktiles, p.nparts, q, k, v, dout, a.lse_in, delta, a.lengths, vq, vk, vo,
-                (T *)a.dk, (T *)a.dv, parts);
+                d, p.ktiles, p.nparts, q, k, v, dout, a.lse_in, delta, a.lengths, (T *)a.dk, (T *)a.dv,
+                parts);
         window_sinks_kernel<T><<<(unsigned)((int64_t)d.B * d.Hk * d.S), kThreads, 0, stream>>>(
             d, p.nparts, parts, (T *)a.dk, (T *)a.dv);
     }
@@ -749,10 +862,10 @@ template <typename T, bool VEC>
 hipError_t dispatch_d(const WindowArgs &a, bool back, hipStream_t stream)
 {
     // head columns padded to 32, 64, 128 or 256
-    if (a.d.D <= 32) return back ? backward<T, 2>(a, stream) : forward<T, 2, VEC>(a, stream);
-    if (a.d.D <= 64) return back ? backward<T, 4>(a, stream) : forward<T, 4, VEC>(a, stream);
-    if (a.d.D <= 128) return back ? backward<T, 8>(a, stream) : forward<T, 8, VEC>(a, stream);
-    return back ? backward<T, 16>(a, stream) : forward<T, 16, VEC>(a, stream);
+    if (a.d.D <= 32) return back ? backward<T, 2, VEC>(a, stream) : forward<T, 2, VEC>(a, stream);
+    if (a.d.D <= 64) return back ? backward<T, 4, VEC>(a, stream) : forward<T, 4, VEC>(a, stream);
+    if (a.d.D <= 128) return back ? backward<T, 8, VEC>(a, stream) : forward<T, 8, VEC>(a, stream);
+    return back ? backward<T, 16, VEC>(a, stream) : forward<T, 16, VEC>(a, stream);
 }
 
 template <typename T>
