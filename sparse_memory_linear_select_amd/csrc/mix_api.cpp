@@ -118,6 +118,8 @@ sdm_status check_scan(const sdm_scan_desc *d)
     if (d->P > 65536) return set_error(SDM_ERR_UNSUPPORTED, "P <= 65536 is supported (got %d)", d->P);
     if ((double)d->B * (double)d->T * d->H >= 2147483648.0)
         return set_error(SDM_ERR_UNSUPPORTED, "B*T*H must be < 2^31");
+    if ((double)d->B * d->H * ((d->P + 31) / 32) >= 2147483648.0)
+        return set_error(SDM_ERR_UNSUPPORTED, "B*H*ceil(P/32) must be < 2^31");
     if ((double)d->B * d->H >= 65536.0)
         return set_error(SDM_ERR_UNSUPPORTED, "B*H must be < 65536");
     if ((int64_t)d->H * d->P >= (int64_t)1 << 22)

@@ -71,7 +71,7 @@ struct WindowArgs {
     void *dq, *dk, *dv;
     unsigned char *ws;
 };
-size_t window_forward_ws(const sdm_window_desc &d, bool cache);
+size_t window_forward_ws(const sdm_window_desc &d, bool cont);
 size_t window_backward_ws(const sdm_window_desc &d);
 hipError_t launch_window_forward(const WindowArgs &a, hipStream_t stream);
 hipError_t launch_window_backward(const WindowArgs &a, hipStream_t stream);

@@ -11,6 +11,7 @@
 // (<= 0 for A <= 0), so nothing is divided by a decay.
 #include "mix_internal.h"
 
+#include "lane_ops.h"
 #include "mix_device.h"
 
 namespace sdm {
@@ -836,6 +837,83 @@ __global__ __launch_bounds__(kThreads) void scan_params_kernel(int64_t rows, int
     if (threadIdx.x == 0) out[h] = (float)sums[0];
 }
 
+// ------------------------------------------------------------ single tokens
+// One token: the state is read, updated and written once, which is all that
+// counts (P N floats each way a head).  LN lanes share a row of the state, four
+// columns each; a workgroup takes 32 rows.
+constexpr int kStepRows = 32;
+
+template <typename T, int LN, bool VEC>
+__global__ __launch_bounds__(kThreads) void scan_step_kernel(
+    ScanDims d, const T *__restrict__ x, const T *__restrict__ dt, const T *__restrict__ Bm,
+    const T *__restrict__ Cm, const float *__restrict__ A, const float *__restrict__ D,
+    const float *__restrict__ bias, const int32_t *__restrict__ lengths, int softplus, int cont,
+    float *__restrict__ state, T *__restrict__ y)
+{
+    constexpr int PASS = kThreads / LN;   // rows at a time
+    constexpr int NP = kStepRows > PASS ? kStepRows / PASS : 1;
+    const int nrb = (d.P + kStepRows - 1) / kStepRows;
+    const int rb = blockIdx.x % nrb;
+    const int64_t bh = blockIdx.x / nrb;
+    const int h = (int)(bh % d.H), grp = h / (d.H / d.G);
+    const int64_t b = bh / d.H;
+    const bool on = seq_len(lengths, b, 1) > 0;
+    const int n = (threadIdx.x % LN) * 4, r = threadIdx.x / LN;
+    float *sp = state + bh * (int64_t)d.P * d.N + n;
+    f32x4 S[NP];
+    float xv[NP];
+    T xr[NP];
+    // all loads first
+#pragma unroll
+    for (int u = 0; u < NP; u++) {
+        const int p = rb * kStepRows + u * PASS + r;
+        S[u] = f32x4{0.f, 0.f, 0.f, 0.f};
+        xr[u] = (T)0.f;
+        if (p >= d.P || (NP == 1 && r >= kStepRows)) continue;
+        if (cont) {
+            if constexpr (VEC) {
+                if (n < d.N) S[u] = *reinterpret_cast<const f32x4 *>(sp + (int64_t)p * d.N);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; i++)
+                    if (n + i < d.N) S[u][i] = sp[(int64_t)p * d.N + i];
+            }
+        }
+        if (on) xr[u] = x[b * d.xb + (int64_t)h * d.P + p];
+    }
+    f32x4 Bv = {0.f, 0.f, 0.f, 0.f}, Cv = Bv;
+    float delta = 0.f;
+    if (on) {
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            if (n + i < d.N) {
+                Bv[i] = (float)Bm[b * d.bb + (int64_t)grp * d.N + n + i];
+                Cv[i] = (float)Cm[b * d.cb + (int64_t)grp * d.N + n + i];
+            }
+        delta = (float)dt[b * d.H + h] + (bias ? bias[h] : 0.f);
+        if (softplus) delta = delta > 20.f ? delta : log1pf(expf(delta));
+    }
+    const float a = expf(delta * A[h]), Dh = D ? D[h] : 0.f;
+#pragma unroll
+    for (int u = 0; u < NP; u++) {
+        const int p = rb * kStepRows + u * PASS + r;
+        if (p >= d.P || (NP == 1 && r >= kStepRows)) continue;
+        xv[u] = (float)xr[u];
+        if (on) S[u] = S[u] * a + Bv * (delta * xv[u]);
+        float s = fmaf(S[u][0], Cv[0], S[u][1] * Cv[1]) + fmaf(S[u][2], Cv[2], S[u][3] * Cv[3]);
+#pragma unroll
+        for (int m = 1; m < LN; m <<= 1) s = xor_add(s, m);
+        if constexpr (VEC) {
+            if (n < d.N) *reinterpret_cast<f32x4 *>(sp + (int64_t)p * d.N) = S[u];
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                if (n + i < d.N) sp[(int64_t)p * d.N + i] = S[u][i];
+        }
+        if (n == 0) y[bh * d.P + p] = (T)(on ? fmaf(Dh, xv[u], s) : 0.f);
+    }
+}
+
 // -------------------------------------------------------------------- host
 
 struct Plan {
@@ -982,6 +1060,27 @@ hipError_t backward(const ScanArgs &a, hipStream_t stream)
     return hipGetLastError();
 }
 
+template <typename T>
+hipError_t step(const ScanArgs &a, hipStream_t stream)
+{
+    const Plan p = plan_of(a.d, false);
+    const ScanDims &d = p.d;
+    const unsigned grid = (unsigned)((int64_t)d.B * d.H * ((d.P + kStepRows - 1) / kStepRows));
+    const auto run = [&](auto kernel) {
+        kernel<<<grid, kThreads, 0, stream>>>(
+            d, (const T *)a.x, (const T *)a.dt, (const T *)a.Bm, (const T *)a.Cm, a.A, a.D, a.dt_bias,
+            a.lengths, a.d.softplus, a.cont, a.state, (T *)a.y);
+    };
+    const bool vec = d.N % 4 == 0;  // rows of the state on 16 bytes
+    if (d.N <= 32)
+        vec ? run(scan_step_kernel<T, 8, true>) : run(scan_step_kernel<T, 8, false>);
+    else if (d.N <= 64)
+        vec ? run(scan_step_kernel<T, 16, true>) : run(scan_step_kernel<T, 16, false>);
+    else
+        vec ? run(scan_step_kernel<T, 32, true>) : run(scan_step_kernel<T, 32, false>);
+    return hipGetLastError();
+}
+
 template <typename T, bool VEC>
 hipError_t dispatch_n(const ScanArgs &a, bool back, hipStream_t stream)
 {
@@ -995,6 +1094,7 @@ template <typename T>
 hipError_t dispatch(const ScanArgs &a, bool back, hipStream_t stream)
 {
     const sdm_scan_desc &d = a.d;
+    if (!back && d.T == 1) return step<T>(a, stream);
     const bool vec = rows_on_16(a.x, d.x_batch, d.x_token, 0, d.P, sizeof(T)) &&
                      rows_on_16(a.Bm, d.B_batch, d.B_token, 0, d.N, sizeof(T)) &&
                      rows_on_16(a.Cm, d.C_batch, d.C_token, 0, d.N, sizeof(T));
@@ -1003,7 +1103,7 @@ hipError_t dispatch(const ScanArgs &a, bool back, hipStream_t stream)
 
 }  // namespace
 
-size_t scan_forward_ws(const sdm_scan_desc &d) { return plan_of(d, false).total; }
+size_t scan_forward_ws(const sdm_scan_desc &d) { return d.T == 1 ? 0 : plan_of(d, false).total; }
 size_t scan_backward_ws(const sdm_scan_desc &d) { return plan_of(d, true).total; }
 
 hipError_t launch_scan_forward(const ScanArgs &a, hipStream_t stream)

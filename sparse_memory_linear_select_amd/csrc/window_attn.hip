@@ -358,6 +358,191 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && DT <= 8 ? 2 : 1) void w
     }
 }
 
+// ------------------------------------------------------------ single tokens
+// One token of every sequence against its rolling cache, whose rows are read
+// as they lie (a softmax does not ask for an order).  LK = D / 8 lanes share a
+// row, 8 columns each; a wave takes 64 / LK rows at a time, for the R query
+// heads of the workgroup, and keeps the running softmax of its rows.  Bound by
+// the cache's bytes, or for short windows by latency: all loads of a step are
+// issued before any is used, and there is one launch (with `splits`, which
+// share the rows of a long cache among workgroups, and a joining one).
+constexpr int kStepWaves = 8;
+
+template <typename T, int LK, int R, bool VEC>
+__global__ __launch_bounds__(64 * kStepWaves) void window_step_kernel(
+    WinDims d, int groups, int splits, const T *__restrict__ q, const T *__restrict__ k,
+    const T *__restrict__ v, T *ck, T *cv, const int64_t *__restrict__ pos,
+    const int32_t *__restrict__ lengths, T *__restrict__ o, float *__restrict__ lse,
+    float *__restrict__ part)
+{
+    constexpr int KW = 64 / LK;
+    constexpr int V = 16 / sizeof(T);
+    constexpr int kStepRows = R >= 4 ? 4 : 8;   // row loads of a lane in flight, for K and for V
+    __shared__ __align__(32) float Os[kStepWaves][R][LK * 8];
+    __shared__ float Ms[kStepWaves][R], Zs[kStepWaves][R];
+    const int split = blockIdx.x % splits;
+    const int64_t r0 = blockIdx.x / splits;
+    const int grp = (int)(r0 % groups);
+    const int64_t r1 = r0 / groups;
+    const int hk = (int)(r1 % d.Hk);
+    const int64_t b = r1 / d.Hk;
+    const int per = d.Hq / d.Hk, h0 = hk * per + grp * R, hn = per - grp * R < R ? per - grp * R : R;
+    const int tid = threadIdx.x, l = tid & 63, w = tid >> 6, kg = l / LK, c0 = (l % LK) * 8;
+    if (seq_len(lengths, b, 1) == 0) {
+        if (split == 0)
+            for (int e = tid; e < hn * d.D; e += 64 * kStepWaves) {
+                o[(b * d.Hq + h0 + e / d.D) * d.D + e % d.D] = (T)0.f;
+                if (e % d.D == 0) lse[b * d.Hq + h0 + e / d.D] = 0.f;
+            }
+        return;
+    }
+    const int64_t p = seq_pos(pos, b), slot = cache_slot(p, d.S, d.W);
+    const int64_t rows = p + 1 < d.cap ? p + 1 : d.cap;
+    const T *kn = k + b * d.kb + hk * d.kh, *vn = v + b * d.vb + hk * d.vh;
+    const int64_t step = (int64_t)d.Hk * d.D;
+    T *kc = ck + (b * d.cap * d.Hk + hk) * d.D, *vc = cv + (b * d.cap * d.Hk + hk) * d.D;
+    if (split == 0 && grp == 0 && tid < d.D) {   // nobody reads this row of the cache
+        kc[slot * step + tid] = kn[tid];
+        vc[slot * step + tid] = vn[tid];
+    }
+    const int64_t share = (rows + splits - 1) / splits;
+    const int64_t first = split * share, end = first + share < rows ? first + share : rows;
+
+    const auto read8 = [&](const T *row, bool in) {
+        typename Mat<T>::Frag f;
+        if constexpr (VEC) {
+            const T *src = row + (c0 < d.D ? c0 : 0);   // a column that exists: meets zeros of q
+#pragma unroll
+            for (int u = 0; u < 8 / V; u++) {
+                const Vec<T, V> x = vload<T, V>(src + u * V);
+#pragma unroll
+                for (int i = 0; i < V; i++) f[u * V + i] = x.e[i];
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; i++) f[i] = in && c0 + i < d.D ? row[c0 + i] : (T)0.f;
+        }
+        return f;
+    };
+    f32x8 qf[R], O[R];
+    float m[R], z[R];
+#pragma unroll
+    for (int r = 0; r < R; r++) {
+        const bool in = r < hn && c0 < d.D;
+        qf[r] = __builtin_convertvector(read8(q + b * d.qb + (h0 + (r < hn ? r : 0)) * d.qh, in), f32x8) *
+                (in ? d.c2 : 0.f);
+        O[r] = f32x8{0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        m[r] = -INFINITY;
+        z[r] = 0.f;
+    }
+    for (int64_t j0 = first; j0 < end; j0 += kStepWaves * kStepRows * KW) {
+        typename Mat<T>::Frag kf[kStepRows], vf[kStepRows];
+#pragma unroll
+        for (int u = 0; u < kStepRows; u++) {
+            int64_t j = j0 + (u * kStepWaves + w) * KW + kg;
+            if (j >= end) j = end - 1;                       // a row that exists, masked below
+            const bool cur = j == slot;
+            kf[u] = read8(cur ? kn : kc + j * step, true);
+            vf[u] = read8(cur ? vn : vc + j * step, true);
+        }
+#pragma unroll
+        for (int r = 0; r < R; r++) {
+            float s[kStepRows], top = m[r];
+#pragma unroll
+            for (int u = 0; u < kStepRows; u++) {
+                float a = 0.f;
+#pragma unroll
+                for (int i = 0; i < 8; i++) a = fmaf(qf[r][i], (float)kf[u][i], a);
+#pragma unroll
+                for (int x = 1; x < LK; x <<= 1) a = xor_add(a, x);
+                s[u] = j0 + (u * kStepWaves + w) * KW + kg < end ? a : -INFINITY;
+                top = fmaxf(top, s[u]);
+            }
+            const float base = top == -INFINITY ? 0.f : top;
+            const float keep = exp2_fast(m[r] - base);
+            m[r] = top;
+            z[r] *= keep;
+            O[r] *= keep;
+#pragma unroll
+            for (int u = 0; u < kStepRows; u++) {
+                const float e = exp2_fast(s[u] - base);
+                z[r] += e;
+                O[r] += __builtin_convertvector(vf[u], f32x8) * e;
+            }
+        }
+    }
+    // join the row groups of the wave, then the waves
+#pragma unroll
+    for (int r = 0; r < R; r++) {
+        float top = m[r];
+#pragma unroll
+        for (int x = LK; x < 64; x <<= 1) top = fmaxf(top, __shfl_xor(top, x));
+        const float f = top == -INFINITY ? 0.f : exp2_fast(m[r] - top);
+        float zz = z[r] * f;
+        O[r] *= f;
+#pragma unroll
+        for (int x = LK; x < 64; x <<= 1) {
+            zz = xor_add(zz, x);
+#pragma unroll
+            for (int i = 0; i < 8; i++) O[r][i] = xor_add(O[r][i], x);
+        }
+        if (kg == 0) *reinterpret_cast<f32x8 *>(&Os[w][r][c0]) = O[r];
+        if (l == 0) {
+            Ms[w][r] = top;
+            Zs[w][r] = zz;
+        }
+    }
+    __syncthreads();
+    for (int e = tid; e < hn * d.D; e += 64 * kStepWaves) {
+        const int r = e / d.D, c = e % d.D;
+        float top = -INFINITY, zz = 0.f, acc = 0.f;
+#pragma unroll
+        for (int x = 0; x < kStepWaves; x++) top = fmaxf(top, Ms[x][r]);
+        if (top > -INFINITY)
+#pragma unroll
+            for (int x = 0; x < kStepWaves; x++) {
+                const float f = exp2_fast(Ms[x][r] - top);
+                zz = fmaf(Zs[x][r], f, zz);
+                acc = fmaf(Os[x][r][c], f, acc);
+            }
+        const int64_t row = b * d.Hq + h0 + r;
+        if (splits == 1) {
+            o[row * d.D + c] = (T)(acc / zz);
+            if (c == 0) lse[row] = (top + log2f(zz)) * 0.6931471805599453f;
+        } else {
+            float *pp = part + (row * splits + split) * (d.D + 2);
+            pp[c] = acc;
+            if (c == 0) {
+                pp[d.D] = top;
+                pp[d.D + 1] = zz;
+            }
+        }
+    }
+}
+
+// o and lse of a query head from its splits.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void window_join_kernel(WinDims d, int splits,
+                                                               const int32_t *__restrict__ lengths,
+                                                               const float *__restrict__ part,
+                                                               T *__restrict__ o, float *__restrict__ lse)
+{
+    const int64_t row = blockIdx.x;
+    if (seq_len(lengths, row / d.Hq, 1) == 0) return;   // written as zeros already
+    const float *pp = part + row * splits * (d.D + 2);
+    float top = -INFINITY, z = 0.f, acc = 0.f;
+    for (int x = 0; x < splits; x++) top = fmaxf(top, pp[x * (d.D + 2) + d.D]);
+    const int c = threadIdx.x;
+    for (int x = 0; x < splits; x++) {
+        const float *q = pp + x * (d.D + 2);
+        const float f = exp2_fast(q[d.D] - top);
+        z = fmaf(q[d.D + 1], f, z);
+        if (c < d.D) acc = fmaf(q[c], f, acc);
+    }
+    if (c < d.D) o[row * d.D + c] = (T)(acc / z);
+    if (c == 0) lse[row] = (top + log2f(z)) * 0.6931471805599453f;
+}
+
 // The call's last tokens into the rolling cache: the sinks, and the newest
 // `window` tokens behind them.
 template <typename T>
@@ -858,9 +1043,59 @@ hipError_t backward(const WindowArgs &a, hipStream_t stream)
     return hipGetLastError();
 }
 
+// Query heads of a workgroup of the single-token kernel, and the workgroups
+// that share a cache: enough for every compute unit where there are few
+// streams, each with at least 256 rows.
+struct StepPlan {
+    int R, groups, splits;
+};
+
+StepPlan step_plan(const sdm_window_desc &s)
+{
+    StepPlan p;
+    const int per = s.Hq / s.Hk;
+    p.R = per == 1 ? 1 : per == 2 ? 2 : per <= 4 ? 4 : 8;
+    p.groups = (per + p.R - 1) / p.R;
+    const int64_t units = (int64_t)s.B * s.Hk * p.groups, rows = s.sinks + s.window;
+    int64_t n = (256 + units - 1) / units;
+    if (n > rows / 256) n = rows / 256;
+    p.splits = n < 1 ? 1 : n > 64 ? 64 : (int)n;
+    return p;
+}
+
+bool is_step(const sdm_window_desc &d, bool cont) { return cont && d.T == 1; }
+
+template <typename T, int LK, bool VEC>
+hipError_t step(const WindowArgs &a, hipStream_t stream)
+{
+    const WinDims d = dims_of(a.d);
+    const StepPlan p = step_plan(a.d);
+    const auto run = [&](auto kernel) {
+        kernel<<<(unsigned)((int64_t)d.B * d.Hk * p.groups * p.splits), 64 * kStepWaves, 0, stream>>>(
+            d, p.groups, p.splits, (const T *)a.q, (const T *)a.k, (const T *)a.v, (T *)a.cache_k,
+            (T *)a.cache_v, a.pos, a.lengths, (T *)a.o, a.lse, (float *)a.ws);
+    };
+    switch (p.R) {
+    case 1: run(window_step_kernel<T, LK, 1, VEC>); break;
+    case 2: run(window_step_kernel<T, LK, 2, VEC>); break;
+    case 4: run(window_step_kernel<T, LK, 4, VEC>); break;
+    default: run(window_step_kernel<T, LK, 8, VEC>); break;
+    }
+    if (p.splits > 1)
+        window_join_kernel<T><<<(unsigned)((int64_t)d.B * d.Hq), kThreads, 0, stream>>>(
+            d, p.splits, a.lengths, (const float *)a.ws, (T *)a.o, a.lse);
+    return hipGetLastError();
+}
+
 template <typename T, bool VEC>
 hipError_t dispatch_d(const WindowArgs &a, bool back, hipStream_t stream)
 {
+    if (!back && is_step(a.d, a.pos)) {  // lanes of a row
+        if (a.d.D <= 32) return step<T, 4, VEC>(a, stream);
+        if (a.d.D <= 64) return step<T, 8, VEC>(a, stream);
+        if (a.d.D <= 128) return step<T, 16, VEC>(a, stream);
+        return step<T, 32, VEC>(a, stream);
+    }
     // head columns padded to 32, 64, 128 or 256
     if (a.d.D <= 32) return back ? backward<T, 2, VEC>(a, stream) : forward<T, 2, VEC>(a, stream);
     if (a.d.D <= 64) return back ? backward<T, 4, VEC>(a, stream) : forward<T, 4, VEC>(a, stream);
@@ -881,7 +1116,12 @@ hipError_t dispatch(const WindowArgs &a, bool back, hipStream_t stream)
 
 }  // namespace
 
-size_t window_forward_ws(const sdm_window_desc &, bool) { return 0; }
+size_t window_forward_ws(const sdm_window_desc &d, bool cont)
+{
+    if (!is_step(d, cont)) return 0;
+    const StepPlan p = step_plan(d);
+    return p.splits == 1 ? 0 : (size_t)d.B * d.Hq * p.splits * (d.D + 2) * 4;
+}
 size_t window_backward_ws(const sdm_window_desc &d) { return back_plan(d).total; }
 
 hipError_t launch_window_forward(const WindowArgs &a, hipStream_t stream)

@@ -9,9 +9,10 @@ new dense tensors unless given.
 from __future__ import annotations
 
 import ctypes
-from ctypes import c_float, c_int, c_int64
+from ctypes import byref, c_float, c_int, c_int64
 
 import torch
+from torch._C import _cuda_getCurrentRawStream, _cuda_getDevice
 
 from . import (BF16, F32, FLAG_CONTINUE, SDMError, _check, _dev_tensor, _out_tensor, _same_device,
                _workspace, lib)
@@ -23,21 +24,45 @@ def _p(t):
     return None if t is None else t.data_ptr()
 
 
-class _On:
-    """Makes a device current for a call, if another one is."""
+def _call(f, device, *args):
+    """f(*args, stream) with `device` current, on its current stream."""
+    index = device.index
+    if _cuda_getDevice() == index:
+        status = f(*args, _cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(index):
+            status = f(*args, _cuda_getCurrentRawStream(index))
+    if status:
+        _check(status)
 
-    def __init__(self, device):
-        self.index = device.index
-        self.other = torch.cuda.current_device()
 
-    def __enter__(self):
-        if self.index != self.other:
-            torch.cuda.set_device(self.index)
-        return torch.cuda.current_stream().cuda_stream
+def _dense(t, name, shape, dtype, ref):
+    """t, which must be a dense tensor of this shape and dtype on ref's device."""
+    try:
+        if (t.shape == shape and t.dtype is dtype and t.device == ref.device
+                and t.is_contiguous()):
+            return t
+    except AttributeError:
+        pass
+    return _out_tensor(t, name, shape, dtype, ref)  # names what is wrong
 
-    def __exit__(self, *exc):
-        if self.index != self.other:
-            torch.cuda.set_device(self.other)
+
+class _Plans(dict):
+    """Checked descriptors by the shapes, strides and types of a call's inputs:
+    a decode loop or training run repeats a few."""
+
+    def keep(self, key, plan):
+        if len(self) >= 64:
+            self.clear()
+        self[key] = plan
+        return plan
+
+
+def _key(*tensors):
+    try:
+        return tuple([(t.shape, t.stride(), t.dtype, t.device) for t in tensors])
+    except AttributeError:
+        raise SDMError(1, "the inputs must be GPU tensors") from None
 
 
 def _dtype(t, name):
@@ -77,9 +102,31 @@ def _view(t, name, like, shape, inner):
 
 
 def _lengths(t, B, like):
-    if t is not None:
-        _out_tensor(t, "lengths", (B,), torch.int32, like)
-    return t
+    return None if t is None else _dense(t, "lengths", (B,), torch.int32, like).data_ptr()
+
+
+def _bytes(call, *args) -> int:
+    n = ctypes.c_size_t()
+    _check(call(*args, byref(n)))
+    return n.value
+
+
+class _Plan:
+    """A checked descriptor and the workspaces it asks for."""
+
+    def __init__(self, desc, shape):
+        self.desc, self.ref, self.shape, self.ws = desc, byref(desc), shape, {}
+
+    def workspace(self, call, given, like, *args):
+        """(tensor or None, its bytes) for a call that asks `call` for the size."""
+        key = (call.__name__, args)
+        need = self.ws.get(key)
+        if need is None:
+            need = self.ws[key] = _bytes(call, self.ref, *args)
+        if given is None and need == 0:
+            return None, 0
+        ws = _workspace(given, need, like)
+        return ws, ws.numel()
 
 
 class _ConvDesc(ctypes.Structure):
@@ -101,15 +148,21 @@ class CausalConv:
         if bias is not None:
             _param(bias, "bias", (self.C,), weight.device)
         self.weight, self.bias, self.silu = weight, bias, bool(silu)
+        self._plans = _Plans()
 
-    def _desc(self, x):
-        if not isinstance(x, torch.Tensor) or x.dim() != 3:
+    def _plan(self, x):
+        key = _key(x)
+        plan = self._plans.get(key)
+        if plan is not None:
+            return plan
+        if x.dim() != 3:
             raise SDMError(1, f"x must be [B, T, {self.C}]")
         B, T = x.shape[:2]
         _view(x, "x", x, (B, T, self.C), 1)
         _same_device(self.weight, x, "weight")
-        return _ConvDesc(B, T, self.C, self.K, int(self.silu), _dtype(x, "x"), x.stride(0),
-                         x.stride(1))
+        d = _ConvDesc(B, T, self.C, self.K, int(self.silu), _dtype(x, "x"), x.stride(0),
+                      x.stride(1))
+        return self._plans.keep(key, _Plan(d, (B, self.K - 1, self.C)))
 
     def forward(self, x, state=None, cont: bool = False, lengths=None, y=None):
         """(y, state): y [B, T, C], and the last K - 1 rows [B, K - 1, C].
@@ -118,55 +171,41 @@ class CausalConv:
         place; otherwise the rows before x are zeros (a given `state` is
         overwritten).  lengths [B] int32: tokens of each sequence.
         """
-        d = self._desc(x)
-        rows = (d.B, self.K - 1, self.C)
-        if state is None:
-            if cont:
-                raise SDMError(1, "cont=True needs the state")
-            state = torch.empty(rows, dtype=x.dtype, device=x.device)
+        plan = self._plan(x)
+        if state is not None:
+            _dense(state, "state", plan.shape, x.dtype, x)
+        elif cont:
+            raise SDMError(1, "cont=True needs the state")
         else:
-            _out_tensor(state, "state", rows, x.dtype, x)
-        if y is None:
-            y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        else:
-            _out_tensor(y, "y", x.shape, x.dtype, x)
-        _lengths(lengths, d.B, x)
-        with _On(x.device) as stream:
-            _check(lib().sdm_conv_forward(ctypes.byref(d), _p(x), _p(self.weight), _p(self.bias),
-                                          _p(lengths), FLAG_CONTINUE if cont else 0, _p(y),
-                                          _p(state), stream))
+            state = x.new_empty(plan.shape)
+        y = x.new_empty(x.shape) if y is None else _dense(y, "y", x.shape, x.dtype, x)
+        _call(lib().sdm_conv_forward, x.device, plan.ref, x.data_ptr(), self.weight.data_ptr(),
+              _p(self.bias), _lengths(lengths, plan.desc.B, x), FLAG_CONTINUE if cont else 0,
+              y.data_ptr(), state.data_ptr())
         return y, state
 
     def backward_workspace_size(self, x) -> int:
         """Bytes of workspace backward needs for inputs like x."""
-        n = ctypes.c_size_t()
-        _check(lib().sdm_conv_backward_workspace_size(ctypes.byref(self._desc(x)),
-                                                      ctypes.byref(n)))
-        return n.value
+        return _bytes(lib().sdm_conv_backward_workspace_size, self._plan(x).ref)
 
     def backward(self, x, dy, state=None, dstate=None, lengths=None, workspace=None) -> dict:
         """Gradients for dy [B, T, C] (and dstate, that of the final state, or
         None for zero): dx, float32 dweight and (with a bias) dbias, and, for a
         forward that started from `state`, dstate, its gradient."""
-        d = self._desc(x)
-        rows = (d.B, self.K - 1, self.C)
-        _out_tensor(dy, "dy", x.shape, x.dtype, x)
+        plan = self._plan(x)
+        _dense(dy, "dy", x.shape, x.dtype, x)
         for t, name in ((state, "state"), (dstate, "dstate")):
             if t is not None:
-                _out_tensor(t, name, rows, x.dtype, x)
-        _lengths(lengths, d.B, x)
-        workspace = _workspace(workspace, self.backward_workspace_size(x), x)
-        out = dict(dx=torch.empty(x.shape, dtype=x.dtype, device=x.device),
-                   dweight=torch.empty_like(self.weight))
+                _dense(t, name, plan.shape, x.dtype, x)
+        ws, ws_bytes = plan.workspace(lib().sdm_conv_backward_workspace_size, workspace, x)
+        out = dict(dx=x.new_empty(x.shape), dweight=torch.empty_like(self.weight))
         if self.bias is not None:
             out["dbias"] = torch.empty_like(self.bias)
         if state is not None:
-            out["dstate"] = torch.empty(rows, dtype=x.dtype, device=x.device)
-        with _On(x.device) as stream:
-            _check(lib().sdm_conv_backward(
-                ctypes.byref(d), _p(x), _p(self.weight), _p(self.bias), _p(lengths), _p(dy),
-                _p(state), _p(dstate), _p(workspace), workspace.numel(), _p(out["dx"]),
-                _p(out["dweight"]), _p(out.get("dbias")), _p(out.get("dstate")), stream))
+            out["dstate"] = x.new_empty(plan.shape)
+        _call(lib().sdm_conv_backward, x.device, plan.ref, _p(x), _p(self.weight), _p(self.bias),
+              _lengths(lengths, plan.desc.B, x), _p(dy), _p(state), _p(dstate), _p(ws), ws_bytes,
+              _p(out["dx"]), _p(out["dweight"]), _p(out.get("dbias")), _p(out.get("dstate")))
         return out
 
 
@@ -195,11 +234,16 @@ class SelectiveScan:
             if t is not None:
                 _param(t, name, (self.H,), A.device)
         self.A, self.D, self.dt_bias, self.softplus = A, D, dt_bias, bool(softplus)
+        self._plans = _Plans()
 
-    def _desc(self, x, dt, Bm, Cm):
-        if not isinstance(x, torch.Tensor) or x.dim() != 4 or x.shape[2] != self.H:
+    def _plan(self, x, dt, Bm, Cm):
+        key = _key(x, dt, Bm, Cm)
+        plan = self._plans.get(key)
+        if plan is not None:
+            return plan
+        if x.dim() != 4 or x.shape[2] != self.H:
             raise SDMError(1, f"x must be [B, T, {self.H}, P]")
-        if not isinstance(Bm, torch.Tensor) or Bm.dim() != 4:
+        if Bm.dim() != 4:
             raise SDMError(1, "Bm must be [B, T, G, N]")
         B, T, H, P = x.shape
         G, N = Bm.shape[2:]
@@ -208,22 +252,17 @@ class SelectiveScan:
         _view(Cm, "Cm", x, (B, T, G, N), 2)
         _out_tensor(dt, "dt", (B, T, H), x.dtype, x)
         _same_device(self.A, x, "A")
-        return _ScanDesc(B, T, H, P, N, G, int(self.softplus), _dtype(x, "x"), x.stride(0),
-                         x.stride(1), Bm.stride(0), Bm.stride(1), Cm.stride(0), Cm.stride(1))
-
-    @staticmethod
-    def _need(call, d) -> int:
-        n = ctypes.c_size_t()
-        _check(call(ctypes.byref(d), ctypes.byref(n)))
-        return n.value
+        d = _ScanDesc(B, T, H, P, N, G, int(self.softplus), _dtype(x, "x"), x.stride(0),
+                      x.stride(1), Bm.stride(0), Bm.stride(1), Cm.stride(0), Cm.stride(1))
+        return self._plans.keep(key, _Plan(d, (B, H, P, N)))
 
     def workspace_size(self, x, dt, Bm, Cm) -> int:
         """Bytes of workspace forward needs for inputs like these."""
-        return self._need(lib().sdm_scan_workspace_size, self._desc(x, dt, Bm, Cm))
+        return _bytes(lib().sdm_scan_workspace_size, self._plan(x, dt, Bm, Cm).ref)
 
     def backward_workspace_size(self, x, dt, Bm, Cm) -> int:
         """Bytes of workspace backward needs for inputs like these."""
-        return self._need(lib().sdm_scan_backward_workspace_size, self._desc(x, dt, Bm, Cm))
+        return _bytes(lib().sdm_scan_backward_workspace_size, self._plan(x, dt, Bm, Cm).ref)
 
     def forward(self, x, dt, Bm, Cm, state=None, cont: bool = False, lengths=None, y=None,
                 workspace=None):
@@ -234,25 +273,19 @@ class SelectiveScan:
         zero (a given `state` is overwritten).  lengths [B] int32: tokens of
         each sequence.
         """
-        d = self._desc(x, dt, Bm, Cm)
-        shape = (d.B, d.H, d.P, d.N)
-        if state is None:
-            if cont:
-                raise SDMError(1, "cont=True needs the state")
-            state = torch.empty(shape, dtype=_F32, device=x.device)
+        plan = self._plan(x, dt, Bm, Cm)
+        if state is not None:
+            _dense(state, "state", plan.shape, _F32, x)
+        elif cont:
+            raise SDMError(1, "cont=True needs the state")
         else:
-            _out_tensor(state, "state", shape, _F32, x)
-        if y is None:
-            y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        else:
-            _out_tensor(y, "y", x.shape, x.dtype, x)
-        _lengths(lengths, d.B, x)
-        workspace = _workspace(workspace, self._need(lib().sdm_scan_workspace_size, d), x)
-        with _On(x.device) as stream:
-            _check(lib().sdm_scan_forward(
-                ctypes.byref(d), _p(x), _p(dt), _p(Bm), _p(Cm), _p(self.A), _p(self.D),
-                _p(self.dt_bias), _p(lengths), FLAG_CONTINUE if cont else 0, _p(workspace),
-                workspace.numel(), _p(y), _p(state), stream))
+            state = x.new_empty(plan.shape, dtype=_F32)
+        y = x.new_empty(x.shape) if y is None else _dense(y, "y", x.shape, x.dtype, x)
+        ws, ws_bytes = plan.workspace(lib().sdm_scan_workspace_size, workspace, x)
+        _call(lib().sdm_scan_forward, x.device, plan.ref, x.data_ptr(), dt.data_ptr(),
+              Bm.data_ptr(), Cm.data_ptr(), self.A.data_ptr(), _p(self.D), _p(self.dt_bias),
+              _lengths(lengths, plan.desc.B, x), FLAG_CONTINUE if cont else 0, _p(ws), ws_bytes,
+              y.data_ptr(), state.data_ptr())
         return y, state
 
     def backward(self, x, dt, Bm, Cm, dy, state=None, dstate=None, lengths=None,
@@ -260,31 +293,25 @@ class SelectiveScan:
         """Gradients for dy [B, T, H, P] (and dstate, that of the final state,
         or None for zero): dx, ddt, dB, dC, float32 dA, dD and ddt_bias (where
         given), and, for a forward that started from `state`, dstate."""
-        d = self._desc(x, dt, Bm, Cm)
-        shape = (d.B, d.H, d.P, d.N)
-        _out_tensor(dy, "dy", x.shape, x.dtype, x)
+        plan = self._plan(x, dt, Bm, Cm)
+        _dense(dy, "dy", x.shape, x.dtype, x)
         for t, name in ((state, "state"), (dstate, "dstate")):
             if t is not None:
-                _out_tensor(t, name, shape, _F32, x)
-        _lengths(lengths, d.B, x)
-        workspace = _workspace(workspace, self._need(lib().sdm_scan_backward_workspace_size, d), x)
-        new = dict(dtype=x.dtype, device=x.device)
-        out = dict(dx=torch.empty(x.shape, **new), ddt=torch.empty(dt.shape, **new),
-                   dB=torch.empty(Bm.shape, **new), dC=torch.empty(Cm.shape, **new),
-                   dA=torch.empty_like(self.A))
+                _dense(t, name, plan.shape, _F32, x)
+        ws, ws_bytes = plan.workspace(lib().sdm_scan_backward_workspace_size, workspace, x)
+        out = dict(dx=x.new_empty(x.shape), ddt=x.new_empty(dt.shape), dB=x.new_empty(Bm.shape),
+                   dC=x.new_empty(Cm.shape), dA=torch.empty_like(self.A))
         if self.D is not None:
             out["dD"] = torch.empty_like(self.D)
         if self.dt_bias is not None:
             out["ddt_bias"] = torch.empty_like(self.dt_bias)
         if state is not None:
-            out["dstate"] = torch.empty(shape, dtype=_F32, device=x.device)
-        with _On(x.device) as stream:
-            _check(lib().sdm_scan_backward(
-                ctypes.byref(d), _p(x), _p(dt), _p(Bm), _p(Cm), _p(self.A), _p(self.D),
-                _p(self.dt_bias), _p(lengths), _p(dy), _p(state), _p(dstate), _p(workspace),
-                workspace.numel(), _p(out["dx"]), _p(out["ddt"]), _p(out["dB"]), _p(out["dC"]),
-                _p(out["dA"]), _p(out.get("dD")), _p(out.get("ddt_bias")), _p(out.get("dstate")),
-                stream))
+            out["dstate"] = x.new_empty(plan.shape, dtype=_F32)
+        _call(lib().sdm_scan_backward, x.device, plan.ref, _p(x), _p(dt), _p(Bm), _p(Cm),
+              _p(self.A), _p(self.D), _p(self.dt_bias), _lengths(lengths, plan.desc.B, x), _p(dy),
+              _p(state), _p(dstate), _p(ws), ws_bytes, _p(out["dx"]), _p(out["ddt"]),
+              _p(out["dB"]), _p(out["dC"]), _p(out["dA"]), _p(out.get("dD")),
+              _p(out.get("ddt_bias")), _p(out.get("dstate")))
         return out
 
 
@@ -309,6 +336,7 @@ class WindowAttention:
                 self.D, self.window, self.sinks, abs(self.Hq), abs(self.Hk)) >= 1 << 31:
             raise SDMError(1, "D and window must be >= 1, sinks >= 0, and all below 2^31")
         self.scale = self.D ** -0.5 if scale is None else float(scale)
+        self._plans = _Plans()
 
     def new_cache(self, B: int, dtype=_BF16, device="cuda"):
         """An empty rolling cache for B streams: (keys, values), each
@@ -317,22 +345,25 @@ class WindowAttention:
         return (torch.zeros(shape, dtype=dtype, device=device),
                 torch.zeros(shape, dtype=dtype, device=device))
 
-    def _desc(self, q, k, v):
-        if not isinstance(q, torch.Tensor) or q.dim() != 4:
+    def _plan(self, q, k, v):
+        key = _key(q, k, v)
+        plan = self._plans.get(key)
+        if plan is not None:
+            return plan
+        if q.dim() != 4:
             raise SDMError(1, f"q must be [B, T, {self.Hq}, {self.D}]")
         B, T = q.shape[:2]
         _view(q, "q", q, (B, T, self.Hq, self.D), 1)
         _view(k, "k", q, (B, T, self.Hk, self.D), 1)
         _view(v, "v", q, (B, T, self.Hk, self.D), 1)
-        return _WindowDesc(B, T, self.Hq, self.Hk, self.D, self.window, self.sinks, self.scale,
-                           _dtype(q, "q"), *q.stride()[:3], *k.stride()[:3], *v.stride()[:3])
+        d = _WindowDesc(B, T, self.Hq, self.Hk, self.D, self.window, self.sinks, self.scale,
+                        _dtype(q, "q"), *q.stride()[:3], *k.stride()[:3], *v.stride()[:3])
+        return self._plans.keep(key, _Plan(d, (B, self.sinks + self.window, self.Hk, self.D)))
 
     def workspace_size(self, q, k, v, cont: bool = False) -> int:
         """Bytes of workspace forward needs for inputs like these."""
-        n = ctypes.c_size_t()
-        _check(lib().sdm_window_workspace_size(ctypes.byref(self._desc(q, k, v)),
-                                               FLAG_CONTINUE if cont else 0, ctypes.byref(n)))
-        return n.value
+        return _bytes(lib().sdm_window_workspace_size, self._plan(q, k, v).ref,
+                      FLAG_CONTINUE if cont else 0)
 
     def forward(self, q, k, v, cache=None, pos=None, cont: bool = False, lengths=None, o=None,
                 lse=None, workspace=None):
@@ -345,59 +376,40 @@ class WindowAttention:
         otherwise they start a sequence.  lengths [B] int32: tokens of each
         sequence in this call.
         """
-        d = self._desc(q, k, v)
+        plan = self._plan(q, k, v)
         ck = cv = None
         if cache is not None:
             ck, cv = cache
-            shape = (d.B, self.sinks + self.window, self.Hk, self.D)
-            _out_tensor(ck, "the cache's keys", shape, q.dtype, q)
-            _out_tensor(cv, "the cache's values", shape, q.dtype, q)
+            _dense(ck, "the cache's keys", plan.shape, q.dtype, q)
+            _dense(cv, "the cache's values", plan.shape, q.dtype, q)
         if cont and (cache is None or pos is None):
             raise SDMError(1, "cont=True needs the cache and pos")
         if pos is not None:
-            _out_tensor(pos, "pos", (d.B,), torch.int64, q)
-        if o is None:
-            o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        else:
-            _out_tensor(o, "o", q.shape, q.dtype, q)
-        if lse is None:
-            lse = torch.empty(q.shape[:3], dtype=_F32, device=q.device)
-        else:
-            _out_tensor(lse, "lse", q.shape[:3], _F32, q)
-        _lengths(lengths, d.B, q)
+            _dense(pos, "pos", (plan.desc.B,), torch.int64, q)
+        o = q.new_empty(q.shape) if o is None else _dense(o, "o", q.shape, q.dtype, q)
+        rows = q.shape[:3]
+        lse = q.new_empty(rows, dtype=_F32) if lse is None else _dense(lse, "lse", rows, _F32, q)
         flags = FLAG_CONTINUE if cont else 0
-        n = ctypes.c_size_t()
-        _check(lib().sdm_window_workspace_size(ctypes.byref(d), flags, ctypes.byref(n)))
-        if n.value or workspace is not None:
-            workspace = _workspace(workspace, n.value, q)
-        with _On(q.device) as stream:
-            _check(lib().sdm_window_forward(
-                ctypes.byref(d), _p(q), _p(k), _p(v), _p(lengths), flags, _p(ck), _p(cv), _p(pos),
-                _p(workspace), 0 if workspace is None else workspace.numel(), _p(o), _p(lse),
-                stream))
+        ws, ws_bytes = plan.workspace(lib().sdm_window_workspace_size, workspace, q, flags)
+        _call(lib().sdm_window_forward, q.device, plan.ref, q.data_ptr(), k.data_ptr(),
+              v.data_ptr(), _lengths(lengths, plan.desc.B, q), flags, _p(ck), _p(cv), _p(pos),
+              _p(ws), ws_bytes, o.data_ptr(), lse.data_ptr())
         return o, lse
 
     def backward_workspace_size(self, q, k, v) -> int:
         """Bytes of workspace backward needs for inputs like these."""
-        n = ctypes.c_size_t()
-        _check(lib().sdm_window_backward_workspace_size(ctypes.byref(self._desc(q, k, v)),
-                                                        ctypes.byref(n)))
-        return n.value
+        return _bytes(lib().sdm_window_backward_workspace_size, self._plan(q, k, v).ref)
 
     def backward(self, q, k, v, o, lse, do, lengths=None, workspace=None) -> dict:
         """Gradients dq, dk, dv for do [B, T, Hq, D], with the o and lse that a
         forward without a cache returned."""
-        d = self._desc(q, k, v)
-        _out_tensor(o, "o", q.shape, q.dtype, q)
-        _out_tensor(do, "do", q.shape, q.dtype, q)
-        _out_tensor(lse, "lse", q.shape[:3], _F32, q)
-        _lengths(lengths, d.B, q)
-        workspace = _workspace(workspace, self.backward_workspace_size(q, k, v), q)
-        out = {n: torch.empty(t.shape, dtype=q.dtype, device=q.device)
-               for n, t in (("dq", q), ("dk", k), ("dv", v))}
-        with _On(q.device) as stream:
-            _check(lib().sdm_window_backward(
-                ctypes.byref(d), _p(q), _p(k), _p(v), _p(o), _p(lse), _p(do), _p(lengths),
-                _p(workspace), workspace.numel(), _p(out["dq"]), _p(out["dk"]), _p(out["dv"]),
-                stream))
+        plan = self._plan(q, k, v)
+        _dense(o, "o", q.shape, q.dtype, q)
+        _dense(do, "do", q.shape, q.dtype, q)
+        _dense(lse, "lse", q.shape[:3], _F32, q)
+        ws, ws_bytes = plan.workspace(lib().sdm_window_backward_workspace_size, workspace, q)
+        out = dict(dq=q.new_empty(q.shape), dk=k.new_empty(k.shape), dv=v.new_empty(v.shape))
+        _call(lib().sdm_window_backward, q.device, plan.ref, _p(q), _p(k), _p(v), _p(o), _p(lse),
+              _p(do), _lengths(lengths, plan.desc.B, q), _p(ws), ws_bytes, _p(out["dq"]),
+              _p(out["dk"]), _p(out["dv"]))
         return out
