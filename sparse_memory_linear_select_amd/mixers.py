@@ -47,20 +47,21 @@ def _dense(t, name, shape, dtype, ref):
     return _out_tensor(t, name, shape, dtype, ref)  # names what is wrong
 
 
-class _Plans(dict):
-    """Checked descriptors by the shapes, strides and types of a call's inputs:
-    a decode loop or training run repeats a few."""
-
-    def keep(self, key, plan):
-        if len(self) >= 64:
-            self.clear()
-        self[key] = plan
-        return plan
+# Checked descriptors by a layer's settings and the shapes, strides and types of
+# a call's inputs: a decode loop or training run repeats a few.
+_plans = {}
 
 
-def _key(*tensors):
+def _keep(key, plan):
+    if len(_plans) >= 256:
+        _plans.clear()
+    _plans[key] = plan
+    return plan
+
+
+def _key(settings, *tensors):
     try:
-        return tuple([(t.shape, t.stride(), t.dtype, t.device) for t in tensors])
+        return (settings, *[(t.shape, t.stride(), t.dtype, t.device) for t in tensors])
     except AttributeError:
         raise SDMError(1, "the inputs must be GPU tensors") from None
 
@@ -75,6 +76,9 @@ def _dtype(t, name):
 
 def _param(t, name, shape, device=None):
     """A float32 parameter: a dense GPU tensor of this shape."""
+    if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is _F32 and t.shape == shape
+            and t.is_contiguous() and (device is None or t.device == device)):
+        return t
     _dev_tensor(t, name, _F32)
     if tuple(t.shape) != tuple(shape):
         raise SDMError(1, f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
@@ -141,18 +145,17 @@ class CausalConv:
     """
 
     def __init__(self, weight, bias=None, silu: bool = True):
-        _dev_tensor(weight, "weight", _F32)
-        if weight.dim() != 2:
+        if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
             raise SDMError(1, "weight must be [C, K]")
-        self.C, self.K = weight.shape
+        self.C, self.K = _param(weight, "weight", weight.shape).shape
         if bias is not None:
             _param(bias, "bias", (self.C,), weight.device)
         self.weight, self.bias, self.silu = weight, bias, bool(silu)
-        self._plans = _Plans()
+        self._settings = ("conv", self.C, self.K, self.silu, weight.device)
 
     def _plan(self, x):
-        key = _key(x)
-        plan = self._plans.get(key)
+        key = _key(self._settings, x)
+        plan = _plans.get(key)
         if plan is not None:
             return plan
         if x.dim() != 3:
@@ -162,7 +165,7 @@ class CausalConv:
         _same_device(self.weight, x, "weight")
         d = _ConvDesc(B, T, self.C, self.K, int(self.silu), _dtype(x, "x"), x.stride(0),
                       x.stride(1))
-        return self._plans.keep(key, _Plan(d, (B, self.K - 1, self.C)))
+        return _keep(key, _Plan(d, (B, self.K - 1, self.C)))
 
     def forward(self, x, state=None, cont: bool = False, lengths=None, y=None):
         """(y, state): y [B, T, C], and the last K - 1 rows [B, K - 1, C].
@@ -226,19 +229,18 @@ class SelectiveScan:
     """
 
     def __init__(self, A, D=None, dt_bias=None, softplus: bool = True):
-        _dev_tensor(A, "A", _F32)
-        if A.dim() != 1:
+        if not isinstance(A, torch.Tensor) or A.dim() != 1:
             raise SDMError(1, "A must be [H]")
-        self.H = A.shape[0]
+        self.H = _param(A, "A", A.shape).shape[0]
         for t, name in ((D, "D"), (dt_bias, "dt_bias")):
             if t is not None:
                 _param(t, name, (self.H,), A.device)
         self.A, self.D, self.dt_bias, self.softplus = A, D, dt_bias, bool(softplus)
-        self._plans = _Plans()
+        self._settings = ("scan", self.H, self.softplus, A.device)
 
     def _plan(self, x, dt, Bm, Cm):
-        key = _key(x, dt, Bm, Cm)
-        plan = self._plans.get(key)
+        key = _key(self._settings, x, dt, Bm, Cm)
+        plan = _plans.get(key)
         if plan is not None:
             return plan
         if x.dim() != 4 or x.shape[2] != self.H:
@@ -254,7 +256,7 @@ class SelectiveScan:
         _same_device(self.A, x, "A")
         d = _ScanDesc(B, T, H, P, N, G, int(self.softplus), _dtype(x, "x"), x.stride(0),
                       x.stride(1), Bm.stride(0), Bm.stride(1), Cm.stride(0), Cm.stride(1))
-        return self._plans.keep(key, _Plan(d, (B, H, P, N)))
+        return _keep(key, _Plan(d, (B, H, P, N)))
 
     def workspace_size(self, x, dt, Bm, Cm) -> int:
         """Bytes of workspace forward needs for inputs like these."""
@@ -336,7 +338,7 @@ class WindowAttention:
                 self.D, self.window, self.sinks, abs(self.Hq), abs(self.Hk)) >= 1 << 31:
             raise SDMError(1, "D and window must be >= 1, sinks >= 0, and all below 2^31")
         self.scale = self.D ** -0.5 if scale is None else float(scale)
-        self._plans = _Plans()
+        self._settings = ("window", self.Hq, self.Hk, self.D, self.window, self.sinks, self.scale)
 
     def new_cache(self, B: int, dtype=_BF16, device="cuda"):
         """An empty rolling cache for B streams: (keys, values), each
@@ -346,8 +348,8 @@ class WindowAttention:
                 torch.zeros(shape, dtype=dtype, device=device))
 
     def _plan(self, q, k, v):
-        key = _key(q, k, v)
-        plan = self._plans.get(key)
+        key = _key(self._settings, q, k, v)
+        plan = _plans.get(key)
         if plan is not None:
             return plan
         if q.dim() != 4:
@@ -358,7 +360,7 @@ class WindowAttention:
         _view(v, "v", q, (B, T, self.Hk, self.D), 1)
         d = _WindowDesc(B, T, self.Hq, self.Hk, self.D, self.window, self.sinks, self.scale,
                         _dtype(q, "q"), *q.stride()[:3], *k.stride()[:3], *v.stride()[:3])
-        return self._plans.keep(key, _Plan(d, (B, self.sinks + self.window, self.Hk, self.D)))
+        return _keep(key, _Plan(d, (B, self.sinks + self.window, self.Hk, self.D)))
 
     def workspace_size(self, q, k, v, cont: bool = False) -> int:
         """Bytes of workspace forward needs for inputs like these."""
