@@ -80,11 +80,12 @@ __device__ __forceinline__ float row_shr(float x)
         __builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x110 | n, 0xF, 0xF, true));
 }
 
-// x of the row's last lane.
-__device__ __forceinline__ float row_last(float x)
+// x of the lane n to the right, 0 for the row's last n lanes.
+template <int n>
+__device__ __forceinline__ float row_shl(float x)
 {
     return __int_as_float(
-        __builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x150 | 15, 0xF, 0xF, true));
+        __builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x100 | n, 0xF, 0xF, true));
 }
 
 // One wave's part of a state: S^T, tiles j0 .. j0 + NJ - 1 of 16 rows n, rows
@@ -347,7 +348,8 @@ __global__ __launch_bounds__(2 * kThreads) void scan_walk_kernel(
 // `each` gets the state before every chunk.  Reverse: U = dy, V = C, weights
 // 2^{c_t}, chunks from last to first: the gradient G of the state,
 //   G <- 2^{c_63} G + sum_t 2^{c_t} C_t dy_t^T,
-// and `each` gets G behind every chunk.  `end` gets the last one: per segment
+// and `each` gets G behind every chunk, in tiles of [16 NT][64] per slice whose
+// rows and columns beyond N and P are zero.  `end` gets the last one: per segment
 // in the workspace's layout, or (end_api) the caller's gradient.  Waves w and
 // w + 4 hold the same 16 columns, each one half of the rows n.
 template <typename T, int NT, bool REV, bool VEC>
@@ -414,7 +416,14 @@ __global__ __launch_bounds__(2 * kThreads) void scan_state_kernel(
     for (int k = c0; k < c1; k++) {
         const int n = (k - c0) & 1;
         if (k + 1 < c1) fetch(chunk(k + 1));
-        if (each) state_store<NJ>(S, each + (bh * d.nc + chunk(k)) * PN, false, j0, p, d.P, d.N);
+        if (each) {
+            float *q = each + ((bh * d.nc + chunk(k)) * d.nps + ps) * (NT * 16 * kSlice) +
+                       (16 * j0 + 4 * ((threadIdx.x & 63) >> 4)) * kSlice + 16 * w + (threadIdx.x & 15);
+#pragma unroll
+            for (int j = 0; j < NJ; j++)
+#pragma unroll
+                for (int i = 0; i < 4; i++) q[(16 * j + i) * kSlice] = S[j][i];
+        }
         const Weighted<T> u(Us[n], wt[n], 16 * w);
         state_add<T, NJ, LN>(S, Vs[n], u, scale[n], j0);
         if (k + 1 < c1) put(n ^ 1);
@@ -463,8 +472,7 @@ __global__ __launch_bounds__(kThreads) void scan_join_kernel(ScanDims d, const f
 
 // ---------------------------------------------------------------- backward
 // Gradients of one chunk from the state S before it, the gradient G of the
-// state behind it (both in [N][P]) and the inputs.  With E_ts = 2^{c_t - c_s},
-// for s <= t:
+// state behind it and the inputs.  With E_ts = 2^{c_t - c_s}, for s <= t:
 //   dx_s = sum_t M_ts dy_t + w_s G B_s + D dy_s
 //   dC_t = sum_h sum_s W_ts B_s + 2^{c_t} S^T dy_t,     W_ts = (dy_t.x_s) E_ts D_s
 //   dB_s = sum_h sum_t W_ts C_t + w_s G^T x_s
@@ -480,11 +488,33 @@ __global__ __launch_bounds__(kThreads) void scan_join_kernel(ScanDims d, const f
 // pairs on one side of it.  S and G enter the products for dC, dB and dD to 24
 // bits.
 //
-// A workgroup owns a chunk and a block of the heads of a group, whose sums for
-// dB and dC stay in registers.  Wave w owns rows 16 w .. of the 64 x 64
-// products, columns 16 w .. of dx, and a quarter of the columns n.
+// A workgroup of eight waves owns a chunk and a block of the heads of a group,
+// whose sums for dB and dC stay in registers: waves 0 .. 3 hold those for dC,
+// a quarter of the columns n each, waves 4 .. 7 those for dB.  The ten 16 x 16
+// tiles on and under the diagonal of the 64 x 64 products are dealt to the
+// waves; dx is split into 16 columns and half of the tokens a wave.  The next
+// slice of x, dy, S and G is loaded while one is worked on.  What a head's
+// dD and dl need is left in LDS, and summed up for four heads at a time, by a
+// wave each.
+constexpr int kBatch = 4;
+
+// What the waves leave for a head's token gradients.
+struct HeadSums {
+    float2 cc[Q];
+    float dl[Q], wt[Q], et[Q];   // D_t, w_t, 2^{c_63 - c_t}
+    float colE[10][16];          // per tile: sum_t e_ts
+    float cross[10][16];         //   pairs with both ends in the tile that cross column r
+    float rows[Q][4];            //   sum_s e_ts D_s of row t
+    float all[10];               //   the tile's sum
+    float dotC[4][Q], dotB[4][Q];  // per quarter of n: C_t.(S^T dy_t), B_s.(G^T x_s)
+    float gs[4], dd[8];          // <G, S> and sum dy x, in parts
+};
+
+__device__ __forceinline__ int tile_row(int id) { return id < 1 ? 0 : id < 3 ? 1 : id < 6 ? 2 : 3; }
+__device__ __forceinline__ int tile_id(int row, int col) { return row * (row + 1) / 2 + col; }
+
 template <typename T, int NT, bool VEC>
-__global__ __launch_bounds__(kThreads) void scan_grad_kernel(
+__global__ __launch_bounds__(2 * kThreads) void scan_grad_kernel(
     ScanDims d, int hblocks, const T *__restrict__ x, const T *__restrict__ dy,
     const T *__restrict__ Bm, const T *__restrict__ Cm, const float *__restrict__ A,
     const float *__restrict__ D, const float *__restrict__ delta, const float2 *__restrict__ cs,
@@ -493,19 +523,21 @@ __global__ __launch_bounds__(kThreads) void scan_grad_kernel(
     T *__restrict__ dC, float *__restrict__ parts, float *__restrict__ hsum)
 {
     using M = Mat<T>;
+    using Frag = typename M::Frag;
+    using Half = typename M::Half;
     constexpr int LN = NT * 16 + 8;
-    constexpr int NW = NT >= 4 ? NT / 4 : 1;  // 16-column tiles of n per wave
-    __shared__ __align__(32) T Xs[Q * LX];
-    __shared__ __align__(32) T Ys[Q * LX];
+    constexpr int NW = NT >= 4 ? NT / 4 : 1;      // 16-column tiles of n per wave
+    constexpr int NF = NT / 2;
+    constexpr int kBufs = sizeof(T) == 2 ? 2 : 1;
+    constexpr bool kGs = sizeof(T) == 2;          // G, rounded, through LDS
+    constexpr int kTile = NT * 16 * kSlice;       // floats of a state tile
+    __shared__ __align__(32) T Xs[kBufs][Q * LX];
+    __shared__ __align__(32) T Ys[kBufs][Q * LX];
     __shared__ __align__(32) T Bs[Q * LN];
     __shared__ __align__(32) T Cs[Q * LN];
-    __shared__ __align__(32) T Ms[Q * LX];
-    __shared__ __align__(32) T Ws[Q * LX];
-    __shared__ float dl[Q], wt[Q], et[Q];
-    __shared__ float2 cc[Q];
-    __shared__ float colE[4][Q], colS[4][Q];  // per wave of rows t: sum_t e_ts, and pairs across s
-    __shared__ float dotC[4][Q], dotB[4][Q];  // per wave of columns: C_t.(S^T dy_t), B_s.(G^T x_s)
-    __shared__ float gs[4], dd[4];
+    __shared__ __align__(32) T Ms[Q * LX];        // M, then W
+    __shared__ __align__(32) T Gs[kGs ? kBufs : 1][kGs ? NT * 16 * LX : 1];
+    __shared__ __align__(16) HeadSums hs[kBatch];
 
     const int hb = blockIdx.x % hblocks;
     const int64_t r0 = blockIdx.x / hblocks;
@@ -519,238 +551,316 @@ __global__ __launch_bounds__(kThreads) void scan_grad_kernel(
     const int64_t t0 = (int64_t)c * Q;
     const int64_t len = seq_len(lengths, b, d.T);
     const int rows = len - t0 < 0 ? 0 : len - t0 < Q ? (int)(len - t0) : Q;
-    const int l = threadIdx.x & 63, w = threadIdx.x >> 6, g = l >> 4, li = l & 15;
-    const int64_t PN = (int64_t)d.P * d.N;
-    {
-        const T *bp = Bm + b * d.bb + (int64_t)grp * d.N;
-        const T *cp = Cm + b * d.cb + (int64_t)grp * d.N;
-        load_tile<T, Q, NT * 16, LN, kThreads, VEC>(Bs, bp + t0 * d.bt, d.bt, rows, d.N);
-        load_tile<T, Q, NT * 16, LN, kThreads, VEC>(Cs, cp + t0 * d.ct, d.ct, rows, d.N);
-    }
-    __syncthreads();
-    f32x4 CB[4];  // C_t.B_s, rows t = 16 w ..
-#pragma unroll
-    for (int ct = 0; ct < 4; ct++) {
-        CB[ct] = f32x4{0.f, 0.f, 0.f, 0.f};
-        if (ct <= w)
-#pragma unroll
-            for (int ks = 0; ks < NT / 2; ks++)
-                CB[ct] = M::mma(frag_row<T>(Cs, LN, 16 * w, 32 * ks),
-                                frag_row<T>(Bs, LN, 16 * ct, 32 * ks), CB[ct]);
-    }
-    const int nt0 = w * NW;                // the wave's column tiles of n
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), w = wave & 3;
+    const bool sideB = wave >= 4;
+    const int l = threadIdx.x & 63, g = l >> 4, li = l & 15;
+    const int nt0 = w * NW;                       // the wave's column tiles of n
     const bool ncols = nt0 < NT;
-    f32x4 dCa[4][NW], dBa[4][NW];
+
+    // one slice of x, dy, S and G in flight
+    TileRegs<T, Q, kSlice, LX, 2 * kThreads, VEC> rx, ry;
+    f32x4 rS[2][NW][2], rG[2][NW][2];             // rows n = 16 j + li, columns 32 ks + 8 g ..
+    const int64_t yt = (int64_t)d.H * d.P;
+    const auto fetch = [&](int step) {
+        const int h = h0 + step / d.nps, ps = step % d.nps;
+        const int pcols = d.P - ps * kSlice < kSlice ? d.P - ps * kSlice : kSlice;
+        rx.load(x + b * d.xb + t0 * d.xt + (int64_t)h * d.P + ps * kSlice, d.xt, rows, pcols);
+        ry.load(dy + (b * d.T + t0) * yt + (int64_t)h * d.P + ps * kSlice, yt, rows, pcols);
+        if (!ncols) return;
+        const int64_t at = (((b * d.H + h) * d.nc + c) * d.nps + ps) * kTile + (16 * nt0 + li) * kSlice + 8 * g;
+#pragma unroll
+        for (int ks = 0; ks < 2; ks++)
+#pragma unroll
+            for (int j = 0; j < NW; j++)
+#pragma unroll
+                for (int u = 0; u < 2; u++) {
+                    const int64_t e = at + 16 * j * kSlice + 32 * ks + 4 * u;
+                    rS[ks][j][u] = *reinterpret_cast<const f32x4 *>(Sws + e);
+                    if (sideB) rG[ks][j][u] = *reinterpret_cast<const f32x4 *>(Gws + e);
+                }
+    };
+    fetch(0);
+    load_tile<T, Q, NT * 16, LN, 2 * kThreads, VEC>(
+        Bs, Bm + b * d.bb + t0 * d.bt + (int64_t)grp * d.N, d.bt, rows, d.N);
+    load_tile<T, Q, NT * 16, LN, 2 * kThreads, VEC>(
+        Cs, Cm + b * d.cb + t0 * d.ct + (int64_t)grp * d.N, d.ct, rows, d.N);
+    __syncthreads();
+
+    // the wave's tiles: `wave`, and for waves 0 and 1 also 8 and 9
+    const int ntile = wave < 2 ? 2 : 1;
+    f32x4 CB[2], E[2], DX[2];
+#pragma unroll
+    for (int k = 0; k < 2; k++) {
+        CB[k] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (k >= ntile) continue;
+        const int id = wave + 8 * k, tr = tile_row(id), tc = id - tile_id(tr, 0);
+#pragma unroll
+        for (int ks = 0; ks < NF; ks++)
+            CB[k] = M::mma(frag_row<T>(Cs, LN, 16 * tr, 32 * ks), frag_row<T>(Bs, LN, 16 * tc, 32 * ks),
+                           CB[k]);
+    }
+    f32x4 sum[4][NW];                             // dC^T or dB^T: rows n, column = token
 #pragma unroll
     for (int r = 0; r < 4; r++)
 #pragma unroll
-        for (int j = 0; j < NW; j++) dCa[r][j] = dBa[r][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int j = 0; j < NW; j++) sum[r][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    // tiles right of the diagonal that products read stay zero
+    if (wave < 2) {
+        const int t = 32 * wave + 4 * g, s = 32 * wave + 16 + li;
+#pragma unroll
+        for (int i = 0; i < 4; i++) Ms[(t + i) * LX + s] = (T)0.f;
+    }
 
-    for (int h = h0; h < h1; h++) {
-        const int64_t bh = b * d.H + h;
-        const float Dh = D ? D[h] : 0.f;
-        __syncthreads();
-        if (threadIdx.x < Q) {
-            const int64_t at = (bh * d.nc + c) * Q;
-            const float2 me = cs[at + threadIdx.x];
-            const float dv = delta[at + threadIdx.x];
-            dl[threadIdx.x] = dv;
-            cc[threadIdx.x] = me;
-            et[threadIdx.x] = decay(cs[at + Q - 1], me);
-            wt[threadIdx.x] = et[threadIdx.x] * dv;
-        }
-        __syncthreads();
-        f32x4 E[4], DX[4];
-#pragma unroll
-        for (int ct = 0; ct < 4; ct++) {
-            const int s = 16 * ct + li;
-            DX[ct] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const int t = 16 * w + 4 * g + i;
-                E[ct][i] = s <= t ? decay(cc[t], cc[s]) : 0.f;
-                Ms[t * LX + s] = (T)(CB[ct][i] * E[ct][i] * dl[s]);
-            }
-        }
-        f32x4 aC[4][NW], aB[4][NW];
-#pragma unroll
-        for (int r = 0; r < 4; r++)
-#pragma unroll
-            for (int j = 0; j < NW; j++) aC[r][j] = aB[r][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-        float gdot = 0.f, ddot = 0.f;
-        const float *Sh = Sws + (bh * d.nc + c) * PN;
-        const float *Gh = Gws + (bh * d.nc + c) * PN;
-
-        for (int ps = 0; ps < d.nps; ps++) {
-            const int p0 = ps * kSlice;
-            const int pcols = d.P - p0 < kSlice ? d.P - p0 : kSlice;
-            const T *xp = x + b * d.xb + (int64_t)h * d.P + p0;
-            const T *yp = dy + b * d.T * d.H * d.P + (int64_t)h * d.P + p0;
-            const int64_t yt = (int64_t)d.H * d.P;
-            __syncthreads();
-            load_tile<T, Q, kSlice, LX, kThreads, VEC>(Xs, xp + t0 * d.xt, d.xt, rows, pcols);
-            load_tile<T, Q, kSlice, LX, kThreads, VEC>(Ys, yp + t0 * yt, yt, rows, pcols);
-            __syncthreads();
-#pragma unroll
-            for (int ks = 0; ks < 2; ks++) {
-                const auto a = frag_row<T>(Ys, LX, 16 * w, 32 * ks);
-#pragma unroll
-                for (int ct = 0; ct < 4; ct++)
-                    if (ct <= w) DX[ct] = M::mma(a, frag_row<T>(Xs, LX, 16 * ct, 32 * ks), DX[ct]);
-            }
-            if (ncols) {
-#pragma unroll
-                for (int ks = 0; ks < 2; ks++)
-#pragma unroll
-                    for (int j = 0; j < NW; j++) {
-                        const int n = 16 * (nt0 + j) + li;
-                        f32x8 sv, gv;
-#pragma unroll
-                        for (int i = 0; i < 8; i++) {
-                            const int p = p0 + 32 * ks + 8 * g + i;
-                            const bool in = p < d.P && n < d.N;
-                            sv[i] = in ? Sh[(int64_t)n * d.P + p] : 0.f;
-                            gv[i] = in ? Gh[(int64_t)n * d.P + p] : 0.f;
-                            gdot = fmaf(sv[i], gv[i], gdot);
-                        }
-                        typename M::Frag sf[M::kTerms], gf[M::kTerms];
-                        split_frag<T>(sv, sf);
-                        split_frag<T>(gv, gf);
-#pragma unroll
-                        for (int r = 0; r < 4; r++) {
-                            const auto ya = frag_row<T>(Ys, LX, 16 * r, 32 * ks);
-                            const auto xa = frag_row<T>(Xs, LX, 16 * r, 32 * ks);
-#pragma unroll
-                            for (int m = 0; m < M::kTerms; m++) {
-                                aC[r][j] = M::mma(ya, sf[m], aC[r][j]);
-                                aB[r][j] = M::mma(xa, gf[m], aB[r][j]);
-                            }
-                        }
-                    }
-            }
-            // dx, the wave's 16 columns
-            const int p = p0 + 16 * w + li;
-            typename M::Frag gn[NT / 2];
-#pragma unroll
-            for (int kk = 0; kk < NT / 2; kk++)
-#pragma unroll
-                for (int i = 0; i < 8; i++) {
-                    const int n = 32 * kk + 8 * g + i;
-                    gn[kk][i] = (T)(p < d.P && n < d.N ? Gh[(int64_t)n * d.P + p] : 0.f);
+    const int steps = (h1 - h0) * d.nps;
+    f32x4 acc[4][NW];
+    float gdot = 0.f, ddot = 0.f;
+    for (int step = 0; step < steps; step++) {
+        const int hn = step / d.nps, h = h0 + hn, ps = step % d.nps, slot = hn % kBatch;
+        const int buf = kBufs == 2 ? step & 1 : 0;
+        HeadSums &H = hs[slot];
+        if (ps == 0) {
+            __syncthreads();  // the head before is done with W, and at slot 0 its batch with hs
+            if (slot == 0) {
+                const int hh = h + (int)(threadIdx.x >> 6), s = threadIdx.x >> 6;
+                if (s < kBatch && hh < h1) {
+                    const int64_t at = ((b * d.H + hh) * d.nc + c) * Q;
+                    const float2 me = cs[at + l];
+                    const float dv = delta[at + l], e = decay(cs[at + Q - 1], me);
+                    hs[s].cc[l] = me;
+                    hs[s].dl[l] = dv;
+                    hs[s].et[l] = e;
+                    hs[s].wt[l] = e * dv;
                 }
+                __syncthreads();
+            }
 #pragma unroll
-            for (int r = 0; r < 4; r++) {
-                f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int kk = 0; kk < NT / 2; kk++)
-                    acc = M::mma(frag_row<T>(Bs, LN, 16 * r, 32 * kk), gn[kk], acc);
-#pragma unroll
-                for (int i = 0; i < 4; i++) acc[i] *= wt[16 * r + 4 * g + i];
-#pragma unroll
-                for (int ks = r / 2; ks < 2; ks++)
-                    acc = M::mma(frag_col<T>(Ms, LX, 32 * ks, 16 * r),
-                                 frag_col<T>(Ys, LX, 32 * ks, 16 * w), acc);
+            for (int k = 0; k < 2; k++) {
+                DX[k] = f32x4{0.f, 0.f, 0.f, 0.f};
+                if (k >= ntile) continue;
+                const int id = wave + 8 * k, tr = tile_row(id), tc = id - tile_id(tr, 0);
+                const int s = 16 * tc + li;
+                const float2 ccs = H.cc[s];
+                const float ds = H.dl[s];
 #pragma unroll
                 for (int i = 0; i < 4; i++) {
-                    const int s = 16 * r + 4 * g + i;
-                    const float gy = (float)Ys[s * LX + 16 * w + li];
-                    ddot = fmaf(gy, (float)Xs[s * LX + 16 * w + li], ddot);
-                    if (p < d.P && t0 + s < d.T)
-                        dx[((b * d.T + t0 + s) * d.H + h) * d.P + p] =
-                            (T)(s < rows ? fmaf(Dh, gy, acc[i]) : 0.f);
+                    const int t = 16 * tr + 4 * g + i;
+                    E[k][i] = s <= t ? decay(H.cc[t], ccs) : 0.f;
+                    Ms[t * LX + s] = (T)(CB[k][i] * E[k][i] * ds);
                 }
             }
-        }
-        // W, the sums of e over t, and per column r the pairs (s < r <= t)
-        float carry[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int ct = 0; ct < 4; ct++) {
-            const int s = 16 * ct + li;
-            float cE = 0.f, cS = 0.f;
+            for (int r = 0; r < 4; r++)
+#pragma unroll
+                for (int j = 0; j < NW; j++) acc[r][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+            gdot = ddot = 0.f;
+        }
+        if (kBufs == 1 && step) __syncthreads();
+        rx.store(Xs[buf]);
+        ry.store(Ys[buf]);
+        // the state of the wave's side in three terms
+        Frag sf[2][NW][M::kTerms];
+        if (ncols)
+#pragma unroll
+            for (int ks = 0; ks < 2; ks++)
+#pragma unroll
+                for (int j = 0; j < NW; j++) {
+                    const f32x8 sv = __builtin_shufflevector(rS[ks][j][0], rS[ks][j][1], 0, 1, 2, 3, 4, 5, 6, 7);
+                    if (!sideB) {
+                        split_frag<T>(sv, sf[ks][j]);
+                    } else {
+                        const f32x8 gv =
+                            __builtin_shufflevector(rG[ks][j][0], rG[ks][j][1], 0, 1, 2, 3, 4, 5, 6, 7);
+#pragma unroll
+                        for (int i = 0; i < 8; i++) gdot = fmaf(sv[i], gv[i], gdot);
+                        split_frag<T>(gv, sf[ks][j]);
+                        if constexpr (kGs)
+                            *reinterpret_cast<Frag *>(Gs[buf] + (16 * (nt0 + j) + li) * LX + 32 * ks + 8 * g) =
+                                sf[ks][j][0];
+                    }
+                }
+        __syncthreads();
+        if (step + 1 < steps) fetch(step + 1);
+        // dy.x for the wave's tiles
+#pragma unroll
+        for (int k = 0; k < 2; k++) {
+            if (k >= ntile) continue;
+            const int id = wave + 8 * k, tr = tile_row(id), tc = id - tile_id(tr, 0);
+#pragma unroll
+            for (int ks = 0; ks < 2; ks++)
+                DX[k] = M::mma(frag_row<T>(Ys[buf], LX, 16 * tr, 32 * ks),
+                               frag_row<T>(Xs[buf], LX, 16 * tc, 32 * ks), DX[k]);
+        }
+        // S^T dy or G^T x, transposed: rows n, column = token
+        if (ncols) {
+            const T *src = sideB ? Xs[buf] : Ys[buf];
+#pragma unroll
+            for (int r = 0; r < 4; r++)
+#pragma unroll
+                for (int ks = 0; ks < 2; ks++) {
+                    const Frag a = frag_row<T>(src, LX, 16 * r, 32 * ks);
+#pragma unroll
+                    for (int j = 0; j < NW; j++)
+#pragma unroll
+                        for (int m = 0; m < M::kTerms; m++) acc[r][j] = M::mma(sf[ks][j][m], a, acc[r][j]);
+                }
+        }
+        // dx^T: 16 columns (rows here) and half of the tokens
+        {
+            Frag gn[NF], yc[2];
+            const float *Gh = Gws + (((b * d.H + h) * d.nc + c) * d.nps + ps) * kTile + 16 * w + li;
+#pragma unroll
+            for (int kk = 0; kk < NF; kk++) {
+                if constexpr (kGs) {
+                    gn[kk] = frag_col<T>(Gs[buf], LX, 32 * kk, 16 * w);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; i++) gn[kk][i] = Gh[(32 * kk + 8 * g + i) * kSlice];
+                }
+            }
+#pragma unroll
+            for (int ks = 0; ks < 2; ks++) yc[ks] = frag_col<T>(Ys[buf], LX, 32 * ks, 16 * w);
+            const int p = ps * kSlice + 16 * w + 4 * g;
+#pragma unroll
+            for (int q = 0; q < 2; q++) {
+                const int r = sideB ? 2 + q : q, s = 16 * r + li;
+                f32x4 o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int kk = 0; kk < NF; kk++)
+                    o = M::mma(gn[kk], frag_row<T>(Bs, LN, 16 * r, 32 * kk), o);
+                o *= H.wt[s];
+#pragma unroll
+                for (int ks = 0; ks < 2; ks++)
+                    if (ks || !sideB) o = M::mma(yc[ks], frag_col<T>(Ms, LX, 32 * ks, 16 * r), o);
+                const f32x4 gy = __builtin_convertvector(
+                    *reinterpret_cast<const Half *>(Ys[buf] + s * LX + 16 * w + 4 * g), f32x4);
+                const f32x4 xv = __builtin_convertvector(
+                    *reinterpret_cast<const Half *>(Xs[buf] + s * LX + 16 * w + 4 * g), f32x4);
+#pragma unroll
+                for (int i = 0; i < 4; i++) ddot = fmaf(gy[i], xv[i], ddot);
+                o += gy * (D ? D[h] : 0.f);
+                if (s >= rows) o = f32x4{0.f, 0.f, 0.f, 0.f};
+                if (t0 + s < d.T)
+                    store4<T, VEC>(dx + ((b * d.T + t0 + s) * d.H + h) * d.P, p, d.P, o);
+            }
+        }
+        if (ps + 1 < d.nps) continue;
+
+        // the head's last slice: W, and the sums that its token gradients are made of
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < 2; k++) {
+            if (k >= ntile) continue;
+            const int id = wave + 8 * k, tr = tile_row(id), tc = id - tile_id(tr, 0);
+            const int s = 16 * tc + li;
+            const float ds = H.dl[s];
+            float cE = 0.f, cS = 0.f, whole = 0.f;
 #pragma unroll
             for (int i = 0; i < 4; i++) {
-                const int t = 16 * w + 4 * g + i;
-                const float wv = DX[ct][i] * E[ct][i];
-                const float e = wv * CB[ct][i];
-                Ws[t * LX + s] = (T)(wv * dl[s]);
+                const int t = 16 * tr + 4 * g + i;
+                const float wv = DX[k][i] * E[k][i];
+                const float e = wv * CB[k][i];
+                Ms[t * LX + s] = (T)(wv * ds);    // rounded for the products with B and C
                 cE += e;
-                float q = e * dl[s];  // prefix over the tile's 16 columns
+                float q = e * ds;                 // prefix over the tile's 16 columns
                 q += row_shr<1>(q);
                 q += row_shr<2>(q);
                 q += row_shr<4>(q);
                 q += row_shr<8>(q);
-                cS += s <= t ? carry[i] + row_shr<1>(q) : 0.f;
-                carry[i] += row_last(q);
+                cS += s <= t ? row_shr<1>(q) : 0.f;
+                if (li == 15) H.rows[t][tc] = q;
+                whole += q;
             }
-            cE += __shfl_xor(cE, 16);
-            cE += __shfl_xor(cE, 32);
-            cS += __shfl_xor(cS, 16);
-            cS += __shfl_xor(cS, 32);
+            cE = xor_add(xor_add(cE, 16), 32);
+            cS = xor_add(xor_add(cS, 16), 32);
+            whole = xor_add(xor_add(whole, 16), 32);
             if (g == 0) {
-                colE[w][s] = cE;
-                colS[w][s] = cS;
+                H.colE[id][li] = cE;
+                H.cross[id][li] = cS;
+                if (li == 15) H.all[id] = whole;
             }
         }
-        // the parts through S and G: row dots, then the running sums
+        if (ncols) {
+            const T *own = sideB ? Bs : Cs;
 #pragma unroll
-        for (int r = 0; r < 4; r++)
+            for (int r = 0; r < 4; r++) {
+                const int t = 16 * r + li;
+                const float2 ct = H.cc[t];
+                const float f = sideB ? H.wt[t] : exp2_fast(ct.x + ct.y);
+                float dot = 0.f;
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const int t = 16 * r + 4 * g + i;
-                float vc = 0.f, vb = 0.f;
-                const float ec = exp2_fast(cc[t].x + cc[t].y);
-                if (ncols)
+                for (int j = 0; j < NW; j++) {
+                    const f32x4 v = __builtin_convertvector(
+                        *reinterpret_cast<const Half *>(own + t * LN + 16 * (nt0 + j) + 4 * g), f32x4);
 #pragma unroll
-                    for (int j = 0; j < NW; j++) {
-                        const int n = 16 * (nt0 + j) + li;
-                        vc = fmaf(aC[r][j][i], (float)Cs[t * LN + n], vc);
-                        vb = fmaf(aB[r][j][i], (float)Bs[t * LN + n], vb);
-                        dCa[r][j][i] = fmaf(ec, aC[r][j][i], dCa[r][j][i]);
-                        dBa[r][j][i] = fmaf(wt[t], aB[r][j][i], dBa[r][j][i]);
-                    }
-#pragma unroll
-                for (int m = 1; m < 16; m <<= 1) {
-                    vc += __shfl_xor(vc, m);
-                    vb += __shfl_xor(vb, m);
+                    for (int i = 0; i < 4; i++) dot = fmaf(acc[r][j][i], v[i], dot);
+                    sum[r][j] += acc[r][j] * f;
                 }
-                if (li == 0) {
-                    dotC[w][t] = vc;
-                    dotB[w][t] = vb;
-                }
+                dot = xor_add(xor_add(dot, 16), 32);
+                if (g == 0) (sideB ? H.dotB : H.dotC)[w][t] = dot;
             }
+        } else if (g == 0) {
+#pragma unroll
+            for (int r = 0; r < 4; r++) (sideB ? H.dotB : H.dotC)[w][16 * r + li] = 0.f;
+        }
 #pragma unroll
         for (int m = 1; m < 64; m <<= 1) {
-            gdot += __shfl_xor(gdot, m);
-            ddot += __shfl_xor(ddot, m);
+            gdot = xor_add(gdot, m);
+            ddot = xor_add(ddot, m);
         }
         if (l == 0) {
-            gs[w] = gdot;
-            dd[w] = ddot;
+            if (sideB) H.gs[w] = gdot;
+            H.dd[wave] = ddot;
         }
         __syncthreads();
-        if (ncols)
+        if (ncols) {
+            const T *other = sideB ? Cs : Bs;
 #pragma unroll
             for (int j = 0; j < NW; j++)
 #pragma unroll
                 for (int ks = 0; ks < 2; ks++) {
-                    const auto bf = frag_col<T>(Bs, LN, 32 * ks, 16 * (nt0 + j));
-                    const auto cf = frag_col<T>(Cs, LN, 32 * ks, 16 * (nt0 + j));
+                    const Frag f = frag_col<T>(other, LN, 32 * ks, 16 * (nt0 + j));
 #pragma unroll
                     for (int r = 0; r < 4; r++) {
-                        if (ks <= r / 2)
-                            dCa[r][j] = M::mma(frag_row<T>(Ws, LX, 16 * r, 32 * ks), bf, dCa[r][j]);
-                        if (ks >= r / 2)
-                            dBa[r][j] = M::mma(frag_col<T>(Ws, LX, 32 * ks, 16 * r), cf, dBa[r][j]);
+                        if (!sideB && ks <= r / 2)
+                            sum[r][j] = M::mma(f, frag_row<T>(Ms, LX, 16 * r, 32 * ks), sum[r][j]);
+                        if (sideB && ks >= r / 2)
+                            sum[r][j] = M::mma(f, frag_col<T>(Ms, LX, 32 * ks, 16 * r), sum[r][j]);
                     }
                 }
-        if (w == 0) {  // lane = token
-            const float2 tot = cc[Q - 1];
-            const float dC_ = (dotC[0][l] + dotC[1][l]) + (dotC[2][l] + dotC[3][l]);
-            const float dB_ = (dotB[0][l] + dotB[1][l]) + (dotB[2][l] + dotB[3][l]);
-            const float ce = (colE[0][l] + colE[1][l]) + (colE[2][l] + colE[3][l]);
-            const float cst = (colS[0][l] + colS[1][l]) + (colS[2][l] + colS[3][l]);
-            float suf = exp2_fast(cc[l].x + cc[l].y) * dC_;
-            float pre = wt[l] * dB_;
+        }
+        if (slot + 1 < kBatch && h + 1 < h1) continue;
+
+        // token gradients of the batch: a wave per head, lane = token
+        if (wave <= slot) {
+            const HeadSums &K = hs[wave];
+            const int hh = h - slot + wave, k = l >> 4;
+            const float2 tot = K.cc[Q - 1], me = K.cc[l];
+            const float dC_ = (K.dotC[0][l] + K.dotC[1][l]) + (K.dotC[2][l] + K.dotC[3][l]);
+            const float dB_ = (K.dotB[0][l] + K.dotB[1][l]) + (K.dotB[2][l] + K.dotB[3][l]);
+            float ce = 0.f, cross = 0.f, left = 0.f;
+#pragma unroll
+            for (int r = 0; r < 4; r++)
+                if (r >= k) {
+                    ce += K.colE[tile_id(r, k)][li];
+                    cross += K.cross[tile_id(r, k)][li];
+                }
+            // sources in tiles left of the token's: rows from it on in its own row of tiles ...
+#pragma unroll
+            for (int q = 0; q < 3; q++)
+                if (q < k) left += K.rows[l][q];
+            left += row_shl<1>(left);
+            left += row_shl<2>(left);
+            left += row_shl<4>(left);
+            left += row_shl<8>(left);
+            cross += left;
+            // ... and whole tiles under that
+#pragma unroll
+            for (int r = 0; r < 4; r++)
+#pragma unroll
+                for (int q = 0; q < 3; q++)
+                    if (r > k && q < k) cross += K.all[tile_id(r, q)];
+            float suf = exp2_fast(me.x + me.y) * dC_;
+            float pre = K.wt[l] * dB_;
 #pragma unroll
             for (int m = 1; m < 64; m <<= 1) {
                 const float a = __shfl_down(suf, m), q = __shfl_up(pre, m);
@@ -758,47 +868,42 @@ __global__ __launch_bounds__(kThreads) void scan_grad_kernel(
                 if (l >= m) pre += q;
             }
             const float up = __shfl_up(pre, 1), before = l ? up : 0.f;
-            const float pass = exp2_fast(tot.x + tot.y) * ((gs[0] + gs[1]) + (gs[2] + gs[3]));
-            float dlr = (cst + suf) + (before + pass);
-            if (l >= rows) dlr = 0.f;
-            float dz = fmaf(A[h], dlr, fmaf(et[l], dB_, ce));
-            if (softplus) dz *= -expm1f(-dl[l]);
-            if (l >= rows) dz = 0.f;
-            if (t0 + l < d.T) ddt[(b * d.T + t0 + l) * d.H + h] = (T)dz;
-            float pa = dl[l] * dlr, pb = dz;
+            const float pass = exp2_fast(tot.x + tot.y) * ((K.gs[0] + K.gs[1]) + (K.gs[2] + K.gs[3]));
+            const float dv = K.dl[l];
+            const float dlr = l < rows ? (cross + suf) + (before + pass) : 0.f;
+            float dz = l < rows ? fmaf(A[hh], dlr, fmaf(K.et[l], dB_, ce)) : 0.f;
+            if (softplus) dz *= -expm1f(-dv);
+            if (t0 + l < d.T) ddt[(b * d.T + t0 + l) * d.H + hh] = (T)dz;
+            float pa = dv * dlr, pb = dz;
 #pragma unroll
             for (int m = 1; m < 64; m <<= 1) {
-                pa += __shfl_xor(pa, m);
-                pb += __shfl_xor(pb, m);
+                pa = xor_add(pa, m);
+                pb = xor_add(pb, m);
             }
             if (l == 0) {
-                float *q = parts + ((b * d.nc + c) * d.H + h) * 3;
+                float *q = parts + ((b * d.nc + c) * d.H + hh) * 3;
                 q[0] = pa;
-                q[1] = (dd[0] + dd[1]) + (dd[2] + dd[3]);
+                q[1] = ((K.dd[0] + K.dd[1]) + (K.dd[2] + K.dd[3])) + ((K.dd[4] + K.dd[5]) + (K.dd[6] + K.dd[7]));
                 q[2] = pb;
             }
         }
     }
     if (!ncols) return;
 #pragma unroll
-    for (int r = 0; r < 4; r++)
+    for (int r = 0; r < 4; r++) {
+        const int t = 16 * r + li;
+        if (t0 + t >= d.T) continue;
+        const int64_t at = ((b * d.T + t0 + t) * d.G + grp) * d.N;
 #pragma unroll
-        for (int j = 0; j < NW; j++)
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const int t = 16 * r + 4 * g + i, n = 16 * (nt0 + j) + li;
-                if (n >= d.N || t0 + t >= d.T) continue;
-                const int64_t at = ((b * d.T + t0 + t) * d.G + grp) * d.N + n;
-                const float vc = t < rows ? dCa[r][j][i] : 0.f, vb = t < rows ? dBa[r][j][i] : 0.f;
-                if (hblocks == 1) {
-                    dC[at] = (T)vc;
-                    dB[at] = (T)vb;
-                } else {
-                    const int64_t all = (int64_t)d.B * d.T * d.G * d.N;
-                    hsum[(2 * hb) * all + at] = vc;
-                    hsum[(2 * hb + 1) * all + at] = vb;
-                }
-            }
+        for (int j = 0; j < NW; j++) {
+            const f32x4 v = t < rows ? sum[r][j] : f32x4{0.f, 0.f, 0.f, 0.f};
+            const int n = 16 * (nt0 + j) + 4 * g;
+            if (hblocks == 1)
+                store4<T, VEC>((sideB ? dB : dC) + at, n, d.N, v);
+            else
+                store4<float, VEC>(hsum + (2 * hb + sideB) * ((int64_t)d.B * d.T * d.G * d.N) + at, n, d.N, v);
+        }
+    }
 }
 
 // dC and dB from the sums of the blocks of heads.
@@ -969,8 +1074,9 @@ Plan plan_of(const sdm_scan_desc &s, bool backward)
         p.start = take(bh * d.nseg * PN * 4);
     }
     if (backward) {
-        p.S = take(bh * d.nc * PN * 4);
-        p.G = take(bh * d.nc * PN * 4);
+        const size_t tile = (size_t)(s.N <= 32 ? 32 : s.N <= 64 ? 64 : 128) * kSlice * 4;
+        p.S = take(bh * d.nc * d.nps * tile);
+        p.G = take(bh * d.nc * d.nps * tile);
         p.parts = take((size_t)s.B * d.nc * s.H * 3 * 4);
         if (p.hblocks > 1) p.hsum = take((size_t)p.hblocks * 2 * s.B * s.T * s.G * s.N * 4);
     }
@@ -1047,7 +1153,7 @@ hipError_t backward(const ScanArgs &a, hipStream_t stream)
     scan_state_kernel<T, NT, true, VEC><<<grid, 2 * kThreads, 0, stream>>>(
         d, dy, yb, yt, Cm, d.cb, d.ct, delta, cs, a.lengths, split ? start : a.dstateT, split ? 0 : 1,
         G, a.dstate0, 1);
-    scan_grad_kernel<T, NT, VEC><<<(unsigned)((int64_t)d.B * d.nc * d.G * p.hblocks), kThreads, 0, stream>>>(
+    scan_grad_kernel<T, NT, VEC><<<(unsigned)((int64_t)d.B * d.nc * d.G * p.hblocks), 2 * kThreads, 0, stream>>>(
         d, p.hblocks, x, dy, Bm, Cm, a.A, a.D, delta, cs, a.lengths, a.d.softplus, S, G, (T *)a.dx,
         (T *)a.ddt, (T *)a.dB, (T *)a.dC, parts, hsum);
     if (p.hblocks > 1) {
