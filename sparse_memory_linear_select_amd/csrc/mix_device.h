@@ -199,6 +199,40 @@ struct Source {
     }
 };
 
+// Writes through a buffer descriptor: four elements from element offset `off`,
+// of which `n` are stored (vectors: all or none), with no branch.
+template <typename T>
+struct Sink {
+    __amdgpu_buffer_rsrc_t r;
+    __device__ __forceinline__ explicit Sink(T *p)
+        : r(__builtin_amdgcn_make_buffer_rsrc((void *)p, 0, (int)kOut, 0x27000))
+    {
+    }
+    template <bool VEC>
+    __device__ __forceinline__ void write4(uint32_t off, int n, f32x4 v) const
+    {
+        typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+        typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+        const auto out = __builtin_convertvector(v, typename Mat<T>::Half);
+        if constexpr (VEC) {
+            const uint32_t at = n > 0 ? off * (uint32_t)sizeof(T) : kOut;
+            if constexpr (sizeof(T) == 2)
+                __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, out), r, at, 0, 0);
+            else
+                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, out), r, at, 0, 0);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const uint32_t at = i < n ? (off + i) * (uint32_t)sizeof(T) : kOut;
+                if constexpr (sizeof(T) == 2)
+                    __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(short, (T)out[i]), r, at, 0, 0);
+                else
+                    __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, (T)out[i]), r, at, 0, 0);
+            }
+        }
+    }
+};
+
 // A ROWS x COLS tile (LDS row stride LD) in two steps, so that a load can be in
 // flight while the previous tile is worked on: rows of a strided tensor to
 // registers, registers to LDS.  Rows from `rows` and columns from `cols` on

@@ -167,9 +167,9 @@ __device__ __forceinline__ void state_add(f32x4 *S, const T *V, const Weighted<T
 // columns each.  Products are taken transposed (M^T, y^T, S^T): a lane then
 // holds one token and four neighbouring columns, so that a token's decay is
 // one number a lane, stores take four columns, and the state's accumulators
-// are the next product's operand as they stand.  The next chunk's tiles are on
-// their way from HBM while a chunk is worked on; with kBufs = 2 they go to a
-// second set of tiles (as long as two sets fit into 160 KB of LDS).
+// are the next product's operand as they stand.  The next two chunks' tiles
+// are on their way from HBM while a chunk is worked on; with kBufs = 2 they go
+// to a second set of tiles (as long as two sets fit into 160 KB of LDS).
 template <typename T, int NT, bool VEC>
 __global__ __launch_bounds__(2 * kThreads) void scan_walk_kernel(
     ScanDims d, const T *__restrict__ x, const T *__restrict__ Bm, const T *__restrict__ Cm,
@@ -208,40 +208,42 @@ __global__ __launch_bounds__(2 * kThreads) void scan_walk_kernel(
     const T *cp = Cm + b * d.cb + (int64_t)grp * d.N;
     const float Dh = D ? D[h] : 0.f;
 
-    TileRegs<T, Q, kSlice, LX, 2 * kThreads, VEC> rx;
-    TileRegs<T, Q, NT * 16, LN, 2 * kThreads, VEC> rb, rc;
-    float rd;
-    float2 rme, rtot;
+    // a chunk's tiles in registers
+    struct Ahead {
+        TileRegs<T, Q, kSlice, LX, 2 * kThreads, VEC> x;
+        TileRegs<T, Q, NT * 16, LN, 2 * kThreads, VEC> b, c;
+        float d;
+        float2 me, tot;
+    };
     const auto rows_of = [&](int c) {
         const int64_t n = len - (int64_t)c * Q;
         return n < 0 ? 0 : n < Q ? (int)n : Q;
     };
-    const auto fetch = [&](int c) {
+    const auto fetch = [&](Ahead &r, int c) {
         const int64_t t0 = (int64_t)c * Q;
         const int rows = rows_of(c);
-        rx.load(xp + t0 * d.xt, d.xt, rows, pcols);
-        rb.load(bp + t0 * d.bt, d.bt, rows, d.N);
-        rc.load(cp + t0 * d.ct, d.ct, rows, d.N);
-        if (threadIdx.x < Q) {
-            const int64_t at = (bh * d.nc + c) * Q;
-            rme = cs[at + threadIdx.x];
-            rtot = cs[at + Q - 1];
-            rd = delta[at + threadIdx.x];
-        }
+        r.x.load(xp + t0 * d.xt, d.xt, rows, pcols);
+        r.b.load(bp + t0 * d.bt, d.bt, rows, d.N);
+        r.c.load(cp + t0 * d.ct, d.ct, rows, d.N);
+        const int64_t at = (bh * d.nc + c) * Q;
+        r.me = cs[at + l];
+        r.tot = cs[at + Q - 1];
+        r.d = delta[at + l];
     };
-    const auto put = [&](int n) {
-        rx.store(Xs[n]);
-        rb.store(Bs[n]);
-        rc.store(Cs[n]);
+    const auto put = [&](const Ahead &r, int n) {
+        r.x.store(Xs[n]);
+        r.b.store(Bs[n]);
+        r.c.store(Cs[n]);
         if (threadIdx.x < Q) {
-            dl[n][threadIdx.x] = rd;
-            cc[n][threadIdx.x] = rme;
-            wt[n][threadIdx.x] = decay(rtot, rme) * rd;
+            dl[n][threadIdx.x] = r.d;
+            cc[n][threadIdx.x] = r.me;
+            wt[n][threadIdx.x] = decay(r.tot, r.me) * r.d;
         }
     };
 
     const int c0 = seg * d.cps, c1 = c0 + d.cps < d.nc ? c0 + d.cps : d.nc;
-    fetch(c0);
+    Ahead r0a, r1a;
+    fetch(r0a, c0);
     f32x4 S[NT];
     const int pl = ps * kSlice + 16 * w + li;
     const auto hand_over = [&](int n) {
@@ -259,13 +261,16 @@ __global__ __launch_bounds__(2 * kThreads) void scan_walk_kernel(
         const Half zero = __builtin_convertvector(f32x4{0.f, 0.f, 0.f, 0.f}, Half);
         *reinterpret_cast<Half *>(Ms + t * LX + 32 * w + 16 + 4 * g) = zero;
     }
-    put(0);
+    put(r0a, 0);
+    fetch(r1a, c0 + 1 < c1 ? c0 + 1 : c0);
     __syncthreads();
-    for (int c = c0; c < c1; c++) {
-        const int n = kBufs == 2 ? (c - c0) & 1 : 0;
+    // Chunk c, with chunk c + 1 in `next`, and chunk c + 2 to be asked for (at the
+    // end the last one once more).  No load or store stands behind a branch, so a
+    // wait for one chunk's loads leaves the next one's in flight.
+    const auto chunk = [&](int c, int n, Ahead &next, Ahead &far) {
         const int64_t t0 = (int64_t)c * Q;
         const int rows = rows_of(c);
-        if (c + 1 < c1) fetch(c + 1);
+        fetch(far, c + 2 < c1 ? c + 2 : c1 - 1);
         if (keeper) {
             const float2 tot = cc[n][Q - 1];
             const float scale = exp2_fast(tot.x + tot.y);
@@ -304,7 +309,8 @@ __global__ __launch_bounds__(2 * kThreads) void scan_walk_kernel(
 #pragma unroll
             for (int ks = 0; ks < 2; ks++) xf[ks] = frag_col<T>(Xs[n], LX, 32 * ks, 16 * w);
             const int p = ps * kSlice + 16 * w + 4 * g;
-            T *yp = y + ((b * d.T + t0 + li) * d.H + h) * d.P + p;
+            const Sink<T> out(y + ((b * d.T + t0) * d.H + h) * d.P);
+            const uint32_t hp = (uint32_t)d.H * d.P;
 #pragma unroll
             for (int r = 0; r < 4; r++) {
                 const int t = 16 * r + li;
@@ -320,44 +326,47 @@ __global__ __launch_bounds__(2 * kThreads) void scan_walk_kernel(
                 const auto xv = *reinterpret_cast<const Half *>(Xs[n] + t * LX + 16 * w + 4 * g);
                 acc += __builtin_convertvector(xv, f32x4) * Dh;
                 if (t >= rows) acc = f32x4{0.f, 0.f, 0.f, 0.f};
-                if (t0 + t < d.T && p < d.P) {
-                    const auto out = __builtin_convertvector(acc, Half);
-                    T *q = yp + (int64_t)(16 * r) * d.H * d.P;
-                    if constexpr (VEC) {
-                        *reinterpret_cast<Half *>(q) = out;
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 4; i++)
-                            if (p + i < d.P) q[i] = out[i];
-                    }
-                }
+                out.template write4<VEC>((uint32_t)t * hp + p, t0 + t < d.T ? d.P - p : 0, acc);
             }
         }
         if (kBufs == 1) {
             __syncthreads();
             if (keeper) hand_over(0);
         }
-        if (c + 1 < c1) put(kBufs == 2 ? n ^ 1 : 0);
+        put(next, kBufs == 2 ? n ^ 1 : 0);
         __syncthreads();
+    };
+    for (int c = c0; c < c1; c += 2) {
+        chunk(c, 0, r1a, r0a);
+        if (c + 1 < c1) chunk(c + 1, kBufs - 1, r0a, r1a);
     }
     if (keeper && seg == d.nseg - 1)
         state_store<NT>(S, state + bh * (int64_t)d.P * d.N, true, 0, pl, d.P, d.N);
 }
 
-// States alone.  Forward (REV = false): U = x, V = B, weights 2^{c_63 - c_s} D_s;
-// `each` gets the state before every chunk.  Reverse: U = dy, V = C, weights
-// 2^{c_t}, chunks from last to first: the gradient G of the state,
+// States alone.  Forward: U = x, V = B, weights 2^{c_63 - c_s} D_s; `each` gets
+// the state before every chunk.  Reverse: U = dy, V = C, weights 2^{c_t},
+// chunks from last to first: the gradient G of the state,
 //   G <- 2^{c_63} G + sum_t 2^{c_t} C_t dy_t^T,
 // and `each` gets G behind every chunk, in tiles of [16 NT][64] per slice whose
 // rows and columns beyond N and P are zero.  `end` gets the last one: per segment
 // in the workspace's layout, or (end_api) the caller's gradient.  Waves w and
-// w + 4 hold the same 16 columns, each one half of the rows n.
-template <typename T, int NT, bool REV, bool VEC>
+// w + 4 hold the same 16 columns, each one half of the rows n.  The backward
+// runs both directions in one launch: a walk is bound by the time of its steps,
+// and two walks share a compute unit.
+template <typename T>
+struct StateJob {
+    const T *U, *V;
+    int64_t ub, ut, vb, vt;
+    const float *init;
+    float *each, *end;
+    int rev, init_api, end_api;
+};
+
+template <typename T, int NT, bool VEC, bool EACH>
 __global__ __launch_bounds__(2 * kThreads) void scan_state_kernel(
-    ScanDims d, const T *__restrict__ U, int64_t ub, int64_t ut, const T *__restrict__ V, int64_t vb,
-    int64_t vt, const float *__restrict__ delta, const float2 *__restrict__ cs,
-    const int32_t *__restrict__ lengths, const float *init, int init_api, float *each, float *end,
-    int end_api)
+    ScanDims d, const float *__restrict__ delta, const float2 *__restrict__ cs,
+    const int32_t *__restrict__ lengths, StateJob<T> job0, StateJob<T> job1)
 {
     constexpr int LN = NT * 16 + 8;
     constexpr int NJ = NT / 2;
@@ -366,6 +375,7 @@ __global__ __launch_bounds__(2 * kThreads) void scan_state_kernel(
     __shared__ __align__(16) float wt[2][Q];
     __shared__ float scale[2];
 
+    const StateJob<T> job = blockIdx.y ? job1 : job0;
     const int seg = blockIdx.x % d.nseg;
     const int64_t r0 = blockIdx.x / d.nseg;
     const int ps = (int)(r0 % d.nps);
@@ -378,46 +388,50 @@ __global__ __launch_bounds__(2 * kThreads) void scan_state_kernel(
     const int pcols = d.P - ps * kSlice < kSlice ? d.P - ps * kSlice : kSlice;
     const int p = ps * kSlice + 16 * w + (threadIdx.x & 15);
     const int64_t PN = (int64_t)d.P * d.N;
-    const T *up = U + b * ub + (int64_t)h * d.P + ps * kSlice;
-    const T *vp = V + b * vb + (int64_t)grp * d.N;
+    const T *up = job.U + b * job.ub + (int64_t)h * d.P + ps * kSlice;
+    const T *vp = job.V + b * job.vb + (int64_t)grp * d.N;
 
     const int c0 = seg * d.cps, c1 = c0 + d.cps < d.nc ? c0 + d.cps : d.nc;
-    TileRegs<T, Q, kSlice, LX, 2 * kThreads, VEC> ru;
-    TileRegs<T, Q, NT * 16, LN, 2 * kThreads, VEC> rv;
-    float rw, rs;
-    const auto chunk = [&](int k) { return REV ? c0 + c1 - 1 - k : k; };
-    const auto fetch = [&](int c) {
+    struct Ahead {
+        TileRegs<T, Q, kSlice, LX, 2 * kThreads, VEC> u;
+        TileRegs<T, Q, NT * 16, LN, 2 * kThreads, VEC> v;
+        float d;
+        float2 me, tot;
+    };
+    const auto chunk_of = [&](int k) { return job.rev ? c0 + c1 - 1 - k : k; };
+    const auto fetch = [&](Ahead &r, int k) {
+        const int c = chunk_of(k);
         const int64_t t0 = (int64_t)c * Q;
         const int rows = len - t0 < 0 ? 0 : len - t0 < Q ? (int)(len - t0) : Q;
-        ru.load(up + t0 * ut, ut, rows, pcols);
-        rv.load(vp + t0 * vt, vt, rows, d.N);
-        if (threadIdx.x < Q) {
-            const int64_t at = (bh * d.nc + c) * Q;
-            const float2 me = cs[at + threadIdx.x], tot = cs[at + Q - 1];
-            rw = REV ? exp2_fast(me.x + me.y) : decay(tot, me) * delta[at + threadIdx.x];
-            rs = exp2_fast(tot.x + tot.y);
-        }
+        r.u.load(up + t0 * job.ut, job.ut, rows, pcols);
+        r.v.load(vp + t0 * job.vt, job.vt, rows, d.N);
+        const int64_t at = (bh * d.nc + c) * Q;
+        r.me = cs[at + (threadIdx.x & 63)];
+        r.tot = cs[at + Q - 1];
+        r.d = delta[at + (threadIdx.x & 63)];
     };
-    const auto put = [&](int n) {
-        ru.store(Us[n]);
-        rv.store(Vs[n]);
-        if (threadIdx.x < Q) wt[n][threadIdx.x] = rw;
-        if (threadIdx.x == 0) scale[n] = rs;
+    const auto put = [&](const Ahead &r, int n) {
+        r.u.store(Us[n]);
+        r.v.store(Vs[n]);
+        if (threadIdx.x < Q)
+            wt[n][threadIdx.x] = job.rev ? exp2_fast(r.me.x + r.me.y) : decay(r.tot, r.me) * r.d;
+        if (threadIdx.x == 0) scale[n] = exp2_fast(r.tot.x + r.tot.y);
     };
-    fetch(chunk(c0));
+    Ahead r0a, r1a;
+    fetch(r0a, c0);
     f32x4 S[NJ];
     {
-        const float *src = init;
-        if (src) src += (init_api ? bh : bh * d.nseg + seg) * PN;
-        state_load<NJ>(S, src, init_api, j0, p, d.P, d.N);
+        const float *src = job.init;
+        if (src) src += (job.init_api ? bh : bh * d.nseg + seg) * PN;
+        state_load<NJ>(S, src, job.init_api, j0, p, d.P, d.N);
     }
-    put(0);
+    put(r0a, 0);
+    fetch(r1a, c0 + 1 < c1 ? c0 + 1 : c0);
     __syncthreads();
-    for (int k = c0; k < c1; k++) {
-        const int n = (k - c0) & 1;
-        if (k + 1 < c1) fetch(chunk(k + 1));
-        if (each) {
-            float *q = each + ((bh * d.nc + chunk(k)) * d.nps + ps) * (NT * 16 * kSlice) +
+    const auto step = [&](int k, int n, Ahead &next, Ahead &far) {
+        fetch(far, k + 2 < c1 ? k + 2 : c1 - 1);
+        if constexpr (EACH) {
+            float *q = job.each + ((bh * d.nc + chunk_of(k)) * d.nps + ps) * (NT * 16 * kSlice) +
                        (16 * j0 + 4 * ((threadIdx.x & 63) >> 4)) * kSlice + 16 * w + (threadIdx.x & 15);
 #pragma unroll
             for (int j = 0; j < NJ; j++)
@@ -426,22 +440,25 @@ __global__ __launch_bounds__(2 * kThreads) void scan_state_kernel(
         }
         const Weighted<T> u(Us[n], wt[n], 16 * w);
         state_add<T, NJ, LN>(S, Vs[n], u, scale[n], j0);
-        if (k + 1 < c1) put(n ^ 1);
+        put(next, n ^ 1);
         __syncthreads();
+    };
+    for (int k = c0; k < c1; k += 2) {
+        step(k, 0, r1a, r0a);
+        if (k + 1 < c1) step(k + 1, 1, r0a, r1a);
     }
-    if (!end) return;
-    if (!end_api)
-        state_store<NJ>(S, end + (bh * d.nseg + seg) * PN, false, j0, p, d.P, d.N);
-    else if (seg == (REV ? 0 : d.nseg - 1))
-        state_store<NJ>(S, end + bh * PN, true, j0, p, d.P, d.N);
+    if (!job.end) return;
+    if (!job.end_api)
+        state_store<NJ>(S, job.end + (bh * d.nseg + seg) * PN, false, j0, p, d.P, d.N);
+    else if (seg == (job.rev ? 0 : d.nseg - 1))
+        state_store<NJ>(S, job.end + bh * PN, true, j0, p, d.P, d.N);
 }
 
 // Joins the segments: from each segment's own contribution (`own`, computed
 // from zero) and the state before the first one, the state before every
 // segment, in the order of the walk.
-template <bool REV>
 __global__ __launch_bounds__(kThreads) void scan_join_kernel(ScanDims d, const float2 *__restrict__ cs,
-                                                             const float *first,
+                                                             int rev, const float *first,
                                                              const float *__restrict__ own,
                                                              float *__restrict__ start)
 {
@@ -464,7 +481,7 @@ __global__ __launch_bounds__(kThreads) void scan_join_kernel(ScanDims d, const f
     float S = first ? first[bh * PN + (int64_t)p * d.N + n] : 0.f;
 #pragma unroll 8
     for (int k = 0; k < d.nseg; k++) {
-        const int seg = REV ? d.nseg - 1 - k : k;
+        const int seg = rev ? d.nseg - 1 - k : k;
         start[(bh * d.nseg + seg) * PN + e] = S;
         S = fmaf(keep[seg], S, own[(bh * d.nseg + seg) * PN + e]);
     }
@@ -1024,7 +1041,7 @@ __global__ __launch_bounds__(kThreads) void scan_step_kernel(
 struct Plan {
     ScanDims d;
     int hblocks;
-    size_t delta, cs, own, start, S, G, parts, hsum, total;
+    size_t delta, cs, own[2], start[2], S, G, parts, hsum, total;
 };
 
 constexpr int64_t kUnits = kMaxSegs;  // workgroups that fill the 256 compute units twice
@@ -1070,8 +1087,10 @@ Plan plan_of(const sdm_scan_desc &s, bool backward)
     p.delta = take(bh * d.nc * Q * 4);
     p.cs = take(bh * d.nc * Q * 8);
     if (d.nseg > 1) {
-        p.own = take(bh * d.nseg * PN * 4);
-        p.start = take(bh * d.nseg * PN * 4);
+        for (int k = 0; k < (backward ? 2 : 1); k++) {
+            p.own[k] = take(bh * d.nseg * PN * 4);
+            p.start[k] = take(bh * d.nseg * PN * 4);
+        }
     }
     if (backward) {
         const size_t tile = (size_t)(s.N <= 32 ? 32 : s.N <= 64 ? 64 : 128) * kSlice * 4;
@@ -1092,19 +1111,32 @@ void run_prep(const ScanArgs &a, const Plan &p, float *delta, float2 *cs, hipStr
         p.d, (const T *)a.dt, a.A, a.dt_bias, a.lengths, a.d.softplus, delta, cs);
 }
 
-// With more than one segment: the state before each (in `start`).
-template <typename T, int NT, bool VEC, bool REV>
-void run_segments(const ScanArgs &a, const Plan &p, const T *U, int64_t ub, int64_t ut, const T *V,
-                  int64_t vb, int64_t vt, const float *first, const float *delta, const float2 *cs,
-                  hipStream_t stream)
+// The walks of `jobs` over whole sequences.  With more than one segment each
+// segment first runs from zero, for the state before every one (in `start`).
+template <typename T, int NT, bool VEC>
+void run_segments(const ScanArgs &a, const Plan &p, StateJob<T> *jobs, int njobs, const float *delta,
+                  const float2 *cs, hipStream_t stream)
 {
     const ScanDims &d = p.d;
-    const unsigned grid = (unsigned)((int64_t)d.B * d.H * d.nps * d.nseg);
-    float *own = (float *)(a.ws + p.own), *start = (float *)(a.ws + p.start);
-    scan_state_kernel<T, NT, REV, VEC><<<grid, 2 * kThreads, 0, stream>>>(
-        d, U, ub, ut, V, vb, vt, delta, cs, a.lengths, nullptr, 0, nullptr, own, 0);
-    scan_join_kernel<REV><<<dim3((d.P * d.N + kThreads - 1) / kThreads, d.B * d.H), kThreads, 0, stream>>>(
-        d, cs, first, own, start);
+    if (d.nseg == 1) return;
+    const dim3 grid((unsigned)((int64_t)d.B * d.H * d.nps * d.nseg), njobs);
+    StateJob<T> own[2];
+    for (int k = 0; k < njobs; k++) {
+        own[k] = jobs[k];
+        own[k].init = nullptr;
+        own[k].each = nullptr;
+        own[k].end = (float *)(a.ws + p.own[k]);
+        own[k].end_api = 0;
+    }
+    scan_state_kernel<T, NT, VEC, false><<<grid, 2 * kThreads, 0, stream>>>(d, delta, cs, a.lengths, own[0],
+                                                                    own[njobs - 1]);
+    for (int k = 0; k < njobs; k++) {
+        float *start = (float *)(a.ws + p.start[k]);
+        scan_join_kernel<<<dim3((d.P * d.N + kThreads - 1) / kThreads, d.B * d.H), kThreads, 0, stream>>>(
+            d, cs, jobs[k].rev, jobs[k].init, own[k].end, start);
+        jobs[k].init = start;
+        jobs[k].init_api = 0;
+    }
 }
 
 template <typename T, int NT, bool VEC>
@@ -1116,15 +1148,11 @@ hipError_t forward(const ScanArgs &a, hipStream_t stream)
     float2 *cs = (float2 *)(a.ws + p.cs);
     run_prep<T>(a, p, delta, cs, stream);
     const T *x = (const T *)a.x, *Bm = (const T *)a.Bm, *Cm = (const T *)a.Cm;
-    const float *init = a.cont ? a.state : nullptr;
-    int api = 1;
-    if (d.nseg > 1) {
-        run_segments<T, NT, VEC, false>(a, p, x, d.xb, d.xt, Bm, d.bb, d.bt, init, delta, cs, stream);
-        init = (const float *)(a.ws + p.start);
-        api = 0;
-    }
-    scan_walk_kernel<T, NT, VEC><<<(unsigned)((int64_t)d.B * d.H * d.nps * d.nseg), 2 * kThreads, 0, stream>>>(
-        d, x, Bm, Cm, a.D, delta, cs, a.lengths, init, api, a.state, (T *)a.y);
+    StateJob<T> job = {x, Bm, d.xb, d.xt, d.bb, d.bt, a.cont ? a.state : nullptr, nullptr, nullptr, 0, 1, 0};
+    run_segments<T, NT, VEC>(a, p, &job, 1, delta, cs, stream);
+    scan_walk_kernel<T, NT, VEC>
+        <<<(unsigned)((int64_t)d.B * d.H * d.nps * d.nseg), 2 * kThreads, 0, stream>>>(
+            d, x, Bm, Cm, a.D, delta, cs, a.lengths, job.init, job.init_api, a.state, (T *)a.y);
     return hipGetLastError();
 }
 
@@ -1137,25 +1165,19 @@ hipError_t backward(const ScanArgs &a, hipStream_t stream)
     float2 *cs = (float2 *)(a.ws + p.cs);
     float *S = (float *)(a.ws + p.S), *G = (float *)(a.ws + p.G);
     float *parts = (float *)(a.ws + p.parts), *hsum = (float *)(a.ws + p.hsum);
-    const float *start = (const float *)(a.ws + p.start);
-    const unsigned grid = (unsigned)((int64_t)d.B * d.H * d.nps * d.nseg);
     const T *x = (const T *)a.x, *Bm = (const T *)a.Bm, *Cm = (const T *)a.Cm, *dy = (const T *)a.dy;
     const int64_t yt = (int64_t)d.H * d.P, yb = d.T * yt;
     run_prep<T>(a, p, delta, cs, stream);
-    const bool split = d.nseg > 1;
-    if (split)
-        run_segments<T, NT, VEC, false>(a, p, x, d.xb, d.xt, Bm, d.bb, d.bt, a.state0, delta, cs, stream);
-    scan_state_kernel<T, NT, false, VEC><<<grid, 2 * kThreads, 0, stream>>>(
-        d, x, d.xb, d.xt, Bm, d.bb, d.bt, delta, cs, a.lengths, split ? start : a.state0,
-        split ? 0 : 1, S, nullptr, 0);
-    if (split)
-        run_segments<T, NT, VEC, true>(a, p, dy, yb, yt, Cm, d.cb, d.ct, a.dstateT, delta, cs, stream);
-    scan_state_kernel<T, NT, true, VEC><<<grid, 2 * kThreads, 0, stream>>>(
-        d, dy, yb, yt, Cm, d.cb, d.ct, delta, cs, a.lengths, split ? start : a.dstateT, split ? 0 : 1,
-        G, a.dstate0, 1);
-    scan_grad_kernel<T, NT, VEC><<<(unsigned)((int64_t)d.B * d.nc * d.G * p.hblocks), 2 * kThreads, 0, stream>>>(
-        d, p.hblocks, x, dy, Bm, Cm, a.A, a.D, delta, cs, a.lengths, a.d.softplus, S, G, (T *)a.dx,
-        (T *)a.ddt, (T *)a.dB, (T *)a.dC, parts, hsum);
+    StateJob<T> jobs[2] = {{x, Bm, d.xb, d.xt, d.bb, d.bt, a.state0, S, nullptr, 0, 1, 0},
+                           {dy, Cm, yb, yt, d.cb, d.ct, a.dstateT, G, a.dstate0, 1, 1, 1}};
+    run_segments<T, NT, VEC>(a, p, jobs, 2, delta, cs, stream);
+    scan_state_kernel<T, NT, VEC, true>
+        <<<dim3((unsigned)((int64_t)d.B * d.H * d.nps * d.nseg), 2), 2 * kThreads, 0, stream>>>(
+            d, delta, cs, a.lengths, jobs[0], jobs[1]);
+    scan_grad_kernel<T, NT, VEC>
+        <<<(unsigned)((int64_t)d.B * d.nc * d.G * p.hblocks), 2 * kThreads, 0, stream>>>(
+            d, p.hblocks, x, dy, Bm, Cm, a.A, a.D, delta, cs, a.lengths, a.d.softplus, S, G, (T *)a.dx,
+            (T *)a.ddt, (T *)a.dB, (T *)a.dC, parts, hsum);
     if (p.hblocks > 1) {
         const int64_t all = (int64_t)d.B * d.T * d.G * d.N;
         scan_heads_kernel<T><<<(unsigned)((all + kThreads - 1) / kThreads), kThreads, 0, stream>>>(
