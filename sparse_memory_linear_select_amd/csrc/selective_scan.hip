@@ -88,6 +88,10 @@ __device__ __forceinline__ float row_shl(float x)
         __builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x100 | n, 0xF, 0xF, true));
 }
 
+// The tiles on and under the diagonal of a 4 x 4 grid: 0 (0,0), 1 (1,0), 2 (1,1) ..
+__device__ __forceinline__ int tile_row(int id) { return id < 1 ? 0 : id < 3 ? 1 : id < 6 ? 2 : 3; }
+__device__ __forceinline__ int tile_id(int row, int col) { return row * (row + 1) / 2 + col; }
+
 // One wave's part of a state: S^T, tiles j0 .. j0 + NJ - 1 of 16 rows n, rows
 // (l / 16) * 4 + i of each, column p of the lane.  In the caller's [P][N]
 // layout or the workspace's [N][P].
@@ -280,26 +284,36 @@ __global__ __launch_bounds__(2 * kThreads) void scan_walk_kernel(
             state_add<T, NF, LN>(S + NF, Bs[n], u, scale, NF);
             if (kBufs == 2) hand_over(n ^ 1);
         } else {
-            // M^T: the ten 16 x 16 tiles on and under the diagonal, tokens in columns
+            // M^T: the ten 16 x 16 tiles on and under the diagonal, tokens in columns.
+            // Three a wave, with no branch between them (the last tile three times over):
+            // what a step costs is the time of its dependent reads and products.
+            f32x4 acc[3];
 #pragma unroll
             for (int k = 0; k < 3; k++) {
-                const int id = w + 4 * k;  // (0,0) (1,0) (1,1) (2,0) ..
-                if (id > 9) break;
-                const int tt = id < 1 ? 0 : id < 3 ? 1 : id < 6 ? 2 : 3, st = id - tt * (tt + 1) / 2;
-                const int t = 16 * tt + li;
-                f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+                const int id = w + 4 * k < 9 ? w + 4 * k : 9;  // (0,0) (1,0) (1,1) (2,0) ..
+                const int tt = tile_row(id), st = id - tile_id(tt, 0);
+                acc[k] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int ks = 0; ks < NF; ks++)
-                    acc = M::mma(frag_row<T>(Bs[n], LN, 16 * st, 32 * ks),
-                                 frag_row<T>(Cs[n], LN, 16 * tt, 32 * ks), acc);
-                const float2 ct = cc[n][t];
+                    acc[k] = M::mma(frag_row<T>(Bs[n], LN, 16 * st, 32 * ks),
+                                    frag_row<T>(Cs[n], LN, 16 * tt, 32 * ks), acc[k]);
+            }
 #pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    const int s = 16 * st + 4 * g + i;
-                    acc[i] = s <= t ? acc[i] * decay(ct, cc[n][s]) * dl[n][s] : 0.f;
-                }
+            for (int k = 0; k < 3; k++) {
+                const int id = w + 4 * k < 9 ? w + 4 * k : 9;
+                const int tt = tile_row(id), st = id - tile_id(tt, 0);
+                const int t = 16 * tt + li, s0 = 16 * st + 4 * g;
+                const float2 ct = cc[n][t];
+                const f32x4 ds = *reinterpret_cast<const f32x4 *>(dl[n] + s0);
+                const f32x4 c0 = *reinterpret_cast<const f32x4 *>(cc[n] + s0);
+                const f32x4 c1 = *reinterpret_cast<const f32x4 *>(cc[n] + s0 + 2);
+                const f32x4 f = {decay(ct, make_float2(c0[0], c0[1])), decay(ct, make_float2(c0[2], c0[3])),
+                                 decay(ct, make_float2(c1[0], c1[1])), decay(ct, make_float2(c1[2], c1[3]))};
+                const f32x4 v = acc[k] * f * ds;
+#pragma unroll
+                for (int i = 0; i < 4; i++) acc[k][i] = s0 + i <= t ? v[i] : 0.f;
                 // the decayed scores are rounded to the inputs' type for the product with x
-                *reinterpret_cast<Half *>(Ms + t * LX + 16 * st + 4 * g) = __builtin_convertvector(acc, Half);
+                *reinterpret_cast<Half *>(Ms + t * LX + s0) = __builtin_convertvector(acc[k], Half);
             }
             __syncthreads();
             // y^T for the wave's columns; the state came rounded to the inputs' type
@@ -526,9 +540,6 @@ struct HeadSums {
     float dotC[4][Q], dotB[4][Q];  // per quarter of n: C_t.(S^T dy_t), B_s.(G^T x_s)
     float gs[4], dd[8];          // <G, S> and sum dy x, in parts
 };
-
-__device__ __forceinline__ int tile_row(int id) { return id < 1 ? 0 : id < 3 ? 1 : id < 6 ? 2 : 3; }
-__device__ __forceinline__ int tile_id(int row, int col) { return row * (row + 1) / 2 + col; }
 
 template <typename T, int NT, bool VEC>
 __global__ __launch_bounds__(2 * kThreads) void scan_grad_kernel(
