@@ -18,44 +18,76 @@
 namespace sdm {
 namespace {
 
-constexpr int kLanes = 64;      // channel vectors of a workgroup
-constexpr int kRuns = 4;        // token runs of a workgroup
-constexpr int kFwdRun = 16;     // tokens of a forward run
-constexpr int kBwdRun = 32;     // tokens of a backward run
-constexpr int kAhead = 8;       // rows loaded before they are used
+constexpr int kLanes = 64;      // channel vectors of a backward workgroup
+constexpr int kRuns = 4;        // token runs of a backward workgroup
+constexpr int kThreads = 256;
+constexpr int kFwdRun = 32;     // tokens of a forward run
+constexpr int kAhead = 8;       // rows of a forward run loaded before they are used
 
 struct ConvDims {
     int64_t T;
     int C, silu;
     int64_t xb, xt;             // strides of x, in elements
-    int cblocks, tblocks;       // workgroups along channels and tokens
+    int nvec;                   // channel vectors
+    int runs;                   // forward: token runs of a sequence
+    int cblocks, tblocks, run;  // backward: workgroups along channels and tokens, tokens of a run
 };
 
-template <typename T, int V, int K>
-__global__ __launch_bounds__(kLanes *kRuns) void conv_fwd_kernel(
-    ConvDims d, const T *__restrict__ x, const float *__restrict__ weight,
-    const float *__restrict__ bias, const int32_t *__restrict__ lengths, int cont, T *state,
-    T *__restrict__ y)
+// 1 / (1 + e^-z) by the hardware's exponential and reciprocal, one unit in the
+// last place each (z log2 e is off by |z| 2^-24, where the result is e^z or 1).
+__device__ __forceinline__ float sigmoid(float z)
 {
-    const int cb = blockIdx.x % d.cblocks;
-    const int64_t rest = blockIdx.x / d.cblocks;
-    const int tb = (int)(rest % d.tblocks);
-    const int64_t b = rest / d.tblocks;
-    const int c = (cb * kLanes + (int)threadIdx.x) * V;
-    const int64_t t0 = ((int64_t)tb * kRuns + threadIdx.y) * kFwdRun;
-    if (c >= d.C || t0 >= d.T) return;
-    const int64_t len = seq_len(lengths, b, d.T);
-    const int64_t t1 = t0 + kFwdRun < d.T ? t0 + kFwdRun : d.T;
-    const T *xp = x + b * d.xb + c;
-    T *yp = y + (b * d.T) * d.C + c;
+    return __builtin_amdgcn_rcpf(1.f + exp2_fast(-1.44269504f * z));
+}
 
-    float w[K][V], bs[V];
+// The K taps of V channels, and their bias.
+template <int V, int K>
+__device__ __forceinline__ void load_taps(const float *__restrict__ weight, const float *__restrict__ bias,
+                                          int c, float (&w)[K][V], float (&bs)[V])
+{
+    const float *p = weight + (int64_t)c * K;
+    float flat[V * K];
+    if constexpr (V * K % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < V * K; i += 4) {
+            const Vec<float, 4> q = vload<float, 4>(p + i);
+#pragma unroll
+            for (int e = 0; e < 4; e++) flat[i + e] = q.e[e];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V * K; i++) flat[i] = p[i];
+    }
 #pragma unroll
     for (int i = 0; i < V; i++) {
         bs[i] = bias ? bias[c + i] : 0.f;
 #pragma unroll
-        for (int k = 0; k < K; k++) w[k][i] = weight[(int64_t)(c + i) * K + k];
+        for (int k = 0; k < K; k++) w[k][i] = flat[i * K + k];
     }
+}
+
+// A thread: V channels and a run of 32 tokens.  Rows are loaded eight at a
+// time and without a branch (rows behind the sequence stand for its last one),
+// so that they are in flight together.
+template <typename T, int V, int K>
+__global__ __launch_bounds__(kThreads) void conv_fwd_kernel(
+    ConvDims d, int64_t total, const T *__restrict__ x, const float *__restrict__ weight,
+    const float *__restrict__ bias, const int32_t *__restrict__ lengths, int cont, T *state,
+    T *__restrict__ y)
+{
+    const int64_t id = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    if (id >= total) return;
+    const int c = (int)(id % d.nvec) * V;
+    const int64_t rest = id / d.nvec;
+    const int64_t b = rest / d.runs, t0 = (rest % d.runs) * kFwdRun;
+    const int64_t len = seq_len(lengths, b, d.T);
+    const int64_t t1 = t0 + kFwdRun < d.T ? t0 + kFwdRun : d.T;
+    const T *xp = x + b * d.xb + c;
+    T *yp = y + (b * d.T) * d.C + c;
+    const int64_t last = len > 0 ? len - 1 : 0;
+
+    float w[K][V], bs[V];
+    load_taps<V, K>(weight, bias, c, w, bs);
     // win: the K - 1 rows before the run
     Vec<T, V> win[K - 1];
 #pragma unroll
@@ -90,35 +122,32 @@ __global__ __launch_bounds__(kLanes *kRuns) void conv_fwd_kernel(
 
     for (int64_t t = t0; t < t1; t += kAhead) {
         Vec<T, V> nx[kAhead];
+        if (len > 0) {
 #pragma unroll
-        for (int u = 0; u < kAhead; u++)
-            if (t + u < len && t + u < t1) nx[u] = vload<T, V>(xp + (t + u) * d.xt);
+            for (int u = 0; u < kAhead; u++)
+                nx[u] = vload<T, V>(xp + (t + u < last ? t + u : last) * d.xt);
+        }
 #pragma unroll
         for (int u = 0; u < kAhead; u++) {
             if (t + u >= t1) break;
             Vec<T, V> out;
-            if (t + u < len) {
 #pragma unroll
-                for (int i = 0; i < V; i++) {
-                    float z = bs[i];
+            for (int i = 0; i < V; i++) {
+                float z = bs[i];
 #pragma unroll
-                    for (int k = 0; k < K - 1; k++) z = fmaf(w[k][i], (float)win[k].e[i], z);
-                    z = fmaf(w[K - 1][i], (float)nx[u].e[i], z);
-                    out.e[i] = (T)(d.silu ? z / (1.f + expf(-z)) : z);
-                }
-#pragma unroll
-                for (int k = 0; k + 1 < K - 1; k++) win[k] = win[k + 1];
-                win[K - 2] = nx[u];
-            } else {
-#pragma unroll
-                for (int i = 0; i < V; i++) out.e[i] = (T)0.f;
+                for (int k = 0; k < K - 1; k++) z = fmaf(w[k][i], (float)win[k].e[i], z);
+                z = fmaf(w[K - 1][i], (float)nx[u].e[i], z);
+                out.e[i] = (T)(t + u < len ? d.silu ? z * sigmoid(z) : z : 0.f);
             }
+#pragma unroll
+            for (int k = 0; k + 1 < K - 1; k++) win[k] = win[k + 1];
+            win[K - 2] = nx[u];
             vstore<T, V>(yp + (t + u) * d.C, out);
         }
     }
 }
 
-// One workgroup: 64 channel vectors x 4 runs of 32 tokens.  A run at token t0
+// One workgroup: 64 channel vectors x 4 runs of tokens.  A run at token t0
 // computes dz for its tokens and the K - 1 after them, and writes dx of its
 // own tokens; the sums for dweight and dbias are joined over the four runs in
 // LDS and written as one row of `partial` per workgroup, which
@@ -131,13 +160,14 @@ __global__ __launch_bounds__(kLanes *kRuns) void conv_bwd_kernel(
     const T *__restrict__ dstateT, T *__restrict__ dx, T *__restrict__ dstate0,
     float *__restrict__ partial)
 {
+    constexpr int kGroup = 4;   // tokens loaded before they are used
     __shared__ float sums[kRuns - 1][kLanes * V];
     const int cb = blockIdx.x % d.cblocks;
     const int64_t rest = blockIdx.x / d.cblocks;
     const int tb = (int)(rest % d.tblocks);
     const int64_t b = rest / d.tblocks;
     const int c = (cb * kLanes + (int)threadIdx.x) * V;
-    const int64_t t0 = ((int64_t)tb * kRuns + threadIdx.y) * kBwdRun;
+    const int64_t t0 = ((int64_t)tb * kRuns + threadIdx.y) * d.run;
     const bool live = c < d.C && t0 < d.T;
 
     float acc[K + 1][V];  // dw_0 .. dw_{K-1}, dbias
@@ -148,17 +178,13 @@ __global__ __launch_bounds__(kLanes *kRuns) void conv_bwd_kernel(
 
     if (live) {
         const int64_t len = seq_len(lengths, b, d.T);
-        const int64_t t1 = t0 + kBwdRun < d.T ? t0 + kBwdRun : d.T;
+        const int64_t t1 = t0 + d.run < d.T ? t0 + d.run : d.T;
+        const int64_t last = len > 0 ? len - 1 : 0;
         const T *xp = x + b * d.xb + c;
         const T *gp = dy + (b * d.T) * d.C + c;
         T *op = dx + (b * d.T) * d.C + c;
         float w[K][V], bs[V];
-#pragma unroll
-        for (int i = 0; i < V; i++) {
-            bs[i] = bias ? bias[c + i] : 0.f;
-#pragma unroll
-            for (int k = 0; k < K; k++) w[k][i] = weight[(int64_t)(c + i) * K + k];
-        }
+        load_taps<V, K>(weight, bias, c, w, bs);
         float win[K][V];  // xe[t .. t + K - 1]
         float dz[K][V];   // dz[t - K + 1 .. t]
 #pragma unroll
@@ -178,58 +204,63 @@ __global__ __launch_bounds__(kLanes *kRuns) void conv_bwd_kernel(
 #pragma unroll
             for (int i = 0; i < V; i++) win[k + 1][i] = (float)v.e[i];
         }
-        for (int64_t t = t0; t < t1 + K - 1; t++) {
+        for (int64_t tg = t0; tg < t1 + K - 1; tg += kGroup) {
+            Vec<T, V> xv[kGroup], gv[kGroup];
+            if (len > 0) {
 #pragma unroll
-            for (int k = 0; k + 1 < K; k++)
+                for (int u = 0; u < kGroup; u++) {
+                    const int64_t r = tg + u < last ? tg + u : last;
+                    xv[u] = vload<T, V>(xp + r * d.xt);
+                    gv[u] = vload<T, V>(gp + r * d.C);
+                }
+            }
 #pragma unroll
-                for (int i = 0; i < V; i++) dz[k][i] = dz[k + 1][i];
-            if (t < len) {
-#pragma unroll
-                for (int k = 0; k + 1 < K; k++)
-#pragma unroll
-                    for (int i = 0; i < V; i++) win[k][i] = win[k + 1][i];
-                const Vec<T, V> xv = vload<T, V>(xp + t * d.xt);
-                const Vec<T, V> gv = vload<T, V>(gp + t * d.C);
+            for (int u = 0; u < kGroup; u++) {
+                const int64_t t = tg + u;
+                if (t >= t1 + K - 1) break;
+                const bool in = t < len, mine = t < t1;
 #pragma unroll
                 for (int i = 0; i < V; i++) {
-                    win[K - 1][i] = (float)xv.e[i];
-                    float g = (float)gv.e[i];
+#pragma unroll
+                    for (int k = 0; k + 1 < K; k++) {
+                        dz[k][i] = dz[k + 1][i];
+                        win[k][i] = win[k + 1][i];
+                    }
+                    win[K - 1][i] = (float)xv[u].e[i];
+                    float g = (float)gv[u].e[i];
                     if (d.silu) {
                         float z = bs[i];
 #pragma unroll
                         for (int k = 0; k < K; k++) z = fmaf(w[k][i], win[k][i], z);
-                        const float s = 1.f / (1.f + expf(-z));
+                        const float s = sigmoid(z);
                         g *= s * fmaf(z, 1.f - s, 1.f);
                     }
+                    g = in ? g : 0.f;
                     dz[K - 1][i] = g;
-                    if (t < t1) {
+                    const float own = mine ? g : 0.f;
 #pragma unroll
-                        for (int k = 0; k < K; k++) acc[k][i] = fmaf(g, win[k][i], acc[k][i]);
-                        acc[K][i] += g;
-                    }
+                    for (int k = 0; k < K; k++) acc[k][i] = fmaf(own, in ? win[k][i] : 0.f, acc[k][i]);
+                    acc[K][i] += own;
                 }
-            } else {
+                // dxe[t] is complete: row t - (K - 1) of x, or row t of the old state
+                const int64_t r = t - (K - 1);
+                if (r < t0 && !(t0 == 0 && r < 0 && dstate0)) continue;
+                Vec<T, V> out;
 #pragma unroll
-                for (int i = 0; i < V; i++) dz[K - 1][i] = 0.f;
+                for (int i = 0; i < V; i++) {
+                    float s = 0.f;
+                    // dz[K - 1 - k] is dz_{t - k}
+#pragma unroll
+                    for (int k = 0; k < K; k++) s = fmaf(w[k][i], dz[K - 1 - k][i], s);
+                    if (dstateT && t >= len && t - len < K - 1)
+                        s += (float)dstateT[(b * (K - 1) + (t - len)) * d.C + c + i];
+                    out.e[i] = (T)s;
+                }
+                if (r >= 0)
+                    vstore<T, V>(op + r * d.C, out);
+                else
+                    vstore<T, V>(dstate0 + (b * (K - 1) + t) * d.C + c, out);
             }
-            // dxe[t] is complete: row t - (K - 1) of x, or row t of the old state
-            const int64_t r = t - (K - 1);
-            if (r < t0 && !(t0 == 0 && r < 0 && dstate0)) continue;
-            Vec<T, V> out;
-#pragma unroll
-            for (int i = 0; i < V; i++) {
-                float s = 0.f;
-                // dz[K - 1 - k] is dz_{t - k}
-#pragma unroll
-                for (int k = 0; k < K; k++) s = fmaf(w[k][i], dz[K - 1 - k][i], s);
-                if (dstateT && t >= len && t - len < K - 1)
-                    s += (float)dstateT[(b * (K - 1) + (t - len)) * d.C + c + i];
-                out.e[i] = (T)s;
-            }
-            if (r >= 0)
-                vstore<T, V>(op + r * d.C, out);
-            else
-                vstore<T, V>(dstate0 + (b * (K - 1) + t) * d.C + c, out);
         }
     }
     float *row = partial + (rest * (K + 1)) * d.C;
@@ -278,7 +309,7 @@ __global__ __launch_bounds__(1024) void conv_reduce_kernel(const float *__restri
     }
 }
 
-ConvDims dims_of(const sdm_conv_desc &d, int V, int run)
+ConvDims dims_of(const sdm_conv_desc &d, int V)
 {
     ConvDims m;
     m.T = d.T;
@@ -286,8 +317,13 @@ ConvDims dims_of(const sdm_conv_desc &d, int V, int run)
     m.silu = d.silu;
     m.xb = d.x_batch;
     m.xt = d.x_token;
-    m.cblocks = (d.C + kLanes * V - 1) / (kLanes * V);
-    m.tblocks = (int)((d.T + kRuns * run - 1) / (kRuns * run));
+    m.nvec = (d.C + V - 1) / V;
+    m.runs = (int)((d.T + kFwdRun - 1) / kFwdRun);
+    m.cblocks = (m.nvec + kLanes - 1) / kLanes;
+    // Backward runs of 32 tokens; of 16 where the workgroups would not fill the
+    // 256 compute units four times (shorter runs overlap more and leave more sums).
+    m.run = (int64_t)d.B * m.cblocks * ((d.T + 127) / 128) >= 1024 ? 32 : 16;
+    m.tblocks = (int)((d.T + kRuns * m.run - 1) / (kRuns * m.run));
     return m;
 }
 
@@ -310,12 +346,13 @@ int vector_width(const ConvArgs &a, int esize)
 template <typename T, int V, int K>
 hipError_t run_conv(const ConvArgs &a, bool backward, hipStream_t stream)
 {
-    const ConvDims m = dims_of(a.d, V, backward ? kBwdRun : kFwdRun);
-    const dim3 grid((unsigned)((int64_t)m.cblocks * m.tblocks * a.d.B)), block(kLanes, kRuns);
+    const ConvDims m = dims_of(a.d, V);
     if (!backward) {
-        conv_fwd_kernel<T, V, K><<<grid, block, 0, stream>>>(
-            m, (const T *)a.x, a.weight, a.bias, a.lengths, a.cont, (T *)a.state, (T *)a.y);
+        const int64_t total = (int64_t)m.nvec * m.runs * a.d.B;
+        conv_fwd_kernel<T, V, K><<<(unsigned)((total + kThreads - 1) / kThreads), kThreads, 0, stream>>>(
+            m, total, (const T *)a.x, a.weight, a.bias, a.lengths, a.cont, (T *)a.state, (T *)a.y);
     } else {
+        const dim3 grid((unsigned)((int64_t)m.cblocks * m.tblocks * a.d.B)), block(kLanes, kRuns);
         conv_bwd_kernel<T, V, K><<<grid, block, 0, stream>>>(
             m, (const T *)a.x, (const T *)a.dy, a.weight, a.bias, a.lengths, (const T *)a.state0,
             (const T *)a.dstateT, (T *)a.dx, (T *)a.dstate0, a.partial);
@@ -360,8 +397,8 @@ hipError_t dispatch_conv(const ConvArgs &a, bool backward, hipStream_t stream)
 
 size_t conv_backward_ws(const sdm_conv_desc &d)
 {
-    const ConvDims m = dims_of(d, 1, kBwdRun);
-    return (size_t)m.tblocks * d.B * (d.K + 1) * d.C * sizeof(float);
+    // the most rows of sums that any vector width leaves: runs of 16 tokens
+    return (size_t)((d.T + 16 * kRuns - 1) / (16 * kRuns)) * d.B * (d.K + 1) * d.C * sizeof(float);
 }
 
 hipError_t launch_conv_forward(const ConvArgs &a, hipStream_t stream)

@@ -23,6 +23,10 @@ constexpr int kThreads = 256;
 constexpr int kMaxSegs = 512;   // segments of the time axis
 constexpr int LX = kSlice + 8;  // LDS row stride of 64-wide tiles
 
+// LDS leaves these kernels two waves a SIMD, so the compiler may use half of the
+// registers for each and need not hold loads back to save some.
+#define TWO_WAVES __attribute__((amdgpu_waves_per_eu(2, 2)))
+
 struct ScanDims {
     int B, H, P, N, G;
     int64_t T;
@@ -175,7 +179,7 @@ __device__ __forceinline__ void state_add(f32x4 *S, const T *V, const Weighted<T
 // are on their way from HBM while a chunk is worked on; with kBufs = 2 they go
 // to a second set of tiles (as long as two sets fit into 160 KB of LDS).
 template <typename T, int NT, bool VEC>
-__global__ __launch_bounds__(2 * kThreads) void scan_walk_kernel(
+__global__ __launch_bounds__(2 * kThreads) TWO_WAVES void scan_walk_kernel(
     ScanDims d, const T *__restrict__ x, const T *__restrict__ Bm, const T *__restrict__ Cm,
     const float *__restrict__ D, const float *__restrict__ delta, const float2 *__restrict__ cs,
     const int32_t *__restrict__ lengths, const float *init, int init_api, float *state,
@@ -350,9 +354,11 @@ __global__ __launch_bounds__(2 * kThreads) void scan_walk_kernel(
         put(next, kBufs == 2 ? n ^ 1 : 0);
         __syncthreads();
     };
-    for (int c = c0; c < c1; c += 2) {
+    for (int c = c0;;) {
         chunk(c, 0, r1a, r0a);
-        if (c + 1 < c1) chunk(c + 1, kBufs - 1, r0a, r1a);
+        if (++c == c1) break;
+        chunk(c, kBufs - 1, r0a, r1a);
+        if (++c == c1) break;
     }
     if (keeper && seg == d.nseg - 1)
         state_store<NT>(S, state + bh * (int64_t)d.P * d.N, true, 0, pl, d.P, d.N);
@@ -457,9 +463,11 @@ __global__ __launch_bounds__(2 * kThreads) void scan_state_kernel(
         put(next, n ^ 1);
         __syncthreads();
     };
-    for (int k = c0; k < c1; k += 2) {
+    for (int k = c0;;) {
         step(k, 0, r1a, r0a);
-        if (k + 1 < c1) step(k + 1, 1, r0a, r1a);
+        if (++k == c1) break;
+        step(k, 1, r0a, r1a);
+        if (++k == c1) break;
     }
     if (!job.end) return;
     if (!job.end_api)
@@ -542,7 +550,7 @@ struct HeadSums {
 };
 
 template <typename T, int NT, bool VEC>
-__global__ __launch_bounds__(2 * kThreads) void scan_grad_kernel(
+__global__ __launch_bounds__(2 * kThreads) TWO_WAVES void scan_grad_kernel(
     ScanDims d, int hblocks, const T *__restrict__ x, const T *__restrict__ dy,
     const T *__restrict__ Bm, const T *__restrict__ Cm, const float *__restrict__ A,
     const float *__restrict__ D, const float *__restrict__ delta, const float2 *__restrict__ cs,
