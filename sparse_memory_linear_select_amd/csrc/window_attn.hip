@@ -15,10 +15,11 @@
 namespace sdm {
 namespace {
 
-constexpr int kRows = 64;     // queries of a workgroup: 16 a wave
-constexpr int kKeys = 64;     // keys of a tile
-constexpr int kThreads = 256;
+constexpr int kTile = 64;     // keys (or queries) of a tile in LDS
+constexpr int kThreads = 256; // of the kernels whose waves hold queries
+constexpr int kKeys = 128;    // keys of a workgroup of the dK, dV kernel: 16 for each of eight waves
 constexpr int kSinkRows = 512;  // queries whose sink gradients one workgroup sums
+constexpr int kFewSinks = 16;   // sinks whose gradients the dQ kernel sums itself
 
 struct WinDims {
     int B, Hq, Hk, D;
@@ -42,43 +43,26 @@ __device__ __forceinline__ int64_t cache_slot(int64_t p, int64_t S, int64_t W)
     return p < S ? p : S + (p - S) % W;
 }
 
-// Fills a 64-row tile: row r from row_of(r) (null: zeros).  D columns, padded
-// with zeros to COLS.
-template <typename T, int COLS, int LD, typename F>
-__device__ __forceinline__ void load_rows(T *tile, F row_of, int D, bool vec)
-{
-    constexpr int V = 16 / sizeof(T);
-    constexpr int PER = COLS / V;
-    for (int e = threadIdx.x; e < 64 * PER; e += kThreads) {
-        const int r = e / PER, c = (e % PER) * V;
-        const T *src = row_of(r);
-        Vec<T, V> v;
-        if (vec && src && c < D) {
-            v = vload<T, V>(src + c);
-        } else {
-#pragma unroll
-            for (int i = 0; i < V; i++) v.e[i] = src && c + i < D ? src[c + i] : (T)0.f;
-        }
-        vstore<T, V>(tile + r * LD + c, v);
-    }
-}
-
-// Fragment of a row in global memory: 8 elements from k, zeros from D on.
-template <typename T>
-__device__ __forceinline__ typename Mat<T>::Frag frag_global(const T *src, int k, int D, bool vec)
+// 8 elements from k of a row, zeros from D on (VEC: all or none).
+template <typename T, bool VEC>
+__device__ __forceinline__ typename Mat<T>::Frag frag_global(const T *row, int k, int D)
 {
     typename Mat<T>::Frag f;
-    if (src && vec && k < D) {
+    if constexpr (VEC) {
         constexpr int V = 16 / sizeof(T);
+        const T *src = row + (k < D ? k : 0);
 #pragma unroll
         for (int u = 0; u < 8 / V; u++) {
-            const Vec<T, V> v = vload<T, V>(src + k + u * V);
+            const Vec<T, V> v = vload<T, V>(src + u * V);
 #pragma unroll
-            for (int i = 0; i < V; i++) f[u * V + i] = v.e[i];
+            for (int i = 0; i < V; i++) f[u * V + i] = k < D ? v.e[i] : (T)0.f;
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; i++) f[i] = src && k + i < D ? src[k + i] : (T)0.f;
+        for (int i = 0; i < 8; i++) {
+            const T v = row[k + i < D ? k + i : 0];
+            f[i] = k + i < D ? v : (T)0.f;
+        }
     }
     return f;
 }
@@ -114,11 +98,12 @@ __device__ __forceinline__ int block_sight(int v0, int shift, int ir0, int W, in
 // access is to a row that exists: columns from D on hold the row's first ones
 // (finite numbers that meet zeros in the other operand, or columns nobody
 // stores).
-template <typename T, int COLS, int LD, bool VEC>
+template <typename T, int COLS, int LD, bool VEC, int THREADS>
 struct RowRegs {
     static constexpr int V = 16 / sizeof(T);
     static constexpr int PER = COLS / V;
-    static constexpr int N = 64 * PER / kThreads;
+    static constexpr int N = (kTile * PER + THREADS - 1) / THREADS;
+    static constexpr bool kWhole = kTile * PER % THREADS == 0;
     Vec<T, V> v[N];
 
     template <typename F>
@@ -126,9 +111,9 @@ struct RowRegs {
     {
 #pragma unroll
         for (int u = 0; u < N; u++) {
-            const int e = threadIdx.x + u * kThreads;
-            const int c = (e % PER) * V;
-            const T *src = row_of(e / PER);
+            const int e = threadIdx.x + u * THREADS;
+            const int c = (e % PER) * V, r = e / PER;
+            const T *src = row_of(kWhole || r < kTile ? r : kTile - 1);
             if constexpr (VEC) {
                 v[u] = vload<T, V>(src + (c < D ? c : 0));
             } else {
@@ -141,8 +126,8 @@ struct RowRegs {
     {
 #pragma unroll
         for (int u = 0; u < N; u++) {
-            const int e = threadIdx.x + u * kThreads;
-            vstore<T, V>(tile + (e / PER) * LD + (e % PER) * V, v[u]);
+            const int e = threadIdx.x + u * THREADS;
+            if (kWhole || e < kTile * PER) vstore<T, V>(tile + (e / PER) * LD + (e % PER) * V, v[u]);
         }
     }
 };
@@ -165,7 +150,10 @@ __device__ __forceinline__ float pair_max(float x, int m)
 // A wave holds QN blocks of 16 queries, over which it uses each fragment of K
 // and V twice: the same queries of two heads that share a key head (HP = 2),
 // or 32 neighbouring queries.  A workgroup is four waves: 64 queries of two
-// heads, or 64 QN queries of one.
+// heads, or 64 QN queries of one, and two workgroups share a compute unit.  (One
+// block a wave, eight waves a workgroup, reads LDS twice as often and runs no
+// more waves: 200 us instead of 165 for 8 x 4096 tokens, 16 and 8 heads of 128,
+// window 128.)  The next tile of keys is loaded while one is worked on.
 template <typename T, int DT, int QN, int HP, bool VEC, bool CACHE>
 __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && DT <= 8 ? 2 : 1) void window_fwd_kernel(
     WinDims d, const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v,
@@ -176,9 +164,9 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && DT <= 8 ? 2 : 1) void w
     using Half = typename M::Half;
     constexpr int LD = DT * 16 + 8;
     constexpr int QR = HP == 2 ? 16 : 16 * QN;   // queries of a wave
-    constexpr int kBufs = 4 * 64 * LD * (int)sizeof(T) <= 160 * 1024 ? 2 : 1;
-    __shared__ __align__(32) T Ks[kBufs][kKeys * LD];
-    __shared__ __align__(32) T Vs[kBufs][kKeys * LD];
+    constexpr int kBufs = 4 * kTile * LD * (int)sizeof(T) <= 160 * 1024 ? 2 : 1;
+    __shared__ __align__(32) T Ks[kBufs][kTile * LD];
+    __shared__ __align__(32) T Vs[kBufs][kTile * LD];
 
     const int64_t blk = xcd_index(blockIdx.x, gridDim.x);
     const int qt = (int)(blk % d.nq);
@@ -209,23 +197,14 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && DT <= 8 ? 2 : 1) void w
         for (int j = 0; j < DT; j++) O[u][j] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
     if (t0 < len) {
-        typename M::Frag qf[QN][DT / 2];
-#pragma unroll
-        for (int u = 0; u < QN; u++) {
-            const T *row = t0 + ir[u] < len ? q + b * d.qb + (t0 + ir[u]) * d.qt +
-                                                  (h0 + (HP == 2 ? u : 0)) * d.qh
-                                            : nullptr;
-#pragma unroll
-            for (int ks = 0; ks < DT / 2; ks++) qf[u][ks] = frag_global<T>(row, 32 * ks + 8 * g, d.D, VEC);
-        }
         const int64_t last = (t0 + 4 * QR < len ? t0 + 4 * QR : len) - 1;
         const KeyList kl(p0 + t0, p0 + last, d.W, S);
-        const int nt = (kl.total + kKeys - 1) / kKeys;
+        const int nt = (kl.total + kTile - 1) / kTile;
         const T *kn = k + b * d.kb + hk * d.kh, *vn = v + b * d.vb + hk * d.vh;
-        RowRegs<T, DT * 16, LD, VEC> rk, rv;
+        RowRegs<T, DT * 16, LD, VEC, kThreads> rk, rv;
         const auto fetch = [&](int n) {
             const auto key = [&](int r) {
-                const int e = n * kKeys + r;
+                const int e = n * kTile + r;
                 return kl.key(e < kl.total ? e : kl.total - 1);
             };
             rk.load([&](int r) {
@@ -240,13 +219,21 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && DT <= 8 ? 2 : 1) void w
             }, d.D);
         };
         fetch(0);
+        typename M::Frag qf[QN][DT / 2];
+#pragma unroll
+        for (int u = 0; u < QN; u++) {
+            const int64_t tr = t0 + ir[u] <= last ? t0 + ir[u] : last;   // a row that exists
+            const T *row = q + b * d.qb + tr * d.qt + (h0 + (HP == 2 ? u : 0)) * d.qh;
+#pragma unroll
+            for (int ks = 0; ks < DT / 2; ks++) qf[u][ks] = frag_global<T, VEC>(row, 32 * ks + 8 * g, d.D);
+        }
         rk.store(Ks[0]);
         rv.store(Vs[0]);
         __syncthreads();
         for (int n = 0; n < nt; n++) {
             const int buf = kBufs == 2 ? n & 1 : 0;
-            if (n + 1 < nt) fetch(n + 1);
-            const int v0 = n * kKeys;
+            fetch(n + 1 < nt ? n + 1 : n);
+            const int v0 = n * kTile;
             int sight[QN][4];
             bool any = false;
 #pragma unroll
@@ -333,10 +320,8 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && DT <= 8 ? 2 : 1) void w
                 }
             }
             if (kBufs == 1) __syncthreads();
-            if (n + 1 < nt) {
-                rk.store(Ks[kBufs == 2 ? buf ^ 1 : 0]);
-                rv.store(Vs[kBufs == 2 ? buf ^ 1 : 0]);
-            }
+            rk.store(Ks[kBufs == 2 ? buf ^ 1 : 0]);
+            rv.store(Vs[kBufs == 2 ? buf ^ 1 : 0]);
             __syncthreads();
         }
     }
@@ -567,21 +552,45 @@ __global__ __launch_bounds__(kThreads) void window_cache_kernel(
     }
 }
 
+// Gradients of the sinks.  Few queries see a key, but all later ones a sink, so
+// their sums are split: part 0 holds the queries that the dK, dV kernel visits
+// for the keys' windows, the others each a part of the queries behind.  With at
+// most 16 sinks the dQ kernel, which has their weights at hand, sums the parts
+// (one a workgroup; `near` = its queries): those of the sinks that stand in
+// front of all its windows.  With more, the dK, dV kernel runs once more, for
+// the sinks alone.
+struct SinkParts {
+    float *sums;     // [part][B][Hk][S][2 D]: dK, dV; null: no query sees a sink from behind its window
+    int near;        // queries of a dQ workgroup that sums its part, or 0
+    int nparts;
+};
+
+__device__ __forceinline__ float *sink_part(const SinkParts &p, const WinDims &d, int64_t part, int64_t b,
+                                            int hk)
+{
+    return p.sums + ((part * d.B + b) * d.Hk + hk) * d.S * 2 * d.D;
+}
+
 // dQ^T += K^T dS^T over the keys, with P^T recomputed from lse and
 // dS = P (dP - delta) scale, dP^T = V dO^T, delta = sum_c dO o (also left in
-// the workspace for the other kernel).  Blocks and tiles as in the forward.
-template <typename T, int DT, int QN, int HP, bool VEC>
+// the workspace for the other kernel).  Rows and tiles as in the forward.
+template <typename T, int DT, int QN, int HP, bool VEC, bool FEW>
 __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && DT <= 8 ? 2 : 1) void window_dq_kernel(
-    WinDims d, const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v,
+    WinDims d, SinkParts sp, const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v,
     const T *__restrict__ o, const T *__restrict__ dout, const float *__restrict__ lse,
     const int32_t *__restrict__ lengths, float *__restrict__ delta, T *__restrict__ dq)
 {
     using M = Mat<T>;
+    using Frag = typename M::Frag;
     constexpr int LD = DT * 16 + 8;
-    constexpr int QR = HP == 2 ? 16 : 16 * QN;
-    constexpr int kBufs = 4 * 64 * LD * (int)sizeof(T) <= 160 * 1024 ? 2 : 1;
-    __shared__ __align__(32) T Ks[kBufs][kKeys * LD];
-    __shared__ __align__(32) T Vs[kBufs][kKeys * LD];
+    constexpr int QR = HP == 2 ? 16 : 16 * QN;    // queries of a wave
+    constexpr int kRows = 64 * QN;                // rows of the workgroup
+    constexpr int LS = kRows + 8;
+    constexpr int kBufs = 4 * kTile * LD * (int)sizeof(T) <= 150 * 1024 ? 2 : 1;
+    __shared__ __align__(32) T Ks[kBufs * kTile * LD];  // at the end (FEW) the rows of Q and dO
+    __shared__ __align__(32) T Vs[kBufs * kTile * LD];
+    __shared__ __align__(32) T Ps[FEW ? 2 : 1][FEW ? kFewSinks * LS : 1];  // sinks' P, dS: [key][row]
+    static_assert(!FEW || kBufs * kTile >= kRows, "room for the rows");
 
     const int64_t blk = xcd_index(blockIdx.x, gridDim.x);
     const int qt = (int)(blk % d.nq);
@@ -592,66 +601,67 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && DT <= 8 ? 2 : 1) void w
     const int64_t len = seq_len(lengths, b, d.T);
     const int64_t t0 = (int64_t)qt * 4 * QR;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int l = threadIdx.x & 63, g = l >> 4;
+    const int l = threadIdx.x & 63, g = l >> 4, li = l & 15;
     const int W = (int)d.W, S = d.S;
     int ir[QN];
-    int64_t at[QN];
     f32x4 O[QN][DT];
 #pragma unroll
     for (int u = 0; u < QN; u++) {
-        ir[u] = QR * w + (HP == 2 ? 0 : 16 * u) + (l & 15);
-        at[u] = (b * d.T + t0 + ir[u]) * d.Hq + h0 + (HP == 2 ? u : 0);
+        ir[u] = QR * w + (HP == 2 ? 0 : 16 * u) + li;
 #pragma unroll
         for (int j = 0; j < DT; j++) O[u][j] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
     if (t0 < len) {
-        typename M::Frag qf[QN][DT / 2], gf[QN][DT / 2];
-        float L[QN], dl[QN];
-#pragma unroll
-        for (int u = 0; u < QN; u++) {
-            const bool live = t0 + ir[u] < len;
-            const T *row = live ? q + b * d.qb + (t0 + ir[u]) * d.qt + (h0 + (HP == 2 ? u : 0)) * d.qh
-                                : nullptr;
-            const T *grow = live ? dout + at[u] * d.D : nullptr;
-            const T *orow = live ? o + at[u] * d.D : nullptr;
-            float s = 0.f;
-#pragma unroll
-            for (int ks = 0; ks < DT / 2; ks++) {
-                qf[u][ks] = frag_global<T>(row, 32 * ks + 8 * g, d.D, VEC);
-                gf[u][ks] = frag_global<T>(grow, 32 * ks + 8 * g, d.D, VEC);
-                const auto of = frag_global<T>(orow, 32 * ks + 8 * g, d.D, VEC);
-#pragma unroll
-                for (int i = 0; i < 8; i++) s = fmaf((float)gf[u][ks][i], (float)of[i], s);
-            }
-            dl[u] = xor_add(xor_add(s, 16), 32);
-            if (live && g == 0) delta[at[u]] = dl[u];
-            L[u] = live ? lse[at[u]] * 1.4426950408889634f : 0.f;
-        }
         const int64_t last = (t0 + 4 * QR < len ? t0 + 4 * QR : len) - 1;
         const KeyList kl(t0, last, d.W, S);
-        const int nt = (kl.total + kKeys - 1) / kKeys;
+        const int nt = (kl.total + kTile - 1) / kTile;
         const T *kn = k + b * d.kb + hk * d.kh, *vn = v + b * d.vb + hk * d.vh;
-        RowRegs<T, DT * 16, LD, VEC> rk, rv;
+        RowRegs<T, DT * 16, LD, VEC, kThreads> rk, rv;
         const auto fetch = [&](int n) {
             const auto key = [&](int r) {
-                const int e = n * kKeys + r;
+                const int e = n * kTile + r;
                 return kl.key(e < kl.total ? e : kl.total - 1);
             };
             rk.load([&](int r) { return kn + key(r) * d.kt; }, d.D);
             rv.load([&](int r) { return vn + key(r) * d.vt; }, d.D);
         };
         fetch(0);
-        rk.store(Ks[0]);
-        rv.store(Vs[0]);
+        Frag qf[QN][DT / 2], gf[QN][DT / 2];
+        float L[QN], dl[QN];
+#pragma unroll
+        for (int u = 0; u < QN; u++) {
+            const bool live = t0 + ir[u] <= last;
+            const int64_t tr = live ? t0 + ir[u] : last;   // a row that exists
+            const int h = h0 + (HP == 2 ? u : 0);
+            const int64_t ar = (b * d.T + tr) * d.Hq + h;
+            float s = 0.f;
+#pragma unroll
+            for (int ks = 0; ks < DT / 2; ks++) {
+                qf[u][ks] = frag_global<T, VEC>(q + b * d.qb + tr * d.qt + h * d.qh, 32 * ks + 8 * g, d.D);
+                gf[u][ks] = frag_global<T, VEC>(dout + ar * d.D, 32 * ks + 8 * g, d.D);
+                const Frag of = frag_global<T, VEC>(o + ar * d.D, 32 * ks + 8 * g, d.D);
+#pragma unroll
+                for (int i = 0; i < 8; i++) {
+                    gf[u][ks][i] = live ? gf[u][ks][i] : (T)0.f;
+                    s = fmaf((float)gf[u][ks][i], (float)of[i], s);
+                }
+            }
+            dl[u] = xor_add(xor_add(s, 16), 32);
+            if (live && g == 0) delta[ar] = dl[u];
+            L[u] = lse[ar] * 1.4426950408889634f;
+        }
+        rk.store(Ks);
+        rv.store(Vs);
         __syncthreads();
         for (int n = 0; n < nt; n++) {
             const int buf = kBufs == 2 ? n & 1 : 0;
-            if (n + 1 < nt) fetch(n + 1);
-            const int v0 = n * kKeys;
+            const T *Kt = Ks + buf * kTile * LD, *Vt = Vs + buf * kTile * LD;
+            fetch(n + 1 < nt ? n + 1 : n);
+            const int v0 = n * kTile;
 #pragma unroll
             for (int kp = 0; kp < 2; kp++) {
                 int sight[QN][2];
-                bool any = false;
+                int any = 0;
 #pragma unroll
                 for (int u = 0; u < QN; u++)
 #pragma unroll
@@ -659,7 +669,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && DT <= 8 ? 2 : 1) void w
                         sight[u][e] = HP == 2 && u ? sight[0][e]
                                                    : block_sight(v0 + 32 * kp + 16 * e, kl.shift,
                                                                  QR * w + (HP == 2 ? 0 : 16 * u), W, S);
-                        any = any || sight[u][e];
+                        any |= sight[u][e];
                     }
                 if (!any) continue;
                 f32x4 s[QN][2], dp[QN][2];
@@ -669,8 +679,8 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && DT <= 8 ? 2 : 1) void w
                     for (int u = 0; u < QN; u++) s[u][kt] = dp[u][kt] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                     for (int ks = 0; ks < DT / 2; ks++) {
-                        const auto ka = frag_row<T>(Ks[buf], LD, 32 * kp + 16 * kt, 32 * ks);
-                        const auto va = frag_row<T>(Vs[buf], LD, 32 * kp + 16 * kt, 32 * ks);
+                        const auto ka = frag_row<T>(Kt, LD, 32 * kp + 16 * kt, 32 * ks);
+                        const auto va = frag_row<T>(Vt, LD, 32 * kp + 16 * kt, 32 * ks);
 #pragma unroll
                         for (int u = 0; u < QN; u++) {
                             s[u][kt] = M::mma(ka, qf[u][ks], s[u][kt]);
@@ -678,75 +688,112 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && DT <= 8 ? 2 : 1) void w
                         }
                     }
                 }
-                typename M::Frag sf[QN];
+                Frag sf[QN];
 #pragma unroll
                 for (int u = 0; u < QN; u++) {
 #pragma unroll
-                    for (int kt = 0; kt < 2; kt++)
+                    for (int kt = 0; kt < 2; kt++) {
 #pragma unroll
                         for (int e = 0; e < 4; e++) {
                             const float p = exp2_fast(fmaf(s[u][kt][e], d.c2, -L[u]));
-                            float ds = p * (dp[u][kt][e] - dl[u]) * d.scale;
-                            if (sight[u][kt] != 2) {
-                                const int ve = v0 + 32 * kp + 16 * kt + 4 * g + e, jr = ve + kl.shift;
-                                ds = jr <= ir[u] && (ve < S || jr > ir[u] - W) ? ds : 0.f;
-                            }
-                            s[u][kt][e] = ds;
+                            dp[u][kt][e] = p * (dp[u][kt][e] - dl[u]) * d.scale;
+                            s[u][kt][e] = p;
                         }
+                        if (FEW && kp == 0 && kt == 0 && n == 0) {
+                            // weights of the sinks in front; the others of the block count as none here
+                            const int rho = 16 * (w * QN + u) + li;
+#pragma unroll
+                            for (int e = 0; e < 4; e++) {
+                                const bool front = 4 * g + e < kl.ns;
+                                Ps[0][(4 * g + e) * LS + rho] = (T)(front ? s[u][0][e] : 0.f);
+                                Ps[1][(4 * g + e) * LS + rho] = (T)(front ? dp[u][0][e] : 0.f);
+                            }
+                        }
+                        if (sight[u][kt] != 2)
+#pragma unroll
+                            for (int e = 0; e < 4; e++) {
+                                const int ve = v0 + 32 * kp + 16 * kt + 4 * g + e, jr = ve + kl.shift;
+                                const bool see = jr <= ir[u] && (ve < S || jr > ir[u] - W);
+                                dp[u][kt][e] = see ? dp[u][kt][e] : 0.f;
+                            }
+                    }
                     // dS is rounded to the inputs' type for the product with K
-                    sf[u] = frag_acc<T>(s[u][0], s[u][1]);
+                    sf[u] = frag_acc<T>(dp[u][0], dp[u][1]);
                 }
 #pragma unroll
                 for (int j = 0; j < DT; j++) {
-                    const auto a = frag_col_pair<T>(Ks[buf], LD, 32 * kp, 16 * j);
+                    const auto a = frag_col_pair<T>(Kt, LD, 32 * kp, 16 * j);
 #pragma unroll
                     for (int u = 0; u < QN; u++) O[u][j] = M::mma(a, sf[u], O[u][j]);
                 }
             }
             if (kBufs == 1) __syncthreads();
-            if (n + 1 < nt) {
-                rk.store(Ks[kBufs == 2 ? buf ^ 1 : 0]);
-                rv.store(Vs[kBufs == 2 ? buf ^ 1 : 0]);
-            }
+            rk.store(Ks + (kBufs == 2 ? (buf ^ 1) * kTile * LD : 0));
+            rv.store(Vs + (kBufs == 2 ? (buf ^ 1) * kTile * LD : 0));
             __syncthreads();
+        }
+        if constexpr (FEW) {
+            if (kl.ns > 0) {   // dK, dV of the sinks in front over the workgroup's rows
+#pragma unroll
+                for (int u = 0; u < QN; u++)
+#pragma unroll
+                    for (int ks = 0; ks < DT / 2; ks++) {
+                        const int at = (16 * (w * QN + u) + li) * LD + 32 * ks + 8 * g;
+                        *reinterpret_cast<Frag *>(Ks + at) = qf[u][ks];
+                        *reinterpret_cast<Frag *>(Vs + at) = gf[u][ks];
+                    }
+                __syncthreads();
+                const int per = d.Hq / d.Hk / HP;
+                float *pp = sink_part(sp, d, 1 + (int64_t)qt * per + (h0 / HP) % per, b, hk);
+                for (int c = w; c < 2 * DT; c += 4) {
+                    const bool isV = c >= DT;
+                    const int c0 = 16 * (isV ? c - DT : c);
+                    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int ks = 0; ks < kRows / 32; ks++)
+                        acc = M::mma(frag_row<T>(Ps[isV ? 0 : 1], LS, 0, 32 * ks),
+                                     frag_col<T>(isV ? Vs : Ks, LD, 32 * ks, c0), acc);
+#pragma unroll
+                    for (int e = 0; e < 4; e++)
+                        if (4 * g + e < kl.ns && c0 + li < d.D)
+                            pp[(4 * g + e) * 2 * d.D + (isV ? d.D : 0) + c0 + li] = acc[e];
+                }
+            }
         }
     }
 #pragma unroll
     for (int u = 0; u < QN; u++) {
         const int64_t t = t0 + ir[u];
         if (t >= d.T) continue;
+        T *row = dq + ((b * d.T + t) * d.Hq + h0 + (HP == 2 ? u : 0)) * d.D;
 #pragma unroll
         for (int j = 0; j < DT; j++)
-            store4<T, VEC>(dq + at[u] * d.D, 16 * j + 4 * g, d.D,
-                           t < len ? O[u][j] : f32x4{0.f, 0.f, 0.f, 0.f});
+            store4<T, VEC>(row, 16 * j + 4 * g, d.D, t < len ? O[u][j] : f32x4{0.f, 0.f, 0.f, 0.f});
     }
 }
 
-// dK and dV: a lane holds one key of KN blocks of 16 (columns) and four
-// neighbouring queries (rows), a workgroup 64 KN keys, over the query heads of
-// their key head.  SINKS = false: the queries that some window over the keys
-// reaches; the sums of sinks go to part 0 of `parts`.  SINKS = true: the sinks
-// for the queries behind those, 512 a workgroup, into parts 1 ..
-template <typename T, int DT, int KN, bool VEC, bool SINKS>
-__global__ __launch_bounds__(kThreads) void window_dkv_kernel(
-    WinDims d, int ntiles, int nparts, const T *__restrict__ q, const T *__restrict__ k,
+// dK and dV of 128 keys, 16 a wave, over the query heads of their key head: a
+// lane holds one key (column) and four neighbouring queries (rows).  SINKS:
+// the sinks alone, for the queries behind part 0, 512 a workgroup, into parts 1 ..
+template <typename T, int DT, bool VEC, bool SINKS>
+__global__ __launch_bounds__(4 * kKeys) void window_dkv_kernel(
+    WinDims d, SinkParts sp, int ntiles, const T *__restrict__ q, const T *__restrict__ k,
     const T *__restrict__ v, const T *__restrict__ dout, const float *__restrict__ lse,
     const float *__restrict__ delta, const int32_t *__restrict__ lengths, T *__restrict__ dk,
-    T *__restrict__ dv, float *__restrict__ parts)
+    T *__restrict__ dv)
 {
     using M = Mat<T>;
     constexpr int LD = DT * 16 + 8;
-    constexpr int KR = 64 * KN;                   // keys of a workgroup
-    constexpr int kBufs = 4 * 64 * LD * (int)sizeof(T) <= 156 * 1024 ? 2 : 1;
-    __shared__ __align__(32) T Qs[kBufs][kRows * LD];
-    __shared__ __align__(32) T Gs[kBufs][kRows * LD];
-    __shared__ __align__(16) float Ls[kBufs][kRows], Dl[kBufs][kRows];
+    constexpr int kBufs = 4 * kTile * LD * (int)sizeof(T) <= 156 * 1024 ? 2 : 1;
+    __shared__ __align__(32) T Qs[kBufs][kTile * LD];
+    __shared__ __align__(32) T Gs[kBufs][kTile * LD];
+    __shared__ __align__(16) float Ls[kBufs][kTile], Dl[kBufs][kTile];
 
     int64_t rest = xcd_index(blockIdx.x, gridDim.x);
     int part = 0;
     if (SINKS) {
-        part = 1 + (int)(rest % (nparts - 1));
-        rest /= nparts - 1;
+        part = 1 + (int)(rest % (sp.nparts - 1));
+        rest /= sp.nparts - 1;
     }
     const int kt = (int)(rest % ntiles);
     rest /= ntiles;
@@ -755,19 +802,20 @@ __global__ __launch_bounds__(kThreads) void window_dkv_kernel(
     const int64_t len = seq_len(lengths, b, d.T);
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int l = threadIdx.x & 63, g = l >> 4;
-    const int W = (int)d.W, S = d.S;
-    const int64_t j0 = (int64_t)kt * KR;
-    const int k0 = 16 * KN * w;                   // the wave's keys, relative to j0
-    const int sinks = (int)(S > j0 ? S - j0 : 0);   // keys below this one are sinks
+    const int W = (int)d.W;
+    const int64_t j0 = (int64_t)kt * kKeys;
+    const int k0 = 16 * w, kr = k0 + (l & 15);    // the wave's first key and the lane's, relative to j0
+    const int64_t j = j0 + kr;
+    const int sinks = (int)(d.S > j0 ? d.S - j0 : 0);   // keys below this one are sinks
     const int per = d.Hq / d.Hk;
-    f32x4 dK[KN][DT], dV[KN][DT];
+    f32x4 dK[DT], dV[DT];
 #pragma unroll
-    for (int u = 0; u < KN; u++)
-#pragma unroll
-        for (int n = 0; n < DT; n++) dK[u][n] = dV[u][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int n = 0; n < DT; n++) dK[n] = dV[n] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    // the queries: [first, end)
-    const int64_t reach = j0 + KR - 1 + d.W;
+    // The queries [first, end).  Where the dQ kernel sums the sinks in front of a
+    // workgroup's windows, the queries of the last workgroup that has one inside
+    // are visited here.
+    const int64_t reach = j0 + kKeys - 1 + d.W + (sinks ? sp.near : 0);
     int64_t first = j0, end = reach < len ? reach : len;
     if (SINKS) {
         first = (int64_t)(part - 1) * kSinkRows;
@@ -775,160 +823,150 @@ __global__ __launch_bounds__(kThreads) void window_dkv_kernel(
         if (first < reach) first = reach;   // nearer queries are in part 0
     }
     if (j0 < len && first < end) {
-        typename M::Frag kf[KN][DT / 2], vf[KN][DT / 2];
-#pragma unroll
-        for (int u = 0; u < KN; u++) {
-            const int64_t j = j0 + k0 + 16 * u + (l & 15);
-            const T *krow = j < len ? k + b * d.kb + j * d.kt + hk * d.kh : nullptr;
-            const T *vrow = j < len ? v + b * d.vb + j * d.vt + hk * d.vh : nullptr;
-#pragma unroll
-            for (int ks = 0; ks < DT / 2; ks++) {
-                kf[u][ks] = frag_global<T>(krow, 32 * ks + 8 * g, d.D, VEC);
-                vf[u][ks] = frag_global<T>(vrow, 32 * ks + 8 * g, d.D, VEC);
-            }
-        }
-        const int nq = (int)((end - first + kRows - 1) / kRows);
-        RowRegs<T, DT * 16, LD, VEC> rq, rg;
+        typename M::Frag kf[DT / 2], vf[DT / 2];
+        const int64_t jr = j < len ? j : len - 1;  // a row that exists; no query sees its copy
+        const int nq = (int)((end - first + kTile - 1) / kTile);
+        RowRegs<T, DT * 16, LD, VEC, 4 * kKeys> rq, rg;
         float rl, rd;
         const auto fetch = [&](int n) {
             const int h = hk * per + n / nq;
-            const int64_t t0 = first + (int64_t)(n % nq) * kRows;
+            const int64_t t0 = first + (int64_t)(n % nq) * kTile;
             const auto row = [&](int r) { return t0 + r < end ? t0 + r : end - 1; };
             rq.load([&](int r) { return q + b * d.qb + row(r) * d.qt + h * d.qh; }, d.D);
             rg.load([&](int r) { return dout + ((b * d.T + row(r)) * d.Hq + h) * d.D; }, d.D);
-            if (threadIdx.x < kRows) {
-                const int64_t at = (b * d.T + row(threadIdx.x)) * d.Hq + h;
-                rl = lse[at] * 1.4426950408889634f;
-                rd = delta[at];
-            }
+            const int64_t at = (b * d.T + row(l)) * d.Hq + h;
+            rl = lse[at] * 1.4426950408889634f;
+            rd = delta[at];
         };
         const auto put = [&](int buf) {
             rq.store(Qs[buf]);
             rg.store(Gs[buf]);
-            if (threadIdx.x < kRows) {
-                Ls[buf][threadIdx.x] = rl;
-                Dl[buf][threadIdx.x] = rd;
+            if (threadIdx.x < kTile) {
+                Ls[buf][l] = rl;
+                Dl[buf][l] = rd;
             }
         };
         fetch(0);
+#pragma unroll
+        for (int ks = 0; ks < DT / 2; ks++) {
+            kf[ks] = frag_global<T, VEC>(k + b * d.kb + jr * d.kt + hk * d.kh, 32 * ks + 8 * g, d.D);
+            vf[ks] = frag_global<T, VEC>(v + b * d.vb + jr * d.vt + hk * d.vh, 32 * ks + 8 * g, d.D);
+        }
         put(0);
         __syncthreads();
         for (int n = 0; n < per * nq; n++) {
             const int buf = kBufs == 2 ? n & 1 : 0;
-            if (n + 1 < per * nq) fetch(n + 1);
+            fetch(n + 1 < per * nq ? n + 1 : n);
             // first query of the tile relative to j0 (sinks: any number behind all keys will do)
-            const int64_t t0 = first + (int64_t)(n % nq) * kRows;
-            const int q0 = SINKS ? KR : (int)(t0 - j0);
+            const int64_t t0 = first + (int64_t)(n % nq) * kTile;
+            const int q0 = SINKS ? kKeys : (int)(t0 - j0);
             const int qend = q0 + (int)(end - t0);
 #pragma unroll
             for (int half = 0; half < 2; half++) {
-                const int r0 = 32 * half;
-                int sight[KN];
-                bool any = false;
-#pragma unroll
-                for (int u = 0; u < KN; u++) {  // as block_sight, for 16 keys and 32 queries
-                    const int c0 = k0 + 16 * u, c1 = c0 + 15, s0 = q0 + r0, s1 = s0 + 31;
-                    const bool none = c0 > s1 || s0 >= qend ||
-                                      (SINKS ? c0 >= sinks : c0 >= sinks && s0 - c1 >= W);
-                    const bool all = c1 <= s0 && s1 < qend && (c1 < sinks || (!SINKS && s1 - c0 < W));
-                    sight[u] = none ? 0 : all ? 2 : 1;
-                    any = any || sight[u];
-                }
-                if (!any) continue;
-                f32x4 p[KN][2], ds[KN][2];
+                const int r0 = 32 * half, k1 = k0 + 15, s0 = q0 + r0, s1 = s0 + 31;
+                // as block_sight, for 16 keys and 32 queries
+                const bool none = k0 > s1 || s0 >= qend ||
+                                  (k0 >= sinks && (SINKS || s0 - k1 >= W));
+                const bool all = k1 <= s0 && s1 < qend &&
+                                 (SINKS ? k1 < sinks : s1 - k0 < W || (k1 < sinks && !sp.near));
+                if (none) continue;
+                f32x4 p[2], ds[2];
 #pragma unroll
                 for (int e2 = 0; e2 < 2; e2++) {
-                    f32x4 s[KN], dp[KN];
-#pragma unroll
-                    for (int u = 0; u < KN; u++) s[u] = dp[u] = f32x4{0.f, 0.f, 0.f, 0.f};
+                    f32x4 s = {0.f, 0.f, 0.f, 0.f}, dp = s;
 #pragma unroll
                     for (int ks = 0; ks < DT / 2; ks++) {
-                        const auto qa = frag_row<T>(Qs[buf], LD, r0 + 16 * e2, 32 * ks);
-                        const auto ga = frag_row<T>(Gs[buf], LD, r0 + 16 * e2, 32 * ks);
-#pragma unroll
-                        for (int u = 0; u < KN; u++) {
-                            s[u] = M::mma(qa, kf[u][ks], s[u]);
-                            dp[u] = M::mma(ga, vf[u][ks], dp[u]);
-                        }
+                        s = M::mma(frag_row<T>(Qs[buf], LD, r0 + 16 * e2, 32 * ks), kf[ks], s);
+                        dp = M::mma(frag_row<T>(Gs[buf], LD, r0 + 16 * e2, 32 * ks), vf[ks], dp);
                     }
                     const f32x4 L = *reinterpret_cast<const f32x4 *>(Ls[buf] + r0 + 16 * e2 + 4 * g);
                     const f32x4 D = *reinterpret_cast<const f32x4 *>(Dl[buf] + r0 + 16 * e2 + 4 * g);
 #pragma unroll
-                    for (int u = 0; u < KN; u++)
+                    for (int e = 0; e < 4; e++) {
+                        p[e2][e] = exp2_fast(fmaf(s[e], d.c2, -L[e]));
+                        ds[e2][e] = p[e2][e] * (dp[e] - D[e]) * d.scale;
+                    }
+                    if (!all)
 #pragma unroll
                         for (int e = 0; e < 4; e++) {
-                            float pe = exp2_fast(fmaf(s[u][e], d.c2, -L[e]));
-                            float de = pe * (dp[u][e] - D[e]) * d.scale;
-                            if (sight[u] != 2) {
-                                const int kr = k0 + 16 * u + (l & 15), qr = q0 + r0 + 16 * e2 + 4 * g + e;
-                                const bool see = kr <= qr && qr < qend &&
-                                                 (kr < sinks || (!SINKS && qr - kr < W));
-                                pe = see ? pe : 0.f;
-                                de = see ? de : 0.f;
-                            }
-                            p[u][e2][e] = pe;
-                            ds[u][e2][e] = de;
+                            const int qr = q0 + r0 + 16 * e2 + 4 * g + e;
+                            // a sink: all, or (near) where it stands in the query's workgroup's list
+                            // behind its first window key
+                            const int from = sp.near ? qr & ~(sp.near - 1) : kr;
+                            const bool see = kr <= qr && qr < qend &&
+                                             (SINKS ? kr < sinks : qr - kr < W || (kr < sinks && from - kr < W));
+                            p[e2][e] = see ? p[e2][e] : 0.f;
+                            ds[e2][e] = see ? ds[e2][e] : 0.f;
                         }
                 }
                 // P and dS are rounded to the inputs' type for the products with dO and Q
-                typename M::Frag pf[KN], sf[KN];
-#pragma unroll
-                for (int u = 0; u < KN; u++) {
-                    pf[u] = frag_acc<T>(p[u][0], p[u][1]);
-                    sf[u] = frag_acc<T>(ds[u][0], ds[u][1]);
-                }
+                const auto pf = frag_acc<T>(p[0], p[1]), sf = frag_acc<T>(ds[0], ds[1]);
 #pragma unroll
                 for (int c = 0; c < DT; c++) {
-                    const auto ga = frag_col_pair<T>(Gs[buf], LD, r0, 16 * c);
-                    const auto qa = frag_col_pair<T>(Qs[buf], LD, r0, 16 * c);
-#pragma unroll
-                    for (int u = 0; u < KN; u++) {
-                        dV[u][c] = M::mma(ga, pf[u], dV[u][c]);
-                        dK[u][c] = M::mma(qa, sf[u], dK[u][c]);
-                    }
+                    dV[c] = M::mma(frag_col_pair<T>(Gs[buf], LD, r0, 16 * c), pf, dV[c]);
+                    dK[c] = M::mma(frag_col_pair<T>(Qs[buf], LD, r0, 16 * c), sf, dK[c]);
                 }
             }
             if (kBufs == 1) __syncthreads();
-            if (n + 1 < per * nq) put(kBufs == 2 ? buf ^ 1 : 0);
+            put(kBufs == 2 ? buf ^ 1 : 0);
             __syncthreads();
         }
     }
+    const bool sink = sp.sums && kr < sinks;
+    if (j >= d.T || (SINKS && !sink)) return;
+    const int64_t at = ((b * d.T + j) * d.Hk + hk) * d.D;
+    float *pp = sink ? sink_part(sp, d, part, b, hk) + j * 2 * d.D : nullptr;
 #pragma unroll
-    for (int u = 0; u < KN; u++) {
-        const int kr = k0 + 16 * u + (l & 15);
-        const int64_t j = j0 + kr;
-        const bool sink = parts && kr < sinks;
-        if (j >= d.T || (SINKS && !sink)) continue;
-        const int64_t at = ((b * d.T + j) * d.Hk + hk) * d.D;
-        float *pp = sink ? parts + ((((int64_t)part * d.B + b) * d.Hk + hk) * d.S + j) * 2 * d.D : nullptr;
-#pragma unroll
-        for (int c = 0; c < DT; c++) {
-            if (sink) {
-                store4<float, false>(pp, 16 * c + 4 * g, d.D, dK[u][c]);
-                store4<float, false>(pp + d.D, 16 * c + 4 * g, d.D, dV[u][c]);
-            } else {
-                store4<T, VEC>(dk + at, 16 * c + 4 * g, d.D, dK[u][c]);
-                store4<T, VEC>(dv + at, 16 * c + 4 * g, d.D, dV[u][c]);
-            }
+    for (int c = 0; c < DT; c++) {
+        if (sink) {
+            store4<float, false>(pp, 16 * c + 4 * g, d.D, dK[c]);
+            store4<float, false>(pp + d.D, 16 * c + 4 * g, d.D, dV[c]);
+        } else {
+            store4<T, VEC>(dk + at, 16 * c + 4 * g, d.D, dK[c]);
+            store4<T, VEC>(dv + at, 16 * c + 4 * g, d.D, dV[c]);
         }
     }
 }
 
-// dK and dV of the sinks: the sum of their parts, in order.
+// dK and dV of the sinks: the sum of their parts, in order: 8 strided sums of a
+// column, joined pairwise.  Parts of workgroups without the sink in front of
+// their windows were not written (near).
 template <typename T>
-__global__ __launch_bounds__(kThreads) void window_sinks_kernel(WinDims d, int nparts,
-                                                                const float *__restrict__ parts,
-                                                                T *__restrict__ dk, T *__restrict__ dv)
+__global__ __launch_bounds__(1024) void window_sinks_kernel(WinDims d, SinkParts sp, int per,
+                                                            const int32_t *__restrict__ lengths,
+                                                            T *__restrict__ dk, T *__restrict__ dv)
 {
+    __shared__ float sums[8][128];
     const int64_t r = blockIdx.x;   // (b, hk, j)
     const int64_t j = r % d.S, bh = r / d.S, hk = bh % d.Hk, b = bh / d.Hk;
     if (j >= d.T) return;
+    const int64_t len = seq_len(lengths, b, d.T);
     const int64_t step = (int64_t)d.B * d.Hk * d.S * 2 * d.D;
-    for (int c = threadIdx.x; c < 2 * d.D; c += kThreads) {
+    const int x = threadIdx.x, y = threadIdx.y;
+    for (int c0 = 0; c0 < 2 * d.D; c0 += 128) {
+        const int c = c0 + x;
         float s = 0.f;
-        for (int n = 0; n < nparts; n++) s += parts[n * step + r * 2 * d.D + c];
-        T *out = c < d.D ? dk : dv;
-        out[((b * d.T + j) * d.Hk + hk) * d.D + (c < d.D ? c : c - d.D)] = (T)s;
+        if (c < 2 * d.D) {
+            const float *src = sp.sums + r * 2 * d.D + c;
+            if (y == 0) s = src[0];
+            for (int n = 1 + y; n < sp.nparts; n += 8) {
+                if (sp.near) {
+                    const int64_t t0 = (int64_t)((n - 1) / per) * sp.near;
+                    if (t0 >= len || t0 - d.W + 1 <= j) continue;
+                }
+                s += src[n * step];
+            }
+        }
+        __syncthreads();
+        sums[y][x] = s;
+        for (int n = 4; n > 0; n >>= 1) {
+            __syncthreads();
+            if (y < n) sums[y][x] += sums[y + n][x];
+        }
+        if (y == 0 && c < 2 * d.D) {
+            T *out = c < d.D ? dk : dv;
+            out[((b * d.T + j) * d.Hk + hk) * d.D + (c < d.D ? c : c - d.D)] = (T)sums[0][x];
+        }
     }
 }
 
@@ -956,28 +994,39 @@ WinDims dims_of(const sdm_window_desc &s)
     d.vt = s.v_token;
     d.vh = s.v_head;
     d.cap = s.sinks + s.window;
-    d.nq = (int)((s.T + kRows - 1) / kRows);
     return d;
 }
 
-// Keys of a wave of the dK, dV kernel in blocks of 16: two, so that each
-// fragment of Q and dO serves 32 keys, unless D = 256 fills the registers.
-constexpr int key_blocks(int D) { return D <= 128 ? 2 : 1; }
+// Blocks of 16 queries of a wave (D = 256 fills the registers with one), and the
+// heads of a workgroup: two where an even number of them shares a key head.
+constexpr int query_blocks(int D) { return D <= 128 ? 2 : 1; }
+int head_pair(const sdm_window_desc &s)
+{
+    return query_blocks(s.D) == 2 && (s.Hq / s.Hk) % 2 == 0 ? 2 : 1;
+}
+int queries_of(const sdm_window_desc &s) { return 64 * query_blocks(s.D) / head_pair(s); }
 
 struct BackPlan {
-    size_t delta, parts, total;
-    int nparts, ktiles;
+    size_t parts, total;
+    int near, nparts, ktiles;
 };
 
 BackPlan back_plan(const sdm_window_desc &s)
 {
     BackPlan p = {};
-    size_t at = ((size_t)s.B * s.T * s.Hq * 4 + 255) & ~(size_t)255;
+    size_t at = ((size_t)s.B * s.T * s.Hq * 4 + 255) & ~(size_t)255;   // delta
     // sinks that queries see from behind their window
     if (s.sinks > 0 && s.T > s.window) {
-        const int64_t keys = 64 * key_blocks(s.D), rows = s.sinks < s.T ? s.sinks : s.T;
-        p.nparts = 1 + (int)((s.T + kSinkRows - 1) / kSinkRows);
-        p.ktiles = (int)((rows + keys - 1) / keys);
+        const int hp = head_pair(s);
+        // the dQ kernel sums few sinks itself, where LDS holds its rows
+        if (s.sinks <= kFewSinks && s.D <= 128) {
+            p.near = queries_of(s);
+            p.nparts = 1 + (int)((s.T + p.near - 1) / p.near) * (s.Hq / s.Hk / hp);
+        } else {
+            const int64_t rows = s.sinks < s.T ? s.sinks : s.T;
+            p.nparts = 1 + (int)((s.T + kSinkRows - 1) / kSinkRows);
+            p.ktiles = (int)((rows + kKeys - 1) / kKeys);
+        }
         p.parts = at;
         at += (size_t)p.nparts * s.B * s.Hk * s.sinks * 2 * s.D * 4;
     }
@@ -988,22 +1037,21 @@ BackPlan back_plan(const sdm_window_desc &s)
 template <typename T, int DT, bool VEC>
 hipError_t forward(const WindowArgs &a, hipStream_t stream)
 {
+    constexpr int QN = query_blocks(DT * 16);
     WinDims d = dims_of(a.d);
-    constexpr int QN = DT == 16 ? 1 : 2;  // D = 256 fills the registers with one
-    const auto run = [&](auto kernel, int hp, int queries) {
-        d.nq = (int)((d.T + queries - 1) / queries);
+    const int hp = head_pair(a.d), queries = queries_of(a.d);
+    d.nq = (int)((d.T + queries - 1) / queries);
+    const auto run = [&](auto kernel) {
         kernel<<<(unsigned)((int64_t)d.B * (d.Hq / hp) * d.nq), kThreads, 0, stream>>>(
             d, (const T *)a.q, (const T *)a.k, (const T *)a.v, (const T *)a.cache_k,
             (const T *)a.cache_v, a.pos, a.lengths, (T *)a.o, a.lse);
     };
-    // heads in pairs where an even number of them shares a key head
-    const bool pairs = QN == 2 && (d.Hq / d.Hk) % 2 == 0;
     if (a.pos)
-        pairs ? run(window_fwd_kernel<T, DT, QN, QN, VEC, true>, 2, 64)
-              : run(window_fwd_kernel<T, DT, QN, 1, VEC, true>, 1, 64 * QN);
+        hp == 2 ? run(window_fwd_kernel<T, DT, QN, QN, VEC, true>)
+                : run(window_fwd_kernel<T, DT, QN, 1, VEC, true>);
     else
-        pairs ? run(window_fwd_kernel<T, DT, QN, QN, VEC, false>, 2, 64)
-              : run(window_fwd_kernel<T, DT, QN, 1, VEC, false>, 1, 64 * QN);
+        hp == 2 ? run(window_fwd_kernel<T, DT, QN, QN, VEC, false>)
+                : run(window_fwd_kernel<T, DT, QN, 1, VEC, false>);
     if (a.cache_k) {
         const int64_t span = (d.S < d.T ? d.S : d.T) + (d.W < d.T ? d.W : d.T);
         window_cache_kernel<T><<<(unsigned)(span * d.B), kThreads, 0, stream>>>(
@@ -1017,29 +1065,33 @@ hipError_t backward(const WindowArgs &a, hipStream_t stream)
 {
     WinDims d = dims_of(a.d);
     const BackPlan p = back_plan(a.d);
-    constexpr int QN = DT == 16 ? 1 : 2, KN = key_blocks(DT * 16);
+    constexpr int QN = query_blocks(DT * 16);
+    const int hp = head_pair(a.d), queries = queries_of(a.d);
     const T *q = (const T *)a.q, *k = (const T *)a.k, *v = (const T *)a.v, *dout = (const T *)a.dout;
-    float *delta = (float *)a.ws, *parts = p.nparts ? (float *)(a.ws + p.parts) : nullptr;
-    const auto run = [&](auto kernel, int hp, int queries) {
-        d.nq = (int)((d.T + queries - 1) / queries);
+    float *delta = (float *)a.ws;
+    const SinkParts sp = {p.nparts ? (float *)(a.ws + p.parts) : nullptr, p.near, p.nparts};
+    d.nq = (int)((d.T + queries - 1) / queries);
+    const auto run = [&](auto kernel) {
         kernel<<<(unsigned)((int64_t)d.B * (d.Hq / hp) * d.nq), kThreads, 0, stream>>>(
-            d, q, k, v, (const T *)a.oin, dout, a.lse_in, a.lengths, delta, (T *)a.dq);
+            d, sp, q, k, v, (const T *)a.oin, dout, a.lse_in, a.lengths, delta, (T *)a.dq);
     };
-    if (QN == 2 && (d.Hq / d.Hk) % 2 == 0)
-        run(window_dq_kernel<T, DT, QN, QN, VEC>, 2, 64);
+    constexpr bool kCan = DT <= 8;   // few sinks: up to 128 columns
+    if (p.near)
+        hp == 2 ? run(window_dq_kernel<T, DT, QN, QN, VEC, kCan>)
+                : run(window_dq_kernel<T, DT, QN, 1, VEC, kCan>);
     else
-        run(window_dq_kernel<T, DT, QN, 1, VEC>, 1, 64 * QN);
-    const int ntiles = (int)((d.T + 64 * KN - 1) / (64 * KN));
-    window_dkv_kernel<T, DT, KN, VEC, false><<<(unsigned)((int64_t)d.B * d.Hk * ntiles), kThreads, 0, stream>>>(
-        d, ntiles, p.nparts, q, k, v, dout, a.lse_in, delta, a.lengths, (T *)a.dk, (T *)a.dv, parts);
-    if (p.nparts) {
-        window_dkv_kernel<T, DT, KN, VEC, true>
-            <<<(unsigned)((int64_t)d.B * d.Hk * p.ktiles * (p.nparts - 1)), kThreads, 0, stream>>>(
-                d, p.ktiles, p.nparts, q, k, v, dout, a.lse_in, delta, a.lengths, (T *)a.dk, (T *)a.dv,
-                parts);
-        window_sinks_kernel<T><<<(unsigned)((int64_t)d.B * d.Hk * d.S), kThreads, 0, stream>>>(
-            d, p.nparts, parts, (T *)a.dk, (T *)a.dv);
-    }
+        hp == 2 ? run(window_dq_kernel<T, DT, QN, QN, VEC, false>)
+                : run(window_dq_kernel<T, DT, QN, 1, VEC, false>);
+    const int ntiles = (int)((d.T + kKeys - 1) / kKeys);
+    window_dkv_kernel<T, DT, VEC, false><<<(unsigned)((int64_t)d.B * d.Hk * ntiles), 4 * kKeys, 0, stream>>>(
+        d, sp, ntiles, q, k, v, dout, a.lse_in, delta, a.lengths, (T *)a.dk, (T *)a.dv);
+    if (p.ktiles)
+        window_dkv_kernel<T, DT, VEC, true>
+            <<<(unsigned)((int64_t)d.B * d.Hk * p.ktiles * (p.nparts - 1)), 4 * kKeys, 0, stream>>>(
+                d, sp, p.ktiles, q, k, v, dout, a.lse_in, delta, a.lengths, (T *)a.dk, (T *)a.dv);
+    if (p.nparts)
+        window_sinks_kernel<T><<<(unsigned)((int64_t)d.B * d.Hk * d.S), dim3(128, 8), 0, stream>>>(
+            d, sp, d.Hq / d.Hk / hp, a.lengths, (T *)a.dk, (T *)a.dv);
     return hipGetLastError();
 }
 
