@@ -85,6 +85,8 @@ struct KeyList {
     __device__ int64_t key(int v) const { return v < ns ? v : lo + (v - ns); }
 };
 
+// (Masks of single numbers below are written with & and |: && and || become
+// branches, and a wave that branches waits for every read in turn.)
 // What 16 neighbouring entries from v0 are to 16 neighbouring queries from ir0
 // (relative to i0): 0 none is seen, 1 some are, 2 all are.
 __device__ __forceinline__ int block_sight(int v0, int shift, int ir0, int W, int S)
@@ -275,7 +277,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && DT <= 8 ? 2 : 1) void w
 #pragma unroll
                             for (int e = 0; e < 4; e++) {
                                 const int ve = v0 + 16 * kt + 4 * g + e, jr = ve + kl.shift;
-                                const bool see = jr <= ir[u] && (ve < S || jr > ir[u] - W);
+                                const bool see = (jr <= ir[u]) & ((ve < S) | (jr > ir[u] - W));
                                 s[u][kt][e] = see ? s[u][kt][e] * d.c2 : -INFINITY;
                             }
                         }
@@ -713,7 +715,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && DT <= 8 ? 2 : 1) void w
 #pragma unroll
                             for (int e = 0; e < 4; e++) {
                                 const int ve = v0 + 32 * kp + 16 * kt + 4 * g + e, jr = ve + kl.shift;
-                                const bool see = jr <= ir[u] && (ve < S || jr > ir[u] - W);
+                                const bool see = (jr <= ir[u]) & ((ve < S) | (jr > ir[u] - W));
                                 dp[u][kt][e] = see ? dp[u][kt][e] : 0.f;
                             }
                     }
@@ -893,8 +895,9 @@ __global__ __launch_bounds__(4 * kKeys) void window_dkv_kernel(
                             // a sink: all, or (near) where it stands in the query's workgroup's list
                             // behind its first window key
                             const int from = sp.near ? qr & ~(sp.near - 1) : kr;
-                            const bool see = kr <= qr && qr < qend &&
-                                             (SINKS ? kr < sinks : qr - kr < W || (kr < sinks && from - kr < W));
+                            const bool see = (kr <= qr) & (qr < qend) &
+                                             (SINKS ? kr < sinks
+                                                    : (qr - kr < W) | ((kr < sinks) & (from - kr < W)));
                             p[e2][e] = see ? p[e2][e] : 0.f;
                             ds[e2][e] = see ? ds[e2][e] : 0.f;
                         }
