@@ -171,7 +171,7 @@ __device__ __forceinline__ void state_add(f32x4 *S, const T *V, const Weighted<T
 // segment) in order.  Its eight waves work in two roles, so that every SIMD
 // has two waves whose waits fall at different times: waves 0 .. 3 hold the
 // state in registers, 16 columns each, update it and hand it to the others
-// through LDS, rounded; waves 4 .. 7 compute M (shared through LDS) and y, 16
+// through LDS, rounded (read before a step's barrier, replaced behind it); waves 4 .. 7 compute M (shared through LDS) and y, 16
 // columns each.  Products are taken transposed (M^T, y^T, S^T): a lane then
 // holds one token and four neighbouring columns, so that a token's decay is
 // one number a lane, stores take four columns, and the state's accumulators
@@ -195,7 +195,7 @@ __global__ __launch_bounds__(2 * kThreads) TWO_WAVES void scan_walk_kernel(
     __shared__ __align__(32) T Bs[kBufs][Q * LN];
     __shared__ __align__(32) T Cs[kBufs][Q * LN];
     __shared__ __align__(32) T Ms[Q * LX];
-    __shared__ __align__(32) Frag Sf[kBufs][4][NF][64];
+    __shared__ __align__(32) Frag Sf[4][NF][64];
     __shared__ __align__(16) float dl[kBufs][Q], wt[kBufs][Q];
     __shared__ __align__(16) float2 cc[kBufs][Q];
 
@@ -254,15 +254,15 @@ __global__ __launch_bounds__(2 * kThreads) TWO_WAVES void scan_walk_kernel(
     fetch(r0a, c0);
     f32x4 S[NT];
     const int pl = ps * kSlice + 16 * w + li;
-    const auto hand_over = [&](int n) {
+    const auto hand_over = [&]() {
 #pragma unroll
-        for (int j = 0; j < NF; j++) Sf[n][w][j][l] = frag_acc<T>(S[2 * j], S[2 * j + 1]);
+        for (int j = 0; j < NF; j++) Sf[w][j][l] = frag_acc<T>(S[2 * j], S[2 * j + 1]);
     };
     if (keeper) {
         const float *src = init;
         if (src) src += (init_api ? bh : bh * d.nseg + seg) * (int64_t)d.P * d.N;
         state_load<NT>(S, src, init_api, 0, pl, d.P, d.N);
-        hand_over(0);
+        hand_over();
     } else if (w < 2) {
         // the two tiles right of the diagonal that products read: sources behind the tokens
         const int t = 32 * w + li;
@@ -286,7 +286,7 @@ __global__ __launch_bounds__(2 * kThreads) TWO_WAVES void scan_walk_kernel(
             state_add<T, NF, LN>(S, Bs[n], u, scale, 0);
             __syncthreads();
             state_add<T, NF, LN>(S + NF, Bs[n], u, scale, NF);
-            if (kBufs == 2) hand_over(n ^ 1);
+            hand_over();
         } else {
             // M^T: the ten 16 x 16 tiles on and under the diagonal, tokens in columns.
             // Three a wave, with no branch between them (the last tile three times over):
@@ -319,25 +319,31 @@ __global__ __launch_bounds__(2 * kThreads) TWO_WAVES void scan_walk_kernel(
                 // the decayed scores are rounded to the inputs' type for the product with x
                 *reinterpret_cast<Half *>(Ms + t * LX + s0) = __builtin_convertvector(acc[k], Half);
             }
-            __syncthreads();
-            // y^T for the wave's columns; the state came rounded to the inputs' type
+            // y^T for the wave's columns.  What comes from the state needs no M, so it is
+            // taken before the barrier; the state came rounded to the inputs' type.
             Frag sf[NF], xf[2];
 #pragma unroll
-            for (int j = 0; j < NF; j++) sf[j] = Sf[n][w][j][l];
+            for (int j = 0; j < NF; j++) sf[j] = Sf[w][j][l];
 #pragma unroll
             for (int ks = 0; ks < 2; ks++) xf[ks] = frag_col<T>(Xs[n], LX, 32 * ks, 16 * w);
+            f32x4 yr[4];
+#pragma unroll
+            for (int r = 0; r < 4; r++) {
+                yr[r] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int j = 0; j < NF; j++)
+                    yr[r] = M::mma(sf[j], frag_row_pair<T>(Cs[n], LN, 16 * r, 32 * j), yr[r]);
+                const float2 ct = cc[n][16 * r + li];
+                yr[r] *= exp2_fast(ct.x + ct.y);
+            }
+            __syncthreads();
             const int p = ps * kSlice + 16 * w + 4 * g;
             const Sink<T> out(y + ((b * d.T + t0) * d.H + h) * d.P);
             const uint32_t hp = (uint32_t)d.H * d.P;
 #pragma unroll
             for (int r = 0; r < 4; r++) {
                 const int t = 16 * r + li;
-                f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int j = 0; j < NF; j++)
-                    acc = M::mma(sf[j], frag_row_pair<T>(Cs[n], LN, 16 * r, 32 * j), acc);
-                const float2 ct = cc[n][t];
-                acc *= exp2_fast(ct.x + ct.y);
+                f32x4 acc = yr[r];
 #pragma unroll
                 for (int ks = 0; ks <= r / 2; ks++)
                     acc = M::mma(xf[ks], frag_row<T>(Ms, LX, 16 * r, 32 * ks), acc);
@@ -347,10 +353,7 @@ __global__ __launch_bounds__(2 * kThreads) TWO_WAVES void scan_walk_kernel(
                 out.template write4<VEC>((uint32_t)t * hp + p, t0 + t < d.T ? d.P - p : 0, acc);
             }
         }
-        if (kBufs == 1) {
-            __syncthreads();
-            if (keeper) hand_over(0);
-        }
+        if (kBufs == 1) __syncthreads();
         put(next, kBufs == 2 ? n ^ 1 : 0);
         __syncthreads();
     };

@@ -166,7 +166,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && DT <= 8 ? 2 : 1) void w
     using Half = typename M::Half;
     constexpr int LD = DT * 16 + 8;
     constexpr int QR = HP == 2 ? 16 : 16 * QN;   // queries of a wave
-    constexpr int kBufs = 4 * kTile * LD * (int)sizeof(T) <= 160 * 1024 ? 2 : 1;
+    constexpr int kBufs = sizeof(T) == 2 ? 2 : 1;
     __shared__ __align__(32) T Ks[kBufs][kTile * LD];
     __shared__ __align__(32) T Vs[kBufs][kTile * LD];
 
@@ -588,7 +588,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && DT <= 8 ? 2 : 1) void w
     constexpr int QR = HP == 2 ? 16 : 16 * QN;    // queries of a wave
     constexpr int kRows = 64 * QN;                // rows of the workgroup
     constexpr int LS = kRows + 8;
-    constexpr int kBufs = 4 * kTile * LD * (int)sizeof(T) <= 150 * 1024 ? 2 : 1;
+    constexpr int kBufs = sizeof(T) == 2 ? 2 : 1;
     __shared__ __align__(32) T Ks[kBufs * kTile * LD];  // at the end (FEW) the rows of Q and dO
     __shared__ __align__(32) T Vs[kBufs * kTile * LD];
     __shared__ __align__(32) T Ps[FEW ? 2 : 1][FEW ? kFewSinks * LS : 1];  // sinks' P, dS: [key][row]
@@ -1000,14 +1000,16 @@ WinDims dims_of(const sdm_window_desc &s)
     return d;
 }
 
-// Blocks of 16 queries of a wave (D = 256 fills the registers with one), and the
-// heads of a workgroup: two where an even number of them shares a key head.
-constexpr int query_blocks(int D) { return D <= 128 ? 2 : 1; }
+// Blocks of 16 queries of a wave (D = 256 fills the registers with one, float32
+// LDS with the tiles), and the heads of a workgroup: two where an even number
+// of them shares a key head.
+constexpr int query_blocks(int D, int esize) { return D <= 128 && esize == 2 ? 2 : 1; }
+int blocks_of(const sdm_window_desc &s) { return query_blocks(s.D, s.dtype == SDM_F32 ? 4 : 2); }
 int head_pair(const sdm_window_desc &s)
 {
-    return query_blocks(s.D) == 2 && (s.Hq / s.Hk) % 2 == 0 ? 2 : 1;
+    return blocks_of(s) == 2 && (s.Hq / s.Hk) % 2 == 0 ? 2 : 1;
 }
-int queries_of(const sdm_window_desc &s) { return 64 * query_blocks(s.D) / head_pair(s); }
+int queries_of(const sdm_window_desc &s) { return 64 * blocks_of(s) / head_pair(s); }
 
 struct BackPlan {
     size_t parts, total;
@@ -1040,7 +1042,7 @@ BackPlan back_plan(const sdm_window_desc &s)
 template <typename T, int DT, bool VEC>
 hipError_t forward(const WindowArgs &a, hipStream_t stream)
 {
-    constexpr int QN = query_blocks(DT * 16);
+    constexpr int QN = query_blocks(DT * 16, sizeof(T));
     WinDims d = dims_of(a.d);
     const int hp = head_pair(a.d), queries = queries_of(a.d);
     d.nq = (int)((d.T + queries - 1) / queries);
@@ -1068,7 +1070,7 @@ hipError_t backward(const WindowArgs &a, hipStream_t stream)
 {
     WinDims d = dims_of(a.d);
     const BackPlan p = back_plan(a.d);
-    constexpr int QN = query_blocks(DT * 16);
+    constexpr int QN = query_blocks(DT * 16, sizeof(T));
     const int hp = head_pair(a.d), queries = queries_of(a.d);
     const T *q = (const T *)a.q, *k = (const T *)a.k, *v = (const T *)a.v, *dout = (const T *)a.dout;
     float *delta = (float *)a.ws;
