@@ -570,6 +570,7 @@ __global__ __launch_bounds__(2 * kThreads) TWO_WAVES void scan_grad_kernel(
     constexpr int kBufs = sizeof(T) == 2 ? 2 : 1;
     constexpr bool kGs = sizeof(T) == 2;          // G, rounded, through LDS
     constexpr int kTile = NT * 16 * kSlice;       // floats of a state tile
+    constexpr bool kEarly = NT < 8;
     __shared__ __align__(32) T Xs[kBufs][Q * LX];
     __shared__ __align__(32) T Ys[kBufs][Q * LX];
     __shared__ __align__(32) T Bs[Q * LN];
@@ -605,7 +606,10 @@ __global__ __launch_bounds__(2 * kThreads) TWO_WAVES void scan_grad_kernel(
         const int pcols = d.P - ps * kSlice < kSlice ? d.P - ps * kSlice : kSlice;
         rx.load(x + b * d.xb + t0 * d.xt + (int64_t)h * d.P + ps * kSlice, d.xt, rows, pcols);
         ry.load(dy + (b * d.T + t0) * yt + (int64_t)h * d.P + ps * kSlice, yt, rows, pcols);
+    };
+    const auto fetch_states = [&](int step) {
         if (!ncols) return;
+        const int h = h0 + step / d.nps, ps = step % d.nps;
         const int64_t at = (((b * d.H + h) * d.nc + c) * d.nps + ps) * kTile + (16 * nt0 + li) * kSlice + 8 * g;
 #pragma unroll
         for (int ks = 0; ks < 2; ks++)
@@ -619,6 +623,7 @@ __global__ __launch_bounds__(2 * kThreads) TWO_WAVES void scan_grad_kernel(
                 }
     };
     fetch(0);
+    fetch_states(0);
     load_tile<T, Q, NT * 16, LN, 2 * kThreads, VEC>(
         Bs, Bm + b * d.bb + t0 * d.bt + (int64_t)grp * d.N, d.bt, rows, d.N);
     load_tile<T, Q, NT * 16, LN, 2 * kThreads, VEC>(
@@ -683,7 +688,8 @@ __global__ __launch_bounds__(2 * kThreads) TWO_WAVES void scan_grad_kernel(
 #pragma unroll
                 for (int i = 0; i < 4; i++) {
                     const int t = 16 * tr + 4 * g + i;
-                    E[k][i] = s <= t ? decay(H.cc[t], ccs) : 0.f;
+                    const float e = decay(H.cc[t], ccs);
+                    E[k][i] = s <= t ? e : 0.f;
                     Ms[t * LX + s] = (T)(CB[k][i] * E[k][i] * ds);
                 }
             }
@@ -696,29 +702,41 @@ __global__ __launch_bounds__(2 * kThreads) TWO_WAVES void scan_grad_kernel(
         if (kBufs == 1 && step) __syncthreads();
         rx.store(Xs[buf]);
         ry.store(Ys[buf]);
-        // the state of the wave's side in three terms
-        Frag sf[2][NW][M::kTerms];
-        if (ncols)
+        // the state of the wave's side in three terms, of one half of the columns at a time
+        // where N = 128 leaves no registers for both
+        Frag sf[kEarly ? 2 : 1][NW][M::kTerms];
+        const auto split = [&](int ks, int at) {
+#pragma unroll
+            for (int j = 0; j < NW; j++) {
+                f32x8 v;
+#pragma unroll
+                for (int i = 0; i < 8; i++) v[i] = sideB ? rG[ks][j][i / 4][i % 4] : rS[ks][j][i / 4][i % 4];
+                split_frag<T>(v, sf[at][j]);
+            }
+        };
+        if constexpr (kEarly)
+            if (ncols) {
+                split(0, 0);
+                split(1, 1);
+            }
+        if (ncols && sideB)
 #pragma unroll
             for (int ks = 0; ks < 2; ks++)
 #pragma unroll
                 for (int j = 0; j < NW; j++) {
-                    const f32x8 sv = __builtin_shufflevector(rS[ks][j][0], rS[ks][j][1], 0, 1, 2, 3, 4, 5, 6, 7);
-                    if (!sideB) {
-                        split_frag<T>(sv, sf[ks][j]);
-                    } else {
-                        const f32x8 gv =
-                            __builtin_shufflevector(rG[ks][j][0], rG[ks][j][1], 0, 1, 2, 3, 4, 5, 6, 7);
 #pragma unroll
-                        for (int i = 0; i < 8; i++) gdot = fmaf(sv[i], gv[i], gdot);
-                        split_frag<T>(gv, sf[ks][j]);
-                        if constexpr (kGs)
-                            *reinterpret_cast<Frag *>(Gs[buf] + (16 * (nt0 + j) + li) * LX + 32 * ks + 8 * g) =
-                                sf[ks][j][0];
-                    }
+                    for (int u = 0; u < 2; u++)
+#pragma unroll
+                        for (int i = 0; i < 4; i++) gdot = fmaf(rS[ks][j][u][i], rG[ks][j][u][i], gdot);
+                    if constexpr (kGs)
+                        *reinterpret_cast<Frag *>(Gs[buf] + (16 * (nt0 + j) + li) * LX + 32 * ks + 8 * g) =
+                            frag_acc<T>(rG[ks][j][0], rG[ks][j][1]);
                 }
         __syncthreads();
-        if (step + 1 < steps) fetch(step + 1);
+        if (step + 1 < steps) {
+            fetch(step + 1);
+            if (kEarly) fetch_states(step + 1);
+        }
         // dy.x for the wave's tiles
 #pragma unroll
         for (int k = 0; k < 2; k++) {
@@ -733,16 +751,20 @@ __global__ __launch_bounds__(2 * kThreads) TWO_WAVES void scan_grad_kernel(
         if (ncols) {
             const T *src = sideB ? Xs[buf] : Ys[buf];
 #pragma unroll
-            for (int r = 0; r < 4; r++)
+            for (int ks = 0; ks < 2; ks++) {
+                if constexpr (!kEarly) split(ks, 0);
 #pragma unroll
-                for (int ks = 0; ks < 2; ks++) {
+                for (int r = 0; r < 4; r++) {
                     const Frag a = frag_row<T>(src, LX, 16 * r, 32 * ks);
 #pragma unroll
                     for (int j = 0; j < NW; j++)
 #pragma unroll
-                        for (int m = 0; m < M::kTerms; m++) acc[r][j] = M::mma(sf[ks][j][m], a, acc[r][j]);
+                        for (int m = 0; m < M::kTerms; m++)
+                            acc[r][j] = M::mma(sf[kEarly ? ks : 0][j][m], a, acc[r][j]);
                 }
+            }
         }
+        if (!kEarly && step + 1 < steps) fetch_states(step + 1);
         // dx^T: 16 columns (rows here) and half of the tokens
         {
             Frag gn[NF], yc[2];
