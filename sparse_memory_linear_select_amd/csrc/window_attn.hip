@@ -19,7 +19,6 @@ constexpr int kTile = 64;     // keys (or queries) of a tile in LDS
 constexpr int kThreads = 256; // of the kernels whose waves hold queries
 constexpr int kKeys = 128;    // keys of a workgroup of the dK, dV kernel: 16 for each of eight waves
 constexpr int kSinkRows = 512;  // queries whose sink gradients one workgroup sums
-constexpr int kFewSinks = 16;   // sinks whose gradients the dQ kernel sums itself
 
 struct WinDims {
     int B, Hq, Hk, D;
@@ -68,18 +67,23 @@ __device__ __forceinline__ typename Mat<T>::Frag frag_global(const T *row, int k
 }
 
 // The keys that the queries i0 .. i1 (positions) can see, as one list: the
-// sinks in front of every window, then the keys from lo on.  Entry v is a sink
-// that is always seen where v < S; jr(v) = its position - i0 (for entries in
-// front of lo some number below that of lo: they precede every query).
+// sinks in front of every window (unless they are taken apart), then the keys
+// from lo on.  Entries v < always are sinks that every later query sees; jr(v)
+// = the position of entry v - i0 (for entries in front of lo some number below
+// that of lo: they precede every query).
 struct KeyList {
-    int64_t lo;     // first key of the window part
-    int ns, total;  // sinks in front of it; entries
-    int shift;      // jr(v) = v + shift
-    __device__ KeyList(int64_t i0, int64_t i1, int64_t W, int S)
+    int64_t lo;        // first key of the window part
+    int front;         // sinks in front of it
+    int ns, total;     // sinks in the list; entries
+    int always;
+    int shift;         // jr(v) = v + shift
+    __device__ KeyList(int64_t i0, int64_t i1, int64_t W, int S, bool apart)
     {
         lo = i0 - W + 1 > 0 ? i0 - W + 1 : 0;
-        ns = S < lo ? S : (int)lo;
+        front = S < lo ? S : (int)lo;
+        ns = apart ? 0 : front;
         total = ns + (int)(i1 - lo + 1);
+        always = S - (front - ns);
         shift = (int)(lo - i0) - ns;
     }
     __device__ int64_t key(int v) const { return v < ns ? v : lo + (v - ns); }
@@ -89,11 +93,11 @@ struct KeyList {
 // branches, and a wave that branches waits for every read in turn.)
 // What 16 neighbouring entries from v0 are to 16 neighbouring queries from ir0
 // (relative to i0): 0 none is seen, 1 some are, 2 all are.
-__device__ __forceinline__ int block_sight(int v0, int shift, int ir0, int W, int S)
+__device__ __forceinline__ int block_sight(int v0, int shift, int ir0, int W, int always)
 {
     const int j0 = v0 + shift, j1 = j0 + 15, ir1 = ir0 + 15;
-    if (j0 > ir1 || (v0 >= S && j1 <= ir0 - W)) return 0;
-    return j1 <= ir0 && (j0 > ir1 - W || v0 + 15 < S) ? 2 : 1;
+    if (j0 > ir1 || (v0 >= always && j1 <= ir0 - W)) return 0;
+    return j1 <= ir0 && (j0 > ir1 - W || v0 + 15 < always) ? 2 : 1;
 }
 
 // A 64-row tile in two steps, as TileRegs, from rows given by pointers.  Every
@@ -134,6 +138,40 @@ struct RowRegs {
     }
 };
 
+// Few sinks in front of the windows are taken apart from the list, as a block of
+// 16 keys of their own: at the head of the list they would cost a whole tile
+// (with 64 queries and a window of 128, 195 entries are four tiles and 191 three).
+constexpr int kFewSinks = 16;
+
+// Fills a 16-row tile from rows given by pointers (which exist).
+template <typename T, int COLS, int LD, bool VEC, int THREADS, typename F>
+__device__ __forceinline__ void load_few(T *tile, F row_of, int D)
+{
+    constexpr int V = 16 / sizeof(T);
+    constexpr int PER = COLS / V;
+    for (int e = threadIdx.x; e < kFewSinks * PER; e += THREADS) {
+        const int c = (e % PER) * V, r = e / PER;
+        const T *src = row_of(r);
+        Vec<T, V> v;
+        if constexpr (VEC) {
+            v = vload<T, V>(src + (c < D ? c : 0));
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; i++) v.e[i] = src[c + i < D ? c + i : 0];
+        }
+        vstore<T, V>(tile + r * LD + c, v);
+    }
+}
+
+// Column fragment of a 16-row tile for weights frag_acc(tile, zeros).
+template <typename T>
+__device__ __forceinline__ typename Mat<T>::Frag frag_col_few(const T *tile, int ld, int col0)
+{
+    const auto zero = __builtin_convertvector(f32x4{0.f, 0.f, 0.f, 0.f}, typename Mat<T>::Half);
+    return __builtin_shufflevector(col4(tile, ld, ((threadIdx.x & 63) >> 4) * 4, col0), zero, 0, 1, 2, 3, 4,
+                                   5, 6, 7);
+}
+
 // Workgroups are dealt to the 8 XCDs in turn; a run of neighbouring indexes on
 // one XCD shares its L2.
 __device__ __forceinline__ int64_t xcd_index(int64_t id, int64_t n)
@@ -169,6 +207,9 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && DT <= 8 ? 2 : 1) void w
     constexpr int kBufs = sizeof(T) == 2 ? 2 : 1;
     __shared__ __align__(32) T Ks[kBufs][kTile * LD];
     __shared__ __align__(32) T Vs[kBufs][kTile * LD];
+    // float32 tiles leave no room for the sinks' beside a second workgroup
+    constexpr bool kApart = sizeof(T) == 2;
+    __shared__ __align__(32) T Few[2][kApart ? kFewSinks * LD : 1];
 
     const int64_t blk = xcd_index(blockIdx.x, gridDim.x);
     const int qt = (int)(blk % d.nq);
@@ -200,25 +241,26 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && DT <= 8 ? 2 : 1) void w
     }
     if (t0 < len) {
         const int64_t last = (t0 + 4 * QR < len ? t0 + 4 * QR : len) - 1;
-        const KeyList kl(p0 + t0, p0 + last, d.W, S);
+        const KeyList kl(p0 + t0, p0 + last, d.W, S, kApart && S <= kFewSinks);
+        const int few = kl.front - kl.ns;
         const int nt = (kl.total + kTile - 1) / kTile;
         const T *kn = k + b * d.kb + hk * d.kh, *vn = v + b * d.vb + hk * d.vh;
+        const auto krow = [&](int64_t j) {
+            if (CACHE && j < p0) return ck + ((b * d.cap + cache_slot(j, S, W)) * d.Hk + hk) * d.D;
+            return kn + (j - p0) * d.kt;
+        };
+        const auto vrow = [&](int64_t j) {
+            if (CACHE && j < p0) return cv + ((b * d.cap + cache_slot(j, S, W)) * d.Hk + hk) * d.D;
+            return vn + (j - p0) * d.vt;
+        };
         RowRegs<T, DT * 16, LD, VEC, kThreads> rk, rv;
         const auto fetch = [&](int n) {
             const auto key = [&](int r) {
                 const int e = n * kTile + r;
                 return kl.key(e < kl.total ? e : kl.total - 1);
             };
-            rk.load([&](int r) {
-                const int64_t j = key(r);
-                if (CACHE && j < p0) return ck + ((b * d.cap + cache_slot(j, S, W)) * d.Hk + hk) * d.D;
-                return kn + (j - p0) * d.kt;
-            }, d.D);
-            rv.load([&](int r) {
-                const int64_t j = key(r);
-                if (CACHE && j < p0) return cv + ((b * d.cap + cache_slot(j, S, W)) * d.Hk + hk) * d.D;
-                return vn + (j - p0) * d.vt;
-            }, d.D);
+            rk.load([&](int r) { return krow(key(r)); }, d.D);
+            rv.load([&](int r) { return vrow(key(r)); }, d.D);
         };
         fetch(0);
         typename M::Frag qf[QN][DT / 2];
@@ -229,9 +271,43 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && DT <= 8 ? 2 : 1) void w
 #pragma unroll
             for (int ks = 0; ks < DT / 2; ks++) qf[u][ks] = frag_global<T, VEC>(row, 32 * ks + 8 * g, d.D);
         }
+        if (kApart && few > 0) {
+            load_few<T, DT * 16, LD, VEC, kThreads>(Few[0], [&](int r) { return krow(r < few ? r : few - 1); }, d.D);
+            load_few<T, DT * 16, LD, VEC, kThreads>(Few[1], [&](int r) { return vrow(r < few ? r : few - 1); }, d.D);
+        }
         rk.store(Ks[0]);
         rv.store(Vs[0]);
         __syncthreads();
+        if (kApart && few > 0) {
+            const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+            typename M::Frag pf[QN];
+#pragma unroll
+            for (int u = 0; u < QN; u++) {
+                f32x4 s = zero;
+#pragma unroll
+                for (int ks = 0; ks < DT / 2; ks++)
+                    s = M::mma(frag_row<T>(Few[0], LD, 0, 32 * ks), qf[u][ks], s);
+                float top = -INFINITY;
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    s[e] = 4 * g + e < few ? s[e] * d.c2 : -INFINITY;
+                    top = fmaxf(top, s[e]);
+                }
+                m[u] = pair_max(pair_max(top, 16), 32);
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    s[e] = exp2_fast(s[e] - m[u]);
+                    sum[u] += s[e];
+                }
+                pf[u] = frag_acc<T>(s, zero);
+            }
+#pragma unroll
+            for (int j = 0; j < DT; j++) {
+                const auto a = frag_col_few<T>(Few[1], LD, 16 * j);
+#pragma unroll
+                for (int u = 0; u < QN; u++) O[u][j] = M::mma(a, pf[u], O[u][j]);
+            }
+        }
         for (int n = 0; n < nt; n++) {
             const int buf = kBufs == 2 ? n & 1 : 0;
             fetch(n + 1 < nt ? n + 1 : n);
@@ -244,7 +320,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && DT <= 8 ? 2 : 1) void w
                 for (int kt = 0; kt < 4; kt++) {
                     sight[u][kt] = HP == 2 && u ? sight[0][kt]
                                                 : block_sight(v0 + 16 * kt, kl.shift,
-                                                              QR * w + (HP == 2 ? 0 : 16 * u), W, S);
+                                                              QR * w + (HP == 2 ? 0 : 16 * u), W, kl.always);
                     any = any || sight[u][kt];
                 }
             if (any) {
@@ -277,7 +353,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && DT <= 8 ? 2 : 1) void w
 #pragma unroll
                             for (int e = 0; e < 4; e++) {
                                 const int ve = v0 + 16 * kt + 4 * g + e, jr = ve + kl.shift;
-                                const bool see = (jr <= ir[u]) & ((ve < S) | (jr > ir[u] - W));
+                                const bool see = (jr <= ir[u]) & ((ve < kl.always) | (jr > ir[u] - W));
                                 s[u][kt][e] = see ? s[u][kt][e] * d.c2 : -INFINITY;
                             }
                         }
@@ -557,7 +633,7 @@ __global__ __launch_bounds__(kThreads) void window_cache_kernel(
 // Gradients of the sinks.  Few queries see a key, but all later ones a sink, so
 // their sums are split: part 0 holds the queries that the dK, dV kernel visits
 // for the keys' windows, the others each a part of the queries behind.  With at
-// most 16 sinks the dQ kernel, which has their weights at hand, sums the parts
+// most 16 sinks (and 128 columns) the dQ kernel, which has their weights at hand, sums the parts
 // (one a workgroup; `near` = its queries): those of the sinks that stand in
 // front of all its windows.  With more, the dK, dV kernel runs once more, for
 // the sinks alone.
@@ -591,7 +667,8 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && DT <= 8 ? 2 : 1) void w
     constexpr int kBufs = sizeof(T) == 2 ? 2 : 1;
     __shared__ __align__(32) T Ks[kBufs * kTile * LD];  // at the end (FEW) the rows of Q and dO
     __shared__ __align__(32) T Vs[kBufs * kTile * LD];
-    __shared__ __align__(32) T Ps[FEW ? 2 : 1][FEW ? kFewSinks * LS : 1];  // sinks' P, dS: [key][row]
+    // the sinks' K and V, then their P and dS: [key][row]
+    __shared__ __align__(32) T Few[2][FEW ? kFewSinks * (LS > LD ? LS : LD) : 1];
     static_assert(!FEW || kBufs * kTile >= kRows, "room for the rows");
 
     const int64_t blk = xcd_index(blockIdx.x, gridDim.x);
@@ -615,7 +692,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && DT <= 8 ? 2 : 1) void w
     }
     if (t0 < len) {
         const int64_t last = (t0 + 4 * QR < len ? t0 + 4 * QR : len) - 1;
-        const KeyList kl(t0, last, d.W, S);
+        const KeyList kl(t0, last, d.W, S, FEW);
         const int nt = (kl.total + kTile - 1) / kTile;
         const T *kn = k + b * d.kb + hk * d.kh, *vn = v + b * d.vb + hk * d.vh;
         RowRegs<T, DT * 16, LD, VEC, kThreads> rk, rv;
@@ -652,9 +729,52 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && DT <= 8 ? 2 : 1) void w
             if (live && g == 0) delta[ar] = dl[u];
             L[u] = lse[ar] * 1.4426950408889634f;
         }
+        const bool few = FEW && kl.front > 0;
+        if (few) {
+            const auto row = [&](int r) { return r < kl.front ? r : kl.front - 1; };
+            load_few<T, DT * 16, LD, VEC, kThreads>(Few[0], [&](int r) { return kn + row(r) * d.kt; }, d.D);
+            load_few<T, DT * 16, LD, VEC, kThreads>(Few[1], [&](int r) { return vn + row(r) * d.vt; }, d.D);
+        }
         rk.store(Ks);
         rv.store(Vs);
         __syncthreads();
+        if (few) {
+            const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+            f32x4 s[QN], dp[QN];
+            Frag sf[QN];
+#pragma unroll
+            for (int u = 0; u < QN; u++) {
+                s[u] = dp[u] = zero;
+#pragma unroll
+                for (int ks = 0; ks < DT / 2; ks++) {
+                    s[u] = M::mma(frag_row<T>(Few[0], LD, 0, 32 * ks), qf[u][ks], s[u]);
+                    dp[u] = M::mma(frag_row<T>(Few[1], LD, 0, 32 * ks), gf[u][ks], dp[u]);
+                }
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    const float p = exp2_fast(fmaf(s[u][e], d.c2, -L[u]));
+                    const float ds = p * (dp[u][e] - dl[u]) * d.scale;
+                    s[u][e] = 4 * g + e < kl.front ? p : 0.f;
+                    dp[u][e] = 4 * g + e < kl.front ? ds : 0.f;
+                }
+                sf[u] = frag_acc<T>(dp[u], zero);
+            }
+#pragma unroll
+            for (int j = 0; j < DT; j++) {
+                const auto a = frag_col_few<T>(Few[0], LD, 16 * j);
+#pragma unroll
+                for (int u = 0; u < QN; u++) O[u][j] = M::mma(a, sf[u], O[u][j]);
+            }
+            __syncthreads();
+#pragma unroll
+            for (int u = 0; u < QN; u++)
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    const int at = (4 * g + e) * LS + 16 * (w * QN + u) + li;
+                    Few[0][at] = (T)s[u][e];
+                    Few[1][at] = (T)dp[u][e];
+                }
+        }
         for (int n = 0; n < nt; n++) {
             const int buf = kBufs == 2 ? n & 1 : 0;
             const T *Kt = Ks + buf * kTile * LD, *Vt = Vs + buf * kTile * LD;
@@ -670,7 +790,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && DT <= 8 ? 2 : 1) void w
                     for (int e = 0; e < 2; e++) {
                         sight[u][e] = HP == 2 && u ? sight[0][e]
                                                    : block_sight(v0 + 32 * kp + 16 * e, kl.shift,
-                                                                 QR * w + (HP == 2 ? 0 : 16 * u), W, S);
+                                                                 QR * w + (HP == 2 ? 0 : 16 * u), W, kl.always);
                         any |= sight[u][e];
                     }
                 if (!any) continue;
@@ -699,23 +819,12 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && DT <= 8 ? 2 : 1) void w
                         for (int e = 0; e < 4; e++) {
                             const float p = exp2_fast(fmaf(s[u][kt][e], d.c2, -L[u]));
                             dp[u][kt][e] = p * (dp[u][kt][e] - dl[u]) * d.scale;
-                            s[u][kt][e] = p;
-                        }
-                        if (FEW && kp == 0 && kt == 0 && n == 0) {
-                            // weights of the sinks in front; the others of the block count as none here
-                            const int rho = 16 * (w * QN + u) + li;
-#pragma unroll
-                            for (int e = 0; e < 4; e++) {
-                                const bool front = 4 * g + e < kl.ns;
-                                Ps[0][(4 * g + e) * LS + rho] = (T)(front ? s[u][0][e] : 0.f);
-                                Ps[1][(4 * g + e) * LS + rho] = (T)(front ? dp[u][0][e] : 0.f);
-                            }
                         }
                         if (sight[u][kt] != 2)
 #pragma unroll
                             for (int e = 0; e < 4; e++) {
                                 const int ve = v0 + 32 * kp + 16 * kt + 4 * g + e, jr = ve + kl.shift;
-                                const bool see = (jr <= ir[u]) & ((ve < S) | (jr > ir[u] - W));
+                                const bool see = (jr <= ir[u]) & ((ve < kl.always) | (jr > ir[u] - W));
                                 dp[u][kt][e] = see ? dp[u][kt][e] : 0.f;
                             }
                     }
@@ -735,7 +844,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && DT <= 8 ? 2 : 1) void w
             __syncthreads();
         }
         if constexpr (FEW) {
-            if (kl.ns > 0) {   // dK, dV of the sinks in front over the workgroup's rows
+            if (few) {   // dK, dV of the sinks in front over the workgroup's rows
 #pragma unroll
                 for (int u = 0; u < QN; u++)
 #pragma unroll
@@ -753,11 +862,11 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && DT <= 8 ? 2 : 1) void w
                     f32x4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                     for (int ks = 0; ks < kRows / 32; ks++)
-                        acc = M::mma(frag_row<T>(Ps[isV ? 0 : 1], LS, 0, 32 * ks),
+                        acc = M::mma(frag_row<T>(Few[isV ? 0 : 1], LS, 0, 32 * ks),
                                      frag_col<T>(isV ? Vs : Ks, LD, 32 * ks, c0), acc);
 #pragma unroll
                     for (int e = 0; e < 4; e++)
-                        if (4 * g + e < kl.ns && c0 + li < d.D)
+                        if (4 * g + e < kl.front && c0 + li < d.D)
                             pp[(4 * g + e) * 2 * d.D + (isV ? d.D : 0) + c0 + li] = acc[e];
                 }
             }
