@@ -20,7 +20,7 @@ namespace {
 constexpr int Q = 64;         // tokens of a chunk
 constexpr int kSlice = 64;    // columns of x that a workgroup holds: 16 a wave
 constexpr int kThreads = 256;
-constexpr int kMaxSegs = 512;   // segments of the time axis
+constexpr int kMaxSegs = 256;   // segments of the time axis
 constexpr int LX = kSlice + 8;  // LDS row stride of 64-wide tiles
 
 // LDS leaves these kernels two waves a SIMD, so the compiler may use half of the
@@ -1088,7 +1088,7 @@ struct Plan {
     size_t delta, cs, own[2], start[2], S, G, parts, hsum, total;
 };
 
-constexpr int64_t kUnits = kMaxSegs;  // workgroups that fill the 256 compute units twice
+constexpr int64_t kFill = 256;   // compute units
 
 Plan plan_of(const sdm_scan_desc &s, bool backward)
 {
@@ -1102,11 +1102,14 @@ Plan plan_of(const sdm_scan_desc &s, bool backward)
     d.T = s.T;
     d.nc = (int)((s.T + Q - 1) / Q);
     d.nps = (s.P + kSlice - 1) / kSlice;
-    // Few chains: the time axis is split into segments of at least 8 chunks,
-    // which first run for their states alone.
-    const int64_t units = (int64_t)s.B * s.H * d.nps;
-    int64_t seg = units >= kUnits / 2 ? 1 : (kUnits + units - 1) / units;
-    if (seg > d.nc / 8) seg = d.nc / 8;
+    // Few chains: the time axis is split into segments, enough for a workgroup on
+    // every compute unit, which first run for their states alone.  A segment is at
+    // least two chunks, or eight in the backward, whose two walks share a launch
+    // and take no longer steps (5 x 777 tokens, 6 heads, float32: forward 67 us in
+    // one segment and 38 in six; backward 71 and 85).
+    const int64_t units = (int64_t)s.B * s.H * d.nps, least = backward ? 8 : 2;
+    int64_t seg = (kFill + units - 1) / units;
+    if (seg > d.nc / least) seg = d.nc / least;
     if (seg < 1) seg = 1;
     d.cps = (int)((d.nc + seg - 1) / seg);
     d.nseg = (d.nc + d.cps - 1) / d.cps;
@@ -1116,10 +1119,18 @@ Plan plan_of(const sdm_scan_desc &s, bool backward)
     d.bt = s.B_token;
     d.cb = s.C_batch;
     d.ct = s.C_token;
-    const int64_t grads = (int64_t)s.B * d.nc * s.G;
-    int64_t hb = grads >= kUnits ? 1 : (kUnits + grads - 1) / grads;
-    if (hb > s.H / s.G) hb = s.H / s.G;
-    p.hblocks = (int)hb;
+    // Blocks of a group's heads: the number with the fewest rounds of workgroups
+    // (one a compute unit) times heads of a workgroup, counting its tiles of B and
+    // C and its last stores as one head more; the fewest blocks of those.
+    const int64_t grads = (int64_t)s.B * d.nc * s.G, per = s.H / s.G;
+    int64_t best = 0;
+    for (int64_t hb = 1; hb <= per && hb <= kFill; hb++) {
+        const int64_t cost = (grads * hb + kFill - 1) / kFill * ((per + hb - 1) / hb + 1);
+        if (hb == 1 || cost < best) {
+            best = cost;
+            p.hblocks = (int)hb;
+        }
+    }
 
     size_t at = 0;
     auto take = [&](size_t bytes) {
