@@ -52,6 +52,7 @@ SHAPES = [
     (5, 17, 12, 2, "bf16", True, False, [17, 3, 0, 16, 1], True),
     (1, 300, 36, 7, "bf16", True, True, None, False),
     (2, 40, 10, 6, "f32", True, True, None, True),
+    (1024, 5, 8, 4, "bf16", True, True, None, False),       # many short sequences: long runs
 ]
 IDS = [f"B{s[0]}-T{s[1]}-C{s[2]}-K{s[3]}-{s[4]}" for s in SHAPES]
 

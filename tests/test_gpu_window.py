@@ -55,6 +55,10 @@ SHAPES = [
     (1, 1200, 2, 1, 64, 128, 4, "bf16", None),         # parts of the sinks' gradients
     (1, 150, 1, 1, 128, 1, 150, "f32", None),          # all tokens are sinks
     (1, 90, 6, 2, 8, 30, 100, "bf16", None),           # more sinks than tokens
+    (1, 400, 8, 2, 64, 40, 6, "bf16", None),           # few sinks, two pairs of heads a key head
+    (2, 300, 4, 1, 64, 30, 16, "f32", [300, 120]),     # as many as are summed apart
+    (1, 300, 2, 2, 20, 50, 3, "bf16", None),           # scalar accesses
+    (1, 260, 3, 1, 128, 60, 17, "bf16", [260]),        # one sink more
 ]
 IDS = ["-".join(map(str, s[:8])) for s in SHAPES]
 
@@ -180,6 +184,54 @@ def test_stream_equals_whole_sequence(dt, Hq, Hk, D, W, S):
         for t in list(range(min(S, n))) + list(range(max(S, n - W), n)):
             slot = t if t < S else S + (t - S) % W
             assert torch.equal(cache[0][b, slot], k[b, t]) and torch.equal(cache[1][b, slot], v[b, t])
+
+
+# B, Hq, Hk, D, window, sinks, dtype, positions
+STEPS = [
+    (3, 2, 1, 64, 2000, 3, "bf16", [0, 700, 5000]),        # a cache shared among workgroups
+    (2, 12, 1, 128, 300, 0, "bf16", [299, 300]),           # two groups of heads
+    (2, 3, 3, 256, 70, 5, "f32", [74, 1000]),
+    (1, 8, 2, 33, 1100, 80, "f32", [40000]),               # scalar accesses
+    (2, 4, 1, 8, 1, 0, "bf16", [0, 9]),                    # the token sees itself alone
+    (4, 5, 1, 96, 130, 4, "bf16", [0, 3, 133, 134]),
+]
+
+
+@pytest.mark.parametrize("case", STEPS, ids=["-".join(map(str, c[:7])) for c in STEPS])
+def test_step(case):
+    """One token against a rolling cache of any age; rows that no token has filled hold NaN."""
+    B, Hq, Hk, D, W, S, dt, at = case
+    q, k, v, _ = inputs(W + D, B, 1, Hq, Hk, D, dt, None)
+    g = gen(9)
+    R = S + W
+    ck, cv = (normal(g, B, R, Hk, D, dtype=q.dtype) for _ in range(2))
+    for b, p in enumerate(at):
+        ck[b, p:], cv[b, p:] = math.nan, math.nan
+    ek, ev = ck.clone(), cv.clone()
+    att = sdm.WindowAttention(Hq, Hk, D, W, S)
+    pos = torch.tensor(at, dtype=torch.int64).cuda()
+    on = torch.tensor([1] * (B - 1) + [0 if B > 3 else 1], dtype=torch.int32).cuda()
+    o, lse = att.forward(q, k, v, cache=(ck, cv), pos=pos, cont=True, lengths=on)
+    r = Hq // Hk
+    for b, p in enumerate(at):
+        if on[b] == 0:
+            assert (o[b] == 0).all() and (lse[b] == 0).all()
+            continue
+        slot = p if p < S else S + (p - S) % W
+        ek[b, slot], ev[b, slot] = k[b, 0], v[b, 0]
+        n = min(p + 1, R)
+        kk = cpu(ek[b, :n]).repeat_interleave(r, 1)
+        vv = cpu(ev[b, :n]).repeat_interleave(r, 1)
+        s = torch.einsum("hd,nhd->hn", cpu(q[b, 0]), kk) * att.scale
+        w = torch.softmax(s, -1)
+        ref = torch.einsum("hn,nhd->hd", w, vv)
+        sm = (torch.einsum("hd,nhd->hn", cpu(q[b, 0]).abs(), kk.abs()) * att.scale).amax(-1)
+        rel = (2 * (D + 4) * sm + n + 32) * 2.0 ** -24   # float32 weights throughout
+        check(o[b, 0], ref, torch.einsum("hn,nhd->hd", w, vv.abs()) * rel[:, None], "o", 0, 1.0)
+        check(lse[b, 0], torch.logsumexp(s, -1), rel + s.abs().amax(-1) * 2.0 ** -22, "lse", 0, 1.0)
+    # only the token's row changed
+    assert torch.equal(ck.nan_to_num(7.0), ek.nan_to_num(7.0))
+    assert torch.equal(cv.nan_to_num(7.0), ev.nan_to_num(7.0))
 
 
 def test_far_position():
