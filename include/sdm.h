@@ -478,7 +478,7 @@ sdm_status sdm_scan_backward(const sdm_scan_desc *d, const void *x, const void *
  * Rolling cache.  A stream needs its sinks and its last `window` tokens:
  * cache_k, cache_v hold sinks + window rows per sequence, the token at
  * position p in row p (p < sinks) or sinks + (p - sinks) % window.
- * Limits: 1 <= D <= 256, Hk divides Hq, 1 <= window < 2^31, 0 <= sinks <= 1024;
+ * Limits: 1 <= D <= 256, Hk divides Hq, 1 <= window < 2^30, 0 <= sinks <= 1024;
  * B * Hq * ceil(T / 64) and B * (min(sinks, T) + min(window, T)) < 2^31.
  */
 typedef struct {

@@ -160,8 +160,8 @@ sdm_status check_window(const sdm_window_desc *d)
     if (d->D > 256) return set_error(SDM_ERR_UNSUPPORTED, "D <= 256 is supported (got %d)", d->D);
     if (d->sinks > 1024)
         return set_error(SDM_ERR_UNSUPPORTED, "sinks <= 1024 is supported (got %d)", d->sinks);
-    if (d->window >= (int64_t)1 << 31)
-        return set_error(SDM_ERR_UNSUPPORTED, "window must be < 2^31");
+    if (d->window >= (int64_t)1 << 30)
+        return set_error(SDM_ERR_UNSUPPORTED, "window must be < 2^30");
     const double rows = (double)(d->sinks < d->T ? d->sinks : d->T) +
                         (double)(d->window < d->T ? d->window : d->T);
     if ((double)d->B * d->Hq * (double)((d->T + 63) / 64) >= 2147483648.0 ||

@@ -753,15 +753,16 @@ __global__ __launch_bounds__(2 * kThreads) TWO_WAVES void scan_grad_kernel(
 #pragma unroll
             for (int ks = 0; ks < 2; ks++) {
                 if constexpr (!kEarly) split(ks, 0);
+                Frag a[4];
 #pragma unroll
-                for (int r = 0; r < 4; r++) {
-                    const Frag a = frag_row<T>(src, LX, 16 * r, 32 * ks);
+                for (int r = 0; r < 4; r++) a[r] = frag_row<T>(src, LX, 16 * r, 32 * ks);
+#pragma unroll
+                for (int m = 0; m < M::kTerms; m++)
 #pragma unroll
                     for (int j = 0; j < NW; j++)
 #pragma unroll
-                        for (int m = 0; m < M::kTerms; m++)
-                            acc[r][j] = M::mma(sf[kEarly ? ks : 0][j][m], a, acc[r][j]);
-                }
+                        for (int r = 0; r < 4; r++)
+                            acc[r][j] = M::mma(sf[kEarly ? ks : 0][j][m], a[r], acc[r][j]);
             }
         }
         if (!kEarly && step + 1 < steps) fetch_states(step + 1);

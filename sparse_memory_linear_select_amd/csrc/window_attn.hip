@@ -683,10 +683,12 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && DT <= 8 ? 2 : 1) void w
     const int l = threadIdx.x & 63, g = l >> 4, li = l & 15;
     const int W = (int)d.W, S = d.S;
     int ir[QN];
+    bool alone[QN];   // a query that sees one key: its weight is 1, whatever the score
     f32x4 O[QN][DT];
 #pragma unroll
     for (int u = 0; u < QN; u++) {
         ir[u] = QR * w + (HP == 2 ? 0 : 16 * u) + li;
+        alone[u] = t0 + ir[u] == 0;
 #pragma unroll
         for (int j = 0; j < DT; j++) O[u][j] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
@@ -825,7 +827,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && DT <= 8 ? 2 : 1) void w
                             for (int e = 0; e < 4; e++) {
                                 const int ve = v0 + 32 * kp + 16 * kt + 4 * g + e, jr = ve + kl.shift;
                                 const bool see = (jr <= ir[u]) & ((ve < kl.always) | (jr > ir[u] - W));
-                                dp[u][kt][e] = see ? dp[u][kt][e] : 0.f;
+                                dp[u][kt][e] = see & !alone[u] ? dp[u][kt][e] : 0.f;
                             }
                     }
                     // dS is rounded to the inputs' type for the product with K
@@ -1008,7 +1010,8 @@ __global__ __launch_bounds__(4 * kKeys) void window_dkv_kernel(
                                              (SINKS ? kr < sinks
                                                     : (qr - kr < W) | ((kr < sinks) & (from - kr < W)));
                             p[e2][e] = see ? p[e2][e] : 0.f;
-                            ds[e2][e] = see ? ds[e2][e] : 0.f;
+                            // the first query sees one key, whose weight is 1 whatever the score
+                            ds[e2][e] = see & (SINKS | (j0 + qr != 0)) ? ds[e2][e] : 0.f;
                         }
                 }
                 // P and dS are rounded to the inputs' type for the products with dO and Q
@@ -1178,6 +1181,7 @@ template <typename T, int DT, bool VEC>
 hipError_t backward(const WindowArgs &a, hipStream_t stream)
 {
     WinDims d = dims_of(a.d);
+    if (d.W == 1 && d.S == 0) d.scale = 0.f;   // every query sees one key: scores have no gradient
     const BackPlan p = back_plan(a.d);
     constexpr int QN = query_blocks(DT * 16, sizeof(T));
     const int hp = head_pair(a.d), queries = queries_of(a.d);

@@ -123,6 +123,22 @@ def test_backward(shape):
             assert all((out[x][b, n:] == 0).all() for x in out)
 
 
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_one_visible_key_has_no_score_gradient(dt):
+    """A softmax over one key is 1: dq and dk are exactly zero, and dv is do."""
+    for T, W, S in ((1, 5, 3), (150, 1, 0)):
+        q, k, v, _ = inputs(T, 2, T, 4, 2, 64, dt, None)
+        do = normal(gen(1), 2, T, 4, 64, dtype=q.dtype)
+        att = sdm.WindowAttention(4, 2, 64, W, S)
+        o, lse = att.forward(q, k, v)
+        out = att.backward(q, k, v, o, lse, do)
+        assert (out["dq"] == 0).all() and (out["dk"] == 0).all()
+        both = do.float().unflatten(2, (2, 2)).sum(3)
+        # the weight exp(s - lse) is off by the rounding of lse: |lse| 2^-22
+        lim = (lse.abs().amax() + 1) * 2.0 ** -21 + torch.finfo(q.dtype).eps
+        assert float(((out["dv"].float() - both).abs() / (1 + both.abs())).max()) <= float(lim)
+
+
 def test_gradient_against_differences():
     q, k, v, _ = inputs(5, 1, 70, 2, 1, 8, "f32", None)
     do = normal(gen(6), 1, 70, 2, 8)

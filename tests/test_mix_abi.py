@@ -145,7 +145,7 @@ def window_desc(**kw):
     (dict(B=0), 1), (dict(T=0), 1), (dict(Hq=0), 1), (dict(Hk=0), 1), (dict(Hk=3), 1), (dict(D=0), 1),
     (dict(window=0), 1), (dict(sinks=-1), 1), (dict(scale=float("nan")), 1), (dict(dtype=2), 1),
     (dict(q_token=-1), 1), (dict(k_head=-1), 1), (dict(v_batch=-1), 1), (dict(D=257), 2),
-    (dict(sinks=1025), 2), (dict(window=1 << 31), 2), (dict(T=1 << 31), 2),
+    (dict(sinks=1025), 2), (dict(window=1 << 30), 2), (dict(T=1 << 31), 2),
     (dict(B=1 << 15, T=1 << 20), 2),
 ])
 def test_window_descriptor_refusals(kw, status):
