@@ -105,6 +105,11 @@ def _view(t, name, like, shape, inner):
     return t
 
 
+def _strides(t, n):
+    """The first n strides, 0 for dimensions of one element (where they say nothing)."""
+    return [s if m > 1 else 0 for s, m in zip(t.stride()[:n], t.shape)]
+
+
 def _lengths(t, B, like):
     return None if t is None else _dense(t, "lengths", (B,), torch.int32, like).data_ptr()
 
@@ -163,8 +168,7 @@ class CausalConv:
         B, T = x.shape[:2]
         _view(x, "x", x, (B, T, self.C), 1)
         _same_device(self.weight, x, "weight")
-        d = _ConvDesc(B, T, self.C, self.K, int(self.silu), _dtype(x, "x"), x.stride(0),
-                      x.stride(1))
+        d = _ConvDesc(B, T, self.C, self.K, int(self.silu), _dtype(x, "x"), *_strides(x, 2))
         return _keep(key, _Plan(d, (B, self.K - 1, self.C)))
 
     def forward(self, x, state=None, cont: bool = False, lengths=None, y=None):
@@ -254,8 +258,8 @@ class SelectiveScan:
         _view(Cm, "Cm", x, (B, T, G, N), 2)
         _out_tensor(dt, "dt", (B, T, H), x.dtype, x)
         _same_device(self.A, x, "A")
-        d = _ScanDesc(B, T, H, P, N, G, int(self.softplus), _dtype(x, "x"), x.stride(0),
-                      x.stride(1), Bm.stride(0), Bm.stride(1), Cm.stride(0), Cm.stride(1))
+        d = _ScanDesc(B, T, H, P, N, G, int(self.softplus), _dtype(x, "x"), *_strides(x, 2),
+                      *_strides(Bm, 2), *_strides(Cm, 2))
         return _keep(key, _Plan(d, (B, H, P, N)))
 
     def workspace_size(self, x, dt, Bm, Cm) -> int:
@@ -359,7 +363,7 @@ class WindowAttention:
         _view(k, "k", q, (B, T, self.Hk, self.D), 1)
         _view(v, "v", q, (B, T, self.Hk, self.D), 1)
         d = _WindowDesc(B, T, self.Hq, self.Hk, self.D, self.window, self.sinks, self.scale,
-                        _dtype(q, "q"), *q.stride()[:3], *k.stride()[:3], *v.stride()[:3])
+                        _dtype(q, "q"), *_strides(q, 3), *_strides(k, 3), *_strides(v, 3))
         return _keep(key, _Plan(d, (B, self.sinks + self.window, self.Hk, self.D)))
 
     def workspace_size(self, q, k, v, cont: bool = False) -> int:

@@ -206,6 +206,25 @@ def test_views(off):
     assert all(torch.equal(a[k], c[k]) for k in a)
 
 
+def test_strides_of_single_dimensions_say_nothing():
+    """One token of one sequence, with strides that no row uses."""
+    d = inputs(71, 1, 1, 2, 16, 8, 1, "bf16", "sbD", None, True)
+    odd = {k: torch.as_strided(d[k], d[k].shape, (1 << 40, 1 << 30, *d[k].stride()[2:]))
+           for k in ("x", "Bm", "Cm")}
+    y, s = d["scan"].forward(d["x"], d["dt"], d["Bm"], d["Cm"], state=d["S0"].clone(), cont=True)
+    y2, s2 = d["scan"].forward(odd["x"], d["dt"], odd["Bm"], odd["Cm"], state=d["S0"].clone(), cont=True)
+    assert torch.equal(y, y2) and torch.equal(s, s2)
+
+
+def test_token_stride_limit():
+    """Rows of a tile lie within 31 bits of each other, or the call is refused."""
+    d = inputs(72, 1, 2, 2, 16, 8, 1, "bf16", "s", None, False)
+    far = torch.empty((1 << 22) + 64, dtype=torch.bfloat16, device="cuda")
+    x = torch.as_strided(far, (1, 2, 2, 16), (1 << 22, 1 << 22, 16, 1))
+    with pytest.raises(sdm.SDMError, match="stride"):
+        d["scan"].forward(x, d["dt"], d["Bm"], d["Cm"])
+
+
 def test_rows_behind_the_length_are_not_read():
     lens = [150, 40, 0]
     d = inputs(41, 3, 150, 2, 20, 16, 1, "bf16", "sbD", lens, True)
