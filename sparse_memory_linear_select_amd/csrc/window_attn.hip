@@ -17,7 +17,7 @@ namespace {
 
 constexpr int kTile = 64;     // keys (or queries) of a tile in LDS
 constexpr int kThreads = 256; // of the kernels whose waves hold queries
-constexpr int kKeys = 128;    // keys of a workgroup of the dK, dV kernel: 16 for each of eight waves
+constexpr int kKeys = 64;     // keys of a workgroup of the dK, dV kernel: 16 for each of four waves
 constexpr int kSinkRows = 512;  // queries whose sink gradients one workgroup sums
 
 struct WinDims {
@@ -204,7 +204,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && DT <= 8 ? 2 : 1) void w
     using Half = typename M::Half;
     constexpr int LD = DT * 16 + 8;
     constexpr int QR = HP == 2 ? 16 : 16 * QN;   // queries of a wave
-    constexpr int kBufs = sizeof(T) == 2 ? 2 : 1;
+    constexpr int kBufs = sizeof(T) == 2 || DT <= 8 ? 2 : 1;
     __shared__ __align__(32) T Ks[kBufs][kTile * LD];
     __shared__ __align__(32) T Vs[kBufs][kTile * LD];
     // float32 tiles leave no room for the sinks' beside a second workgroup
@@ -664,7 +664,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && DT <= 8 ? 2 : 1) void w
     constexpr int QR = HP == 2 ? 16 : 16 * QN;    // queries of a wave
     constexpr int kRows = 64 * QN;                // rows of the workgroup
     constexpr int LS = kRows + 8;
-    constexpr int kBufs = sizeof(T) == 2 ? 2 : 1;
+    constexpr int kBufs = sizeof(T) == 2 || DT <= 8 ? 2 : 1;
     __shared__ __align__(32) T Ks[kBufs * kTile * LD];  // at the end (FEW) the rows of Q and dO
     __shared__ __align__(32) T Vs[kBufs * kTile * LD];
     // the sinks' K and V, then their P and dS: [key][row]
@@ -885,11 +885,14 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && DT <= 8 ? 2 : 1) void w
     }
 }
 
-// dK and dV of 128 keys, 16 a wave, over the query heads of their key head: a
-// lane holds one key (column) and four neighbouring queries (rows).  SINKS:
+// dK and dV of 64 keys, 16 a wave, over the query heads of their key head: a
+// lane holds one key (column) and four neighbouring queries (rows).  Two
+// workgroups share a compute unit; 128 keys and eight waves in one load fewer
+// tiles but start and end together (backward of 8 x 4096 tokens, 16 and 8 heads
+// of 128, window 128: 540 us instead of 507).  SINKS:
 // the sinks alone, for the queries behind part 0, 512 a workgroup, into parts 1 ..
 template <typename T, int DT, bool VEC, bool SINKS>
-__global__ __launch_bounds__(4 * kKeys) void window_dkv_kernel(
+__global__ __launch_bounds__(kThreads, sizeof(T) * DT <= 16 ? 2 : 1) void window_dkv_kernel(
     WinDims d, SinkParts sp, int ntiles, const T *__restrict__ q, const T *__restrict__ k,
     const T *__restrict__ v, const T *__restrict__ dout, const float *__restrict__ lse,
     const float *__restrict__ delta, const int32_t *__restrict__ lengths, T *__restrict__ dk,
@@ -897,7 +900,7 @@ __global__ __launch_bounds__(4 * kKeys) void window_dkv_kernel(
 {
     using M = Mat<T>;
     constexpr int LD = DT * 16 + 8;
-    constexpr int kBufs = 4 * kTile * LD * (int)sizeof(T) <= 156 * 1024 ? 2 : 1;
+    constexpr int kBufs = sizeof(T) == 2 || DT <= 8 ? 2 : 1;
     __shared__ __align__(32) T Qs[kBufs][kTile * LD];
     __shared__ __align__(32) T Gs[kBufs][kTile * LD];
     __shared__ __align__(16) float Ls[kBufs][kTile], Dl[kBufs][kTile];
@@ -939,7 +942,7 @@ __global__ __launch_bounds__(4 * kKeys) void window_dkv_kernel(
         typename M::Frag kf[DT / 2], vf[DT / 2];
         const int64_t jr = j < len ? j : len - 1;  // a row that exists; no query sees its copy
         const int nq = (int)((end - first + kTile - 1) / kTile);
-        RowRegs<T, DT * 16, LD, VEC, 4 * kKeys> rq, rg;
+        RowRegs<T, DT * 16, LD, VEC, kThreads> rq, rg;
         float rl, rd;
         const auto fetch = [&](int n) {
             const int h = hk * per + n / nq;
@@ -1201,11 +1204,11 @@ hipError_t backward(const WindowArgs &a, hipStream_t stream)
         hp == 2 ? run(window_dq_kernel<T, DT, QN, QN, VEC, false>)
                 : run(window_dq_kernel<T, DT, QN, 1, VEC, false>);
     const int ntiles = (int)((d.T + kKeys - 1) / kKeys);
-    window_dkv_kernel<T, DT, VEC, false><<<(unsigned)((int64_t)d.B * d.Hk * ntiles), 4 * kKeys, 0, stream>>>(
+    window_dkv_kernel<T, DT, VEC, false><<<(unsigned)((int64_t)d.B * d.Hk * ntiles), kThreads, 0, stream>>>(
         d, sp, ntiles, q, k, v, dout, a.lse_in, delta, a.lengths, (T *)a.dk, (T *)a.dv);
     if (p.ktiles)
         window_dkv_kernel<T, DT, VEC, true>
-            <<<(unsigned)((int64_t)d.B * d.Hk * p.ktiles * (p.nparts - 1)), 4 * kKeys, 0, stream>>>(
+            <<<(unsigned)((int64_t)d.B * d.Hk * p.ktiles * (p.nparts - 1)), kThreads, 0, stream>>>(
                 d, sp, p.ktiles, q, k, v, dout, a.lse_in, delta, a.lengths, (T *)a.dk, (T *)a.dv);
     if (p.nparts)
         window_sinks_kernel<T><<<(unsigned)((int64_t)d.B * d.Hk * d.S), dim3(128, 8), 0, stream>>>(
