@@ -287,6 +287,31 @@ __device__ __forceinline__ void store4(T *row, int c, int D, f32x4 v)
     }
 }
 
+// A whole row of D: v[j] holds columns 16 j + 4 g .. + 3.  bfloat16 lanes g and
+// g ^ 1 first trade halves of two neighbouring blocks, so that a lane stores 16
+// bytes and a row gets 64 in one piece.
+template <typename T, int DT, bool VEC>
+__device__ __forceinline__ void store_row(T *row, int D, const f32x4 *v)
+{
+    const int g = (threadIdx.x & 63) >> 4;
+    if constexpr (VEC && sizeof(T) == 2) {
+        typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+        typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+        const int c0 = 16 * (g & 1) + 4 * (g & 2);
+#pragma unroll
+        for (int j = 0; j < DT; j += 2) {
+            const u32x2 a = __builtin_bit_cast(u32x2, __builtin_convertvector(v[j], typename Mat<T>::Half));
+            const u32x2 b = __builtin_bit_cast(u32x2, __builtin_convertvector(v[j + 1], typename Mat<T>::Half));
+            const auto x = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
+            const auto y = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
+            if (16 * j + c0 < D) *reinterpret_cast<u32x4 *>(row + 16 * j + c0) = u32x4{x[0], y[0], x[1], y[1]};
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < DT; j++) store4<T, VEC>(row, 16 * j + 4 * g, D, v[j]);
+    }
+}
+
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
 }  // namespace

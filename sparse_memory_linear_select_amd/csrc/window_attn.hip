@@ -412,11 +412,8 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && DT <= 8 ? 2 : 1) void w
         const float inv = live ? 1.f / all : 0.f;
         T *op = o + at[u] * d.D;
 #pragma unroll
-        for (int j = 0; j < DT; j++) {
-            const int c = 16 * j + 4 * g;
-            const f32x4 r = live ? O[u][j] * inv : f32x4{0.f, 0.f, 0.f, 0.f};
-            store4<T, VEC>(op, c, d.D, r);
-        }
+        for (int j = 0; j < DT; j++) O[u][j] = live ? O[u][j] * inv : f32x4{0.f, 0.f, 0.f, 0.f};
+        store_row<T, DT, VEC>(op, d.D, O[u]);
         if (g == 0) lse[at[u]] = live ? (m[u] + log2f(all)) * 0.6931471805599453f : 0.f;
     }
 }
@@ -880,8 +877,8 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && DT <= 8 ? 2 : 1) void w
         if (t >= d.T) continue;
         T *row = dq + ((b * d.T + t) * d.Hq + h0 + (HP == 2 ? u : 0)) * d.D;
 #pragma unroll
-        for (int j = 0; j < DT; j++)
-            store4<T, VEC>(row, 16 * j + 4 * g, d.D, t < len ? O[u][j] : f32x4{0.f, 0.f, 0.f, 0.f});
+        for (int j = 0; j < DT; j++) O[u][j] = t < len ? O[u][j] : f32x4{0.f, 0.f, 0.f, 0.f};
+        store_row<T, DT, VEC>(row, d.D, O[u]);
     }
 }
 
@@ -1034,15 +1031,12 @@ __global__ __launch_bounds__(kThreads, sizeof(T) * DT <= 16 ? 2 : 1) void window
     if (j >= d.T || (SINKS && !sink)) return;
     const int64_t at = ((b * d.T + j) * d.Hk + hk) * d.D;
     float *pp = sink ? sink_part(sp, d, part, b, hk) + j * 2 * d.D : nullptr;
-#pragma unroll
-    for (int c = 0; c < DT; c++) {
-        if (sink) {
-            store4<float, false>(pp, 16 * c + 4 * g, d.D, dK[c]);
-            store4<float, false>(pp + d.D, 16 * c + 4 * g, d.D, dV[c]);
-        } else {
-            store4<T, VEC>(dk + at, 16 * c + 4 * g, d.D, dK[c]);
-            store4<T, VEC>(dv + at, 16 * c + 4 * g, d.D, dV[c]);
-        }
+    if (sink) {
+        store_row<float, DT, false>(pp, d.D, dK);
+        store_row<float, DT, false>(pp + d.D, d.D, dV);
+    } else {
+        store_row<T, DT, VEC>(dk + at, d.D, dK);
+        store_row<T, DT, VEC>(dv + at, d.D, dV);
     }
 }
 
