@@ -367,16 +367,22 @@ __global__ __launch_bounds__(2 * kThreads) TWO_WAVES void scan_walk_kernel(
         state_store<NT>(S, state + bh * (int64_t)d.P * d.N, true, 0, pl, d.P, d.N);
 }
 
+// A tile of `each` lies as the lanes hold it: element (n, p) = (16 j + 4 g + i,
+// 16 w + li) at each_at(j, w, i) + 16 g + li, so that a store covers 256 bytes in
+// one piece, and so do the gradient kernel's reads (whole backward of 8 x 4096
+// tokens, 16 heads of 128 x 64: 506 us; with rows of p 523).
+__device__ __forceinline__ constexpr int each_at(int j, int w, int i) { return (j * 4 + w) * 256 + 64 * i; }
+
 // States alone.  Forward: U = x, V = B, weights 2^{c_63 - c_s} D_s; `each` gets
 // the state before every chunk.  Reverse: U = dy, V = C, weights 2^{c_t},
 // chunks from last to first: the gradient G of the state,
 //   G <- 2^{c_63} G + sum_t 2^{c_t} C_t dy_t^T,
-// and `each` gets G behind every chunk, in tiles of [16 NT][64] per slice whose
-// rows and columns beyond N and P are zero.  `end` gets the last one: per segment
-// in the workspace's layout, or (end_api) the caller's gradient.  Waves w and
-// w + 4 hold the same 16 columns, each one half of the rows n.  The backward
-// runs both directions in one launch: a walk is bound by the time of its steps,
-// and two walks share a compute unit.
+// and `each` gets G behind every chunk; a tile per slice, whose rows and columns
+// beyond N and P are zero.  `end` gets the last one: per segment in the
+// workspace's layout, or (end_api) the caller's gradient.  Waves w and w + 4 hold
+// the same 16 columns, each one half of the rows n.  The backward runs both
+// directions in one launch: a walk is bound by the time of its steps, and two
+// walks share a compute unit.
 template <typename T>
 struct StateJob {
     const T *U, *V;
@@ -455,11 +461,11 @@ __global__ __launch_bounds__(2 * kThreads) void scan_state_kernel(
         fetch(far, k + 2 < c1 ? k + 2 : c1 - 1);
         if constexpr (EACH) {
             float *q = job.each + ((bh * d.nc + chunk_of(k)) * d.nps + ps) * (NT * 16 * kSlice) +
-                       (16 * j0 + 4 * ((threadIdx.x & 63) >> 4)) * kSlice + 16 * w + (threadIdx.x & 15);
+                       each_at(j0, w, 0) + (threadIdx.x & 63);
 #pragma unroll
             for (int j = 0; j < NJ; j++)
 #pragma unroll
-                for (int i = 0; i < 4; i++) q[(16 * j + i) * kSlice] = S[j][i];
+                for (int i = 0; i < 4; i++) q[each_at(j, 0, i)] = S[j][i];
         }
         const Weighted<T> u(Us[n], wt[n], 16 * w);
         state_add<T, NJ, LN>(S, Vs[n], u, scale[n], j0);
@@ -610,14 +616,15 @@ __global__ __launch_bounds__(2 * kThreads) TWO_WAVES void scan_grad_kernel(
     const auto fetch_states = [&](int step) {
         if (!ncols) return;
         const int h = h0 + step / d.nps, ps = step % d.nps;
-        const int64_t at = (((b * d.H + h) * d.nc + c) * d.nps + ps) * kTile + (16 * nt0 + li) * kSlice + 8 * g;
+        const int64_t at = (((b * d.H + h) * d.nc + c) * d.nps + ps) * kTile + each_at(nt0, g >> 1, li & 3) +
+                           16 * (li >> 2) + 8 * (g & 1);
 #pragma unroll
         for (int ks = 0; ks < 2; ks++)
 #pragma unroll
             for (int j = 0; j < NW; j++)
 #pragma unroll
                 for (int u = 0; u < 2; u++) {
-                    const int64_t e = at + 16 * j * kSlice + 32 * ks + 4 * u;
+                    const int64_t e = at + each_at(j, 2 * ks, 0) + 4 * u;
                     rS[ks][j][u] = *reinterpret_cast<const f32x4 *>(Sws + e);
                     if (sideB) rG[ks][j][u] = *reinterpret_cast<const f32x4 *>(Gws + e);
                 }
@@ -769,14 +776,15 @@ __global__ __launch_bounds__(2 * kThreads) TWO_WAVES void scan_grad_kernel(
         // dx^T: 16 columns (rows here) and half of the tokens
         {
             Frag gn[NF], yc[2];
-            const float *Gh = Gws + (((b * d.H + h) * d.nc + c) * d.nps + ps) * kTile + 16 * w + li;
+            const float *Gh = Gws + (((b * d.H + h) * d.nc + c) * d.nps + ps) * kTile +
+                              each_at(g >> 1, w, 0) + 32 * (g & 1) + li;
 #pragma unroll
             for (int kk = 0; kk < NF; kk++) {
                 if constexpr (kGs) {
                     gn[kk] = frag_col<T>(Gs[buf], LX, 32 * kk, 16 * w);
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 8; i++) gn[kk][i] = Gh[(32 * kk + 8 * g + i) * kSlice];
+                    for (int i = 0; i < 8; i++) gn[kk][i] = Gh[each_at(2 * kk, 0, i & 3) + 16 * (i >> 2)];
                 }
             }
 #pragma unroll
