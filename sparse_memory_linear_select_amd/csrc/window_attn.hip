@@ -7,6 +7,8 @@
 // over registers and two lane exchanges, and P^T is already the right operand
 // of O^T += V^T P^T.  One pass over the keys with the running maximum m and
 // sum l of 2^{s - m}, s in units of log2.
+#include <type_traits>
+
 #include "mix_internal.h"
 
 #include "lane_ops.h"
@@ -17,6 +19,7 @@ namespace {
 
 constexpr int kTile = 64;     // keys (or queries) of a tile in LDS
 constexpr int kThreads = 256; // of the kernels whose waves hold queries
+constexpr int kFewKeys = 64;  // fewer visible keys: delta from the keys
 constexpr int kKeys = 64;     // keys of a workgroup of the dK, dV kernel: 16 for each of four waves
 constexpr int kSinkRows = 512;  // queries whose sink gradients one workgroup sums
 
@@ -647,8 +650,16 @@ __device__ __forceinline__ float *sink_part(const SinkParts &p, const WinDims &d
 }
 
 // dQ^T += K^T dS^T over the keys, with P^T recomputed from lse and
-// dS = P (dP - delta) scale, dP^T = V dO^T, delta = sum_c dO o (also left in
-// the workspace for the other kernel).  Rows and tiles as in the forward.
+// dS = P (dP - delta) scale, dP^T = V dO^T, delta = sum_c dO o = sum_j P_j dP_j
+// (also left in the workspace for the other kernel).  Rows and tiles as in the
+// forward.  A bfloat16 o was rounded, which delta feels where few keys share a
+// row's weight: with n equal weights dS is off by 1 / sqrt(n - 1) of a rounding.
+// Queries that may see fewer than kFewKeys keys get delta from a walk of its own
+// over their keys, at most three tiles: delta + sum_j P_j (dP_j - delta)
+// (backward of 8 x 4096 tokens, 16 and 8 heads of 128, window 32, 4 sinks: 438 us
+// instead of 414).  Bound by HBM's latency and the tiles' together: 16 rows of
+// 4 waves, two workgroups a compute unit; 260 of the 480 us of a backward with
+// window 128, 230 with window 1.
 template <typename T, int DT, int QN, int HP, bool VEC, bool FEW>
 __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && DT <= 8 ? 2 : 1) void window_dq_kernel(
     WinDims d, SinkParts sp, const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v,
@@ -725,7 +736,6 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && DT <= 8 ? 2 : 1) void w
                 }
             }
             dl[u] = xor_add(xor_add(s, 16), 32);
-            if (live && g == 0) delta[ar] = dl[u];
             L[u] = lse[ar] * 1.4426950408889634f;
         }
         const bool few = FEW && kl.front > 0;
@@ -737,10 +747,9 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && DT <= 8 ? 2 : 1) void w
         rk.store(Ks);
         rv.store(Vs);
         __syncthreads();
-        if (few) {
-            const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-            f32x4 s[QN], dp[QN];
-            Frag sf[QN];
+        const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+        // P and dS (without the scale) of the sinks in front
+        const auto front = [&](f32x4 *s, f32x4 *dp) {
 #pragma unroll
             for (int u = 0; u < QN; u++) {
                 s[u] = dp[u] = zero;
@@ -752,10 +761,115 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && DT <= 8 ? 2 : 1) void w
 #pragma unroll
                 for (int e = 0; e < 4; e++) {
                     const float p = exp2_fast(fmaf(s[u][e], d.c2, -L[u]));
-                    const float ds = p * (dp[u][e] - dl[u]) * d.scale;
+                    const float ds = p * (dp[u][e] - dl[u]);
                     s[u][e] = 4 * g + e < kl.front ? p : 0.f;
                     dp[u][e] = 4 * g + e < kl.front ? ds : 0.f;
                 }
+            }
+        };
+        // One walk over the tiles, from the one in buffer `at` on: of dQ, or of eps, the
+        // rows' sums of P (dP - delta), which leaves the first tile in the next buffer.
+        f32x4 eps[QN];
+        int at = 0;
+        const auto walk = [&](auto sum) {
+            constexpr bool kSum = decltype(sum)::value;
+            for (int n = 0; n < nt; n++) {
+                const int buf = kBufs == 2 ? at : 0;
+                const T *Kt = Ks + buf * kTile * LD, *Vt = Vs + buf * kTile * LD;
+                fetch(n + 1 < nt ? n + 1 : kSum ? 0 : n);
+                const int v0 = n * kTile;
+#pragma unroll
+                for (int kp = 0; kp < 2; kp++) {
+                    int sight[QN][2];
+                    int any = 0;
+#pragma unroll
+                    for (int u = 0; u < QN; u++)
+#pragma unroll
+                        for (int e = 0; e < 2; e++) {
+                            sight[u][e] = HP == 2 && u ? sight[0][e]
+                                                       : block_sight(v0 + 32 * kp + 16 * e, kl.shift,
+                                                                     QR * w + (HP == 2 ? 0 : 16 * u), W, kl.always);
+                            any |= sight[u][e];
+                        }
+                    if (!any) continue;
+                    f32x4 s[QN][2], dp[QN][2];
+#pragma unroll
+                    for (int kt = 0; kt < 2; kt++) {
+#pragma unroll
+                        for (int u = 0; u < QN; u++) s[u][kt] = dp[u][kt] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int ks = 0; ks < DT / 2; ks++) {
+                            const auto ka = frag_row<T>(Kt, LD, 32 * kp + 16 * kt, 32 * ks);
+                            const auto va = frag_row<T>(Vt, LD, 32 * kp + 16 * kt, 32 * ks);
+#pragma unroll
+                            for (int u = 0; u < QN; u++) {
+                                s[u][kt] = M::mma(ka, qf[u][ks], s[u][kt]);
+                                dp[u][kt] = M::mma(va, gf[u][ks], dp[u][kt]);
+                            }
+                        }
+                    }
+                    Frag sf[QN];
+#pragma unroll
+                    for (int u = 0; u < QN; u++) {
+#pragma unroll
+                        for (int kt = 0; kt < 2; kt++) {
+#pragma unroll
+                            for (int e = 0; e < 4; e++) {
+                                const float p = exp2_fast(fmaf(s[u][kt][e], d.c2, -L[u]));
+                                dp[u][kt][e] = p * (dp[u][kt][e] - dl[u]);
+                                if (!kSum) dp[u][kt][e] *= d.scale;
+                            }
+                            if (sight[u][kt] != 2)
+#pragma unroll
+                                for (int e = 0; e < 4; e++) {
+                                    const int ve = v0 + 32 * kp + 16 * kt + 4 * g + e, jr = ve + kl.shift;
+                                    const bool see = (jr <= ir[u]) & ((ve < kl.always) | (jr > ir[u] - W));
+                                    dp[u][kt][e] = see & !alone[u] ? dp[u][kt][e] : 0.f;
+                                }
+                        }
+                        // dS is rounded to the inputs' type for the product with K
+                        if constexpr (kSum)
+                            eps[u] += dp[u][0] + dp[u][1];
+                        else
+                            sf[u] = frag_acc<T>(dp[u][0], dp[u][1]);
+                    }
+                    if constexpr (!kSum)
+#pragma unroll
+                        for (int j = 0; j < DT; j++) {
+                            const auto a = frag_col_pair<T>(Kt, LD, 32 * kp, 16 * j);
+#pragma unroll
+                            for (int u = 0; u < QN; u++) O[u][j] = M::mma(a, sf[u], O[u][j]);
+                        }
+                }
+                if (kBufs == 1) __syncthreads();
+                rk.store(Ks + (kBufs == 2 ? (buf ^ 1) * kTile * LD : 0));
+                rv.store(Vs + (kBufs == 2 ? (buf ^ 1) * kTile * LD : 0));
+                __syncthreads();
+                at ^= 1;
+            }
+        };
+        // (float32: o is as good as the sum)
+        const bool exact = sizeof(T) == 2 && (d.W + S < kFewKeys || t0 < kFewKeys);
+        if (exact) {
+            f32x4 s[QN], dp[QN];
+            if (few) front(s, dp);
+#pragma unroll
+            for (int u = 0; u < QN; u++) eps[u] = few ? dp[u] : zero;
+            walk(std::true_type{});
+#pragma unroll
+            for (int u = 0; u < QN; u++)
+                dl[u] += xor_add(xor_add((eps[u][0] + eps[u][1]) + (eps[u][2] + eps[u][3]), 16), 32);
+        }
+#pragma unroll
+        for (int u = 0; u < QN; u++)
+            if (t0 + ir[u] <= last && g == 0) delta[(b * d.T + t0 + ir[u]) * d.Hq + h0 + (HP == 2 ? u : 0)] = dl[u];
+        if (few) {
+            f32x4 s[QN], dp[QN];
+            front(s, dp);
+            Frag sf[QN];
+#pragma unroll
+            for (int u = 0; u < QN; u++) {
+                dp[u] *= d.scale;
                 sf[u] = frag_acc<T>(dp[u], zero);
             }
 #pragma unroll
@@ -774,74 +888,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && DT <= 8 ? 2 : 1) void w
                     Few[1][at] = (T)dp[u][e];
                 }
         }
-        for (int n = 0; n < nt; n++) {
-            const int buf = kBufs == 2 ? n & 1 : 0;
-            const T *Kt = Ks + buf * kTile * LD, *Vt = Vs + buf * kTile * LD;
-            fetch(n + 1 < nt ? n + 1 : n);
-            const int v0 = n * kTile;
-#pragma unroll
-            for (int kp = 0; kp < 2; kp++) {
-                int sight[QN][2];
-                int any = 0;
-#pragma unroll
-                for (int u = 0; u < QN; u++)
-#pragma unroll
-                    for (int e = 0; e < 2; e++) {
-                        sight[u][e] = HP == 2 && u ? sight[0][e]
-                                                   : block_sight(v0 + 32 * kp + 16 * e, kl.shift,
-                                                                 QR * w + (HP == 2 ? 0 : 16 * u), W, kl.always);
-                        any |= sight[u][e];
-                    }
-                if (!any) continue;
-                f32x4 s[QN][2], dp[QN][2];
-#pragma unroll
-                for (int kt = 0; kt < 2; kt++) {
-#pragma unroll
-                    for (int u = 0; u < QN; u++) s[u][kt] = dp[u][kt] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int ks = 0; ks < DT / 2; ks++) {
-                        const auto ka = frag_row<T>(Kt, LD, 32 * kp + 16 * kt, 32 * ks);
-                        const auto va = frag_row<T>(Vt, LD, 32 * kp + 16 * kt, 32 * ks);
-#pragma unroll
-                        for (int u = 0; u < QN; u++) {
-                            s[u][kt] = M::mma(ka, qf[u][ks], s[u][kt]);
-                            dp[u][kt] = M::mma(va, gf[u][ks], dp[u][kt]);
-                        }
-                    }
-                }
-                Frag sf[QN];
-#pragma unroll
-                for (int u = 0; u < QN; u++) {
-#pragma unroll
-                    for (int kt = 0; kt < 2; kt++) {
-#pragma unroll
-                        for (int e = 0; e < 4; e++) {
-                            const float p = exp2_fast(fmaf(s[u][kt][e], d.c2, -L[u]));
-                            dp[u][kt][e] = p * (dp[u][kt][e] - dl[u]) * d.scale;
-                        }
-                        if (sight[u][kt] != 2)
-#pragma unroll
-                            for (int e = 0; e < 4; e++) {
-                                const int ve = v0 + 32 * kp + 16 * kt + 4 * g + e, jr = ve + kl.shift;
-                                const bool see = (jr <= ir[u]) & ((ve < kl.always) | (jr > ir[u] - W));
-                                dp[u][kt][e] = see & !alone[u] ? dp[u][kt][e] : 0.f;
-                            }
-                    }
-                    // dS is rounded to the inputs' type for the product with K
-                    sf[u] = frag_acc<T>(dp[u][0], dp[u][1]);
-                }
-#pragma unroll
-                for (int j = 0; j < DT; j++) {
-                    const auto a = frag_col_pair<T>(Kt, LD, 32 * kp, 16 * j);
-#pragma unroll
-                    for (int u = 0; u < QN; u++) O[u][j] = M::mma(a, sf[u], O[u][j]);
-                }
-            }
-            if (kBufs == 1) __syncthreads();
-            rk.store(Ks + (kBufs == 2 ? (buf ^ 1) * kTile * LD : 0));
-            rv.store(Vs + (kBufs == 2 ? (buf ^ 1) * kTile * LD : 0));
-            __syncthreads();
-        }
+        walk(std::false_type{});
         if constexpr (FEW) {
             if (few) {   // dK, dV of the sinks in front over the workgroup's rows
 #pragma unroll

@@ -139,6 +139,24 @@ def test_one_visible_key_has_no_score_gradient(dt):
         assert float(((out["dv"].float() - both).abs() / (1 + both.abs())).max()) <= float(lim)
 
 
+@pytest.mark.parametrize("T,D,W,S", [(34, 64, 1235, 4), (300, 64, 2, 0), (300, 64, 3, 1), (300, 128, 8, 4),
+                                     (300, 64, 40, 20), (500, 256, 20, 4)])
+def test_few_visible_keys_lose_no_precision(T, D, W, S):
+    """bfloat16 dq and dk carry two roundings, dS's for the products and their own, which
+    add up in squares: sqrt(2) = 1.41 times the error of rounding the exact result (and
+    dv, with its weights' rounding, too).  The rounding of o would be a third one, above 2
+    times at two visible keys; 1.55 leaves 10% for the scatter of sums over 10^4 elements."""
+    q, k, v, do = (normal(gen(11 + n), 2, T, h, D, dtype=torch.bfloat16) for n, h in enumerate((4, 2, 2, 4)))
+    att = sdm.WindowAttention(4, 2, D, W, S)
+    o, lse = att.forward(q, k, v)
+    out = att.backward(q, k, v, o, lse, do)
+    x = [leaf(cpu(t)) for t in (q, k, v)]
+    (definition(*x, W, S, None, D ** -0.5)[0] * cpu(do)).sum().backward()
+    for n, t in zip("qkv", x):
+        one = (t.grad.bfloat16().double() - t.grad).norm()
+        assert float((cpu(out["d" + n]) - t.grad).norm() / one) <= 1.55, n
+
+
 def test_gradient_against_differences():
     q, k, v, _ = inputs(5, 1, 70, 2, 1, 8, "f32", None)
     do = normal(gen(6), 1, 70, 2, 8)
