@@ -196,9 +196,14 @@ __device__ __forceinline__ float pair_max(float x, int m)
 // heads, or 64 QN queries of one, and two workgroups share a compute unit.  (One
 // block a wave, eight waves a workgroup, reads LDS twice as often and runs no
 // more waves: 200 us instead of 165 for 8 x 4096 tokens, 16 and 8 heads of 128,
-// window 128.)  The next tile of keys is loaded while one is worked on.
+// window 128.)  The next tile of keys is loaded while one is worked on; bfloat16
+// tiles go to a second buffer, float32 ones (35 KB) leave the LDS to a second
+// workgroup instead (3 x 1333 tokens, 6 and 2 heads of 72, window 301: 66 us
+// instead of 83).  Bound by the latency between HBM and the tiles: 133 us for the
+// bfloat16 shape above, 3.0 TB/s (window 1: 98); long windows by the matrix
+// products (window 1000: 397 us).
 template <typename T, int DT, int QN, int HP, bool VEC, bool CACHE>
-__global__ __launch_bounds__(kThreads, sizeof(T) == 2 && DT <= 8 ? 2 : 1) void window_fwd_kernel(
+__global__ __launch_bounds__(kThreads, DT <= 8 ? 2 : 1) void window_fwd_kernel(
     WinDims d, const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v,
     const T *__restrict__ ck, const T *__restrict__ cv, const int64_t *__restrict__ pos,
     const int32_t *__restrict__ lengths, T *__restrict__ o, float *__restrict__ lse)
@@ -207,7 +212,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && DT <= 8 ? 2 : 1) void w
     using Half = typename M::Half;
     constexpr int LD = DT * 16 + 8;
     constexpr int QR = HP == 2 ? 16 : 16 * QN;   // queries of a wave
-    constexpr int kBufs = sizeof(T) == 2 || DT <= 8 ? 2 : 1;
+    constexpr int kBufs = sizeof(T) == 2 ? 2 : 1;
     __shared__ __align__(32) T Ks[kBufs][kTile * LD];
     __shared__ __align__(32) T Vs[kBufs][kTile * LD];
     // float32 tiles leave no room for the sinks' beside a second workgroup
@@ -428,7 +433,8 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && DT <= 8 ? 2 : 1) void w
 // heads of the workgroup, and keeps the running softmax of its rows.  Bound by
 // the cache's bytes, or for short windows by latency: all loads of a step are
 // issued before any is used, and there is one launch (with `splits`, which
-// share the rows of a long cache among workgroups, and a joining one).
+// share the rows of a long cache among workgroups, and a joining one).  32
+// streams, 16 and 8 heads of 128, window 128, bfloat16: 8 us.
 constexpr int kStepWaves = 8;
 
 template <typename T, int LK, int R, bool VEC>
@@ -657,9 +663,8 @@ __device__ __forceinline__ float *sink_part(const SinkParts &p, const WinDims &d
 // Queries that may see fewer than kFewKeys keys get delta from a walk of its own
 // over their keys, at most three tiles: delta + sum_j P_j (dP_j - delta)
 // (backward of 8 x 4096 tokens, 16 and 8 heads of 128, window 32, 4 sinks: 438 us
-// instead of 414).  Bound by HBM's latency and the tiles' together: 16 rows of
-// 4 waves, two workgroups a compute unit; 260 of the 480 us of a backward with
-// window 128, 230 with window 1.
+// instead of 414).  Bound, like the forward, by the latency between HBM and the
+// tiles: 269 us with window 128, 670 MB.
 template <typename T, int DT, int QN, int HP, bool VEC, bool FEW>
 __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && DT <= 8 ? 2 : 1) void window_dq_kernel(
     WinDims d, SinkParts sp, const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v,
@@ -672,7 +677,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && DT <= 8 ? 2 : 1) void w
     constexpr int QR = HP == 2 ? 16 : 16 * QN;    // queries of a wave
     constexpr int kRows = 64 * QN;                // rows of the workgroup
     constexpr int LS = kRows + 8;
-    constexpr int kBufs = sizeof(T) == 2 || DT <= 8 ? 2 : 1;
+    constexpr int kBufs = sizeof(T) == 2 ? 2 : 1;
     __shared__ __align__(32) T Ks[kBufs * kTile * LD];  // at the end (FEW) the rows of Q and dO
     __shared__ __align__(32) T Vs[kBufs * kTile * LD];
     // the sinks' K and V, then their P and dS: [key][row]
@@ -933,7 +938,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 && DT <= 8 ? 2 : 1) void w
 // lane holds one key (column) and four neighbouring queries (rows).  Two
 // workgroups share a compute unit; 128 keys and eight waves in one load fewer
 // tiles but start and end together (backward of 8 x 4096 tokens, 16 and 8 heads
-// of 128, window 128: 540 us instead of 507).  SINKS:
+// of 128, window 128: 540 us instead of 507; this kernel 237 us, 540 MB).  SINKS:
 // the sinks alone, for the queries behind part 0, 512 a workgroup, into parts 1 ..
 template <typename T, int DT, bool VEC, bool SINKS>
 __global__ __launch_bounds__(kThreads, sizeof(T) * DT <= 16 ? 2 : 1) void window_dkv_kernel(
